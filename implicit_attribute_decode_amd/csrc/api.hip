@@ -1006,3 +1006,259 @@ ia_status ia_densify(const float* xyzt, const float* grad_acc, const int32_t* gr
 }
 
 }  // extern "C"
+
+// ============================================================== clipping
+
+namespace {
+
+size_t dtype_size(int32_t dtype) {
+    return dtype == IA_DTYPE_F32 ? 4 : (dtype == IA_DTYPE_F16 || dtype == IA_DTYPE_BF16 ? 2 : 0);
+}
+
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+// rows x dim is within [0, 2^40] (dim >= 1)
+bool size_ok(int64_t rows, int64_t dim) { return rows >= 0 && dim >= 1 && rows <= kMaxElements / dim; }
+
+// Byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+// Bytes from the first to the last element of rows of `cols` elements `ld` apart.
+size_t extent(int64_t rows, int64_t cols, int64_t ld, size_t es) {
+    return rows == 0 || cols == 0 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * es;
+}
+
+ia_status check_clip(int32_t count, float max_norm, const void* ws, size_t ws_bytes, const float* stats) {
+    if (count < 0) return fail(IA_ERR_INVALID_ARG, "count must be >= 0");
+    if (!(max_norm >= 0.0f)) return fail(IA_ERR_INVALID_ARG, "max_norm must be >= 0");
+    if (!stats || !aligned(stats, 4)) return fail(IA_ERR_INVALID_ARG, "stats is null or misaligned");
+    return check_ws(ws, ws_bytes, ia::clip_workspace(count));
+}
+
+ia_status check_grads(const ia_grad* grads, int32_t count, bool outputs) {
+    if (count > 0 && !grads) return fail(IA_ERR_INVALID_ARG, "grads is null");
+    int64_t total = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        const ia_grad& g = grads[k];
+        const size_t es = dtype_size(g.dtype);
+        if (es == 0) return fail(IA_ERR_UNSUPPORTED, "gradients are F32, F16 or BF16");
+        if (!size_ok(g.rows, g.dim) || (total += g.rows * g.dim) > kMaxElements)
+            return fail(IA_ERR_INVALID_ARG, "need rows >= 0, dim >= 1 and at most 2^40 elements");
+        if (g.stride < g.dim || (g.out && g.out_stride < g.dim))
+            return fail(IA_ERR_INVALID_ARG, "a stride is below dim");
+        if (g.rows == 0) continue;
+        if (!g.data || !aligned(g.data, es) || !aligned(g.out, es))
+            return fail(IA_ERR_INVALID_ARG, "a gradient is null or misaligned");
+        if (outputs && g.out && !(g.out == g.data && g.out_stride == g.stride) &&
+            overlap(g.data, extent(g.rows, g.dim, g.stride, es), g.out, extent(g.rows, g.dim, g.out_stride, es)))
+            return fail(IA_ERR_INVALID_ARG, "out overlaps data");
+    }
+    return IA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ia_status ia_clip_workspace_size(int32_t count, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    if (count < 0) return fail(IA_ERR_INVALID_ARG, "count must be >= 0");
+    *bytes = ia::clip_workspace(count);
+    return IA_OK;
+}
+
+ia_status ia_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes, float* stats,
+                       void* stream) {
+    ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
+    if (st == IA_OK) st = check_grads(grads, count, false);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_grad_norm(grads, count, max_norm, ws, stats, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "gradient norm launch");
+    return IA_OK;
+}
+
+ia_status ia_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes,
+                            float* stats, void* stream) {
+    ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
+    if (st == IA_OK) st = check_grads(grads, count, true);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_clip_grad_norm(grads, count, max_norm, ws, stats, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "gradient clipping launch");
+    return IA_OK;
+}
+
+ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
+                            float eps, int32_t step, void* ws, size_t ws_bytes, float* stats, void* stream) {
+    ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
+    if (st != IA_OK) return st;
+    if (count > 0 && !groups) return fail(IA_ERR_INVALID_ARG, "groups is null");
+    if (step < 1) return fail(IA_ERR_INVALID_ARG, "step must be >= 1");
+    if (!(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f))
+        return fail(IA_ERR_INVALID_ARG, "betas must be in [0, 1)");
+    if (!(eps >= 0.0f)) return fail(IA_ERR_INVALID_ARG, "eps must be >= 0");
+    int64_t total = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        const ia_adam_group& g = groups[k];
+        if (!(g.lr >= 0.0f)) return fail(IA_ERR_INVALID_ARG, "lr must be >= 0");
+        if (!size_ok(g.rows, g.dim) || g.param_stride < g.dim || (total += g.rows * g.dim) > kMaxElements)
+            return fail(IA_ERR_INVALID_ARG, "need rows >= 0, 1 <= dim <= param_stride and at most 2^40 elements");
+        if (g.rows == 0) continue;
+        if (!g.param || !g.grad || !g.m || !g.v) return fail(IA_ERR_INVALID_ARG, "null argument");
+        if (!aligned(g.param, 4) || !aligned(g.grad, 4) || !aligned(g.m, 4) || !aligned(g.v, 4) ||
+            !aligned(g.param_f16, 2))
+            return fail(IA_ERR_INVALID_ARG, "a group's array is misaligned");
+    }
+    hipError_t e = ia::launch_adam_clip(groups, count, max_norm, beta1, beta2, eps, step, ws, stats,
+                                        (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "clipped adam launch");
+    return IA_OK;
+}
+
+}  // extern "C"
+
+// ============================================================== MXFP4
+
+namespace {
+
+constexpr int64_t kMaxMatmulDim = (int64_t(1) << 31) - 1;
+
+ia_status check_mx4(const ia_mx4* q, const char* name) {
+    if (!q) return fail(IA_ERR_INVALID_ARG, std::string(name) + " is null");
+    if (q->rows < 0 || q->cols < 0 || (q->cols > 0 && !size_ok(q->rows, q->cols)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": sizes must be >= 0 with at most 2^40 values");
+    if (q->rows > 0 && q->cols > 0 && (!q->codes || !q->scales || !aligned(q->codes, 16)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": null scales, or codes not 16-byte aligned");
+    return IA_OK;
+}
+
+// A dense-row matrix argument; ld = 0 (one row repeated) only for inputs.
+ia_status check_matrix(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, bool input,
+                       const char* name) {
+    const size_t es = dtype_size(dtype);
+    if (es == 0) return fail(IA_ERR_UNSUPPORTED, "dtype must be F32, F16 or BF16");
+    if (rows < 0 || cols < 0 || (cols > 0 && !size_ok(rows, cols)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": sizes must be >= 0 with at most 2^40 values");
+    if (rows == 0 || cols == 0) return IA_OK;
+    if (ld < cols && !(input && ld == 0))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": the row stride is below the number of columns");
+    if (ld > kMaxElements / rows) return fail(IA_ERR_INVALID_ARG, std::string(name) + ": row stride too large");
+    if (!x || !aligned(x, es)) return fail(IA_ERR_INVALID_ARG, std::string(name) + " is null or misaligned");
+    return IA_OK;
+}
+
+ia_status check_product(int64_t M, int64_t N, int64_t K, int32_t act, const float* bias) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxMatmulDim || N > kMaxMatmulDim || K > kMaxMatmulDim)
+        return fail(IA_ERR_INVALID_ARG, "M, N and K must be in [0, 2^31)");
+    if (act != IA_ACT_NONE && act != IA_ACT_RELU) return fail(IA_ERR_UNSUPPORTED, "act must be NONE or RELU");
+    if (!aligned(bias, 4)) return fail(IA_ERR_INVALID_ARG, "bias is misaligned");
+    return IA_OK;
+}
+
+ia::Mx4View view(const ia_mx4& q) { return ia::Mx4View{q.codes, q.scales, q.rows, q.cols}; }
+
+}  // namespace
+
+extern "C" {
+
+ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, int32_t transpose,
+                          const ia_mx4* out, void* stream) {
+    ia_status st = check_matrix(x, dtype, rows, cols, ld, true, "x");
+    if (st == IA_OK) st = check_mx4(out, "out");
+    if (st != IA_OK) return st;
+    if (out->rows != (transpose ? cols : rows) || out->cols != (transpose ? rows : cols))
+        return fail(IA_ERR_INVALID_ARG, "out has another shape");
+    hipError_t e = ia::launch_mx4_quantize(ia::Mx4Source{x, nullptr, rows, cols, ld, 0, dtype}, transpose != 0,
+                                           view(*out), (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mx4 quantize launch");
+    return IA_OK;
+}
+
+ia_status ia_mx4_dequantize(const ia_mx4* q, int32_t dtype, void* x, int64_t ld, void* stream) {
+    ia_status st = check_mx4(q, "q");
+    if (st == IA_OK) st = check_matrix(x, dtype, q->rows, q->cols, ld, false, "x");
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_mx4_dequantize(view(*q), dtype, x, ld, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mx4 dequantize launch");
+    return IA_OK;
+}
+
+ia_status ia_mx4_matmul_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    ia_status st = check_product(M, N, K, IA_ACT_NONE, nullptr);
+    if (st != IA_OK) return st;
+    *bytes = ia::mx4_matmul_workspace(M, N, K);
+    return IA_OK;
+}
+
+ia_status ia_mx4_matmul(const ia_mx4* a, const ia_mx4* b, const float* bias, int32_t act, int32_t dtype, void* c,
+                        int64_t ldc, void* ws, size_t ws_bytes, void* stream) {
+    ia_status st = check_mx4(a, "a");
+    if (st == IA_OK) st = check_mx4(b, "b");
+    if (st != IA_OK) return st;
+    if (a->cols != b->cols) return fail(IA_ERR_INVALID_ARG, "a and b have different numbers of columns");
+    st = check_product(a->rows, b->rows, a->cols, act, bias);
+    if (st == IA_OK) st = check_matrix(c, dtype, a->rows, b->rows, ldc, false, "c");
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_matmul_workspace(a->rows, b->rows, a->cols));
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_mx4_matmul(view(*a), view(*b), bias, act, dtype, c, ldc, ws, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mx4 matmul launch");
+    return IA_OK;
+}
+
+ia_status ia_mx4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    ia_status st = check_product(M, N, K, IA_ACT_NONE, nullptr);
+    if (st != IA_OK) return st;
+    *bytes = ia::mx4_linear_workspace(M, K, N);
+    return IA_OK;
+}
+
+ia_status ia_mx4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const ia_mx4* w, const float* bias,
+                        int32_t act, void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    ia_status st = check_mx4(w, "w");
+    if (st != IA_OK) return st;
+    st = check_product(M, w->rows, w->cols, act, bias);
+    if (st == IA_OK) st = check_matrix(x, dtype, M, w->cols, ldx, true, "x");
+    if (st == IA_OK) st = check_matrix(y, dtype, M, w->rows, ldy, false, "y");
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_linear_workspace(M, w->cols, w->rows));
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_mx4_linear(ia::Mx4Source{x, nullptr, M, w->cols, ldx, 0, dtype}, view(*w), bias, act, y,
+                                         ldy, ws, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mx4 linear launch");
+    return IA_OK;
+}
+
+ia_status ia_mx4_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    ia_status st = check_product(M, N, K, IA_ACT_NONE, nullptr);
+    if (st != IA_OK) return st;
+    *bytes = ia::mx4_linear_backward_workspace(M, N, K);
+    return IA_OK;
+}
+
+ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void* y, int64_t ldy, const void* x, int64_t ldx,
+                                 int32_t dtype, int64_t M, int64_t N, int64_t K, const ia_mx4* wt, void* dx,
+                                 int64_t lddx, float* dw, float* db, void* ws, size_t ws_bytes, void* stream) {
+    ia_status st = check_product(M, N, K, IA_ACT_NONE, db);
+    if (st == IA_OK) st = check_matrix(dy, dtype, M, N, lddy, true, "dy");
+    if (st == IA_OK && y) st = check_matrix(y, dtype, M, N, ldy, true, "y");
+    if (st == IA_OK && dw) st = check_matrix(x, dtype, M, K, ldx, true, "x");
+    if (st == IA_OK && dw) st = check_matrix(dw, IA_DTYPE_F32, N, K, K, false, "dw");
+    if (st == IA_OK && dx) {
+        st = check_mx4(wt, "wt");
+        if (st == IA_OK && (wt->rows != K || wt->cols != N)) st = fail(IA_ERR_INVALID_ARG, "wt must be [K][N]");
+        if (st == IA_OK) st = check_matrix(dx, dtype, M, K, lddx, false, "dx");
+    }
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_linear_backward_workspace(M, N, K));
+    if (st != IA_OK) return st;
+    const ia::Mx4Source d{dy, y, M, N, lddy, ldy, dtype}, xs{x, nullptr, M, K, ldx, 0, dtype};
+    hipError_t e = ia::launch_mx4_linear_backward(d, xs, dx ? view(*wt) : ia::Mx4View{}, dx, lddx, dw, db, ws,
+                                                  (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "mx4 linear backward launch");
+    return IA_OK;
+}
+
+}  // extern "C"

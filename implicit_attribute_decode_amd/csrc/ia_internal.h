@@ -316,4 +316,52 @@ size_t radix_sort_counts_bytes(int max_blocks);
 hipError_t launch_adam(float* p, const float* g, float* m, float* v, int64_t n, int32_t dim, int32_t stride,
                        float lr, float beta1, float beta2, float eps, int32_t step, uint16_t* p16, hipStream_t s);
 
+// ---------------------------------------------------------------- clipping
+
+// Gradient norm, clipping and the clipped Adam step over many tensors
+// (clip.hip); stats: device float[3] {norm, factor, finite}.
+size_t clip_workspace(int32_t tensors);
+hipError_t launch_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, float* stats,
+                            hipStream_t s);
+hipError_t launch_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, float* stats,
+                                 hipStream_t s);
+hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
+                            float eps, int32_t step, void* ws, float* stats, hipStream_t s);
+
+// ---------------------------------------------------------------- MXFP4
+
+constexpr int32_t kMx4NoAct = IA_ACT_NONE;
+
+// A matrix to quantise (mx4.hip): x [rows][cols] of dtype, rows ldx apart; with
+// y (the same shape and dtype, rows ldy apart) x counts as zero where y <= 0.
+struct Mx4Source {
+    const void* x;
+    const void* y;
+    int64_t rows, cols, ldx, ldy;
+    int32_t dtype;
+};
+
+// codes [rows][mx4_blocks(cols)][16], scales [rows][mx4_blocks(cols)]
+struct Mx4View {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows, cols;
+};
+
+int64_t mx4_blocks(int64_t cols);
+// transpose: out.rows = x.cols, blocks along x's columns
+hipError_t launch_mx4_quantize(const Mx4Source& x, bool transpose, const Mx4View& out, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s);
+// c[a.rows][ldc] of dtype = act(a b^T + bias)
+size_t mx4_matmul_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx4_matmul(const Mx4View& a, const Mx4View& b, const float* bias, int32_t act, int32_t dtype, void* c,
+                             int64_t ldc, void* ws, hipStream_t s);
+size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N);
+hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
+                             int64_t ldy, void* ws, hipStream_t s);
+// dx, dw, db: null skips that gradient; wt: [K][N], needed for dx
+size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
+                                      float* dw, float* db, void* ws, hipStream_t s);
+
 }  // namespace ia

@@ -25,6 +25,7 @@
 //   - lambda (blur(dS/dmu_x) + 2 x blur(dS/dE[x^2]) + y blur(dS/dE[xy])) / n.
 #include <hip/hip_runtime.h>
 
+#include "adam_common.h"
 #include "ia_internal.h"
 
 namespace ia {
@@ -253,26 +254,21 @@ __global__ void __launch_bounds__(kFinish) loss_finish_kernel(const double2* par
     }
 }
 
-// p -= step_size * m / (sqrt(v * v_scale) + eps) after the moment updates;
-// step_size = lr / (1 - b1^t), v_scale = 1 / (1 - b2^t) (host, double).
-// g, m, v are dense [n]; with STRIDED the parameter is rows of `dim` values
+// One Adam step (adam_common.h); g, m, v are dense [n]; with STRIDED the parameter is rows of `dim` values
 // `stride` floats apart (element i at (i / dim) * stride + i % dim).
 template <bool STRIDED>
 __global__ void __launch_bounds__(256) adam_kernel(float* p, const float* g, float* m, float* v, int64_t n, int dim,
-                                                   int stride, float b1, float b2, float eps, float step_size,
-                                                   float v_scale, uint16_t* p16) {
+                                                   int stride, AdamConsts c, float step_size, uint16_t* p16) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         int64_t j = i;
         if constexpr (STRIDED) {
             const int64_t row = i / dim;
             j = row * stride + (i - row * dim);
         }
-        const float gi = g[i];
-        const float mi = b1 * m[i] + (1.0f - b1) * gi;
-        const float vi = b2 * v[i] + (1.0f - b2) * (gi * gi);
+        float mi = m[i], vi = v[i];
+        const float pi = adam_element(p[j], g[i], mi, vi, c, step_size);
         m[i] = mi;
         v[i] = vi;
-        const float pi = p[j] - step_size * mi / (sqrtf(vi * v_scale) + eps);
         p[j] = pi;
         if (p16) p16[i] = __builtin_bit_cast(uint16_t, (_Float16)pi);
     }
@@ -308,14 +304,15 @@ hipError_t launch_adam(float* p, const float* g, float* m, float* v, int64_t n, 
     if (n <= 0) return hipSuccess;
     const double step_size = (double)lr / (1.0 - pow((double)beta1, (double)step));
     const double v_scale = 1.0 / (1.0 - pow((double)beta2, (double)step));
+    const AdamConsts c{beta1, beta2, eps, (float)v_scale};
     int64_t blocks = (n + 255) / 256;
     if (blocks > 8192) blocks = 8192;
     if (dim == stride)
         IA_LAUNCH("adam_kernel", adam_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, p, g, m, v, n, dim,
-                  stride, beta1, beta2, eps, (float)step_size, (float)v_scale, p16);
+                  stride, c, (float)step_size, p16);
     else
         IA_LAUNCH("adam_kernel", adam_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, p, g, m, v, n, dim,
-                  stride, beta1, beta2, eps, (float)step_size, (float)v_scale, p16);
+                  stride, c, (float)step_size, p16);
     return hipGetLastError();
 }
 

@@ -21,8 +21,8 @@ IA_ERR_UNSUPPORTED = -2
 IA_ERR_WORKSPACE_TOO_SMALL = -3
 IA_ERR_DEVICE = -4
 IA_ERR_OUT_OF_MEMORY = -5
-IA_DTYPE_F32, IA_DTYPE_F16 = 0, 1
-IA_ACT_RELU, IA_ACT_GELU = 0, 1
+IA_DTYPE_F32, IA_DTYPE_F16, IA_DTYPE_BF16 = 0, 1, 2
+IA_ACT_NONE, IA_ACT_RELU, IA_ACT_GELU = -1, 0, 1
 IA_COLOR_RGB, IA_COLOR_SH3 = 0, 1
 IA_BRANCHES_SHARED, IA_BRANCHES_PER_ATTRIBUTE = 0, 1
 # ia_render_aux.binning
@@ -37,6 +37,10 @@ EXPORTS = ("ia_last_error", "ia_decoder_create", "ia_decoder_set_params", "ia_de
            "ia_render_workspace_size", "ia_render", "ia_render_backward", "ia_l1_loss",
            "ia_image_loss_workspace_size", "ia_image_loss", "ia_adam_step", "ia_adam_step_strided",
            "ia_densify_accumulate", "ia_densify_workspace_size", "ia_densify",
+           "ia_clip_workspace_size", "ia_grad_norm", "ia_clip_grad_norm", "ia_adam_clip_step",
+           "ia_mx4_quantize", "ia_mx4_dequantize", "ia_mx4_matmul_workspace_size", "ia_mx4_matmul",
+           "ia_mx4_linear_workspace_size", "ia_mx4_linear", "ia_mx4_linear_backward_workspace_size",
+           "ia_mx4_linear_backward",
            "ia_profile_enable", "ia_profile_report", "ia_profile_reset")
 
 
@@ -90,6 +94,21 @@ class GaussianGrads(C.Structure):
                 ("colors", C.c_void_p), ("sh", C.c_void_p)]
 
 
+class Grad(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("out", C.c_void_p), ("rows", C.c_int64), ("dim", C.c_int32),
+                ("stride", C.c_int32), ("out_stride", C.c_int32), ("dtype", C.c_int32)]
+
+
+class AdamGroup(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("param_f16", C.c_void_p), ("rows", C.c_int64), ("dim", C.c_int32), ("param_stride", C.c_int32),
+                ("lr", C.c_float)]
+
+
+class Mx4(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64)]
+
+
 _lib = None
 P = C.c_void_p
 
@@ -139,6 +158,21 @@ def load(path: str = LIB_PATH):
         L.ia_densify_accumulate.argtypes = [P, C.c_int64, P, P, P]
         L.ia_densify_workspace_size.argtypes = [C.c_int64, P]
         L.ia_densify.argtypes = [P, P, P, P, P, P, P, P, P, C.c_int64, P, P, P, P, C.c_int64, P, P, C.c_size_t, P]
+        L.ia_clip_workspace_size.argtypes = [C.c_int32, P]
+        L.ia_grad_norm.argtypes = [P, C.c_int32, C.c_float, P, C.c_size_t, P, P]
+        L.ia_clip_grad_norm.argtypes = [P, C.c_int32, C.c_float, P, C.c_size_t, P, P]
+        L.ia_adam_clip_step.argtypes = [P, C.c_int32, C.c_float, C.c_float, C.c_float, C.c_float, C.c_int32, P,
+                                        C.c_size_t, P, P]
+        L.ia_mx4_quantize.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32, P, P]
+        L.ia_mx4_dequantize.argtypes = [P, C.c_int32, P, C.c_int64, P]
+        L.ia_mx4_matmul_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_mx4_matmul.argtypes = [P, P, P, C.c_int32, C.c_int32, P, C.c_int64, P, C.c_size_t, P]
+        L.ia_mx4_linear_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_mx4_linear.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, P, P, C.c_int32, P, C.c_int64, P, C.c_size_t,
+                                    P]
+        L.ia_mx4_linear_backward_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_mx4_linear_backward.argtypes = [P, C.c_int64, P, C.c_int64, P, C.c_int64, C.c_int32, C.c_int64, C.c_int64,
+                                             C.c_int64, P, P, C.c_int64, P, P, P, C.c_size_t, P]
         L.ia_profile_enable.argtypes = [C.c_int32]
         L.ia_profile_report.argtypes = [P, C.c_size_t, P]
         L.ia_profile_reset.argtypes = []
@@ -410,6 +444,84 @@ def ia_densify(xyzt, grad_acc, grad_count, scales, quats, opacity, noise, m, v, 
                              _ptr(opacity), _ptr(noise), _ptr(m), _ptr(v), int(xyzt.shape[0]), C.byref(params),
                              _ptr(out_xyzt), _ptr(out_m), _ptr(out_v), int(out_xyzt.shape[0]), _ptr(out_n),
                              _ptr(ws), 0 if ws is None else int(ws.numel() * ws.element_size()), _stream(stream)))
+
+
+# ----------------------------------------------------------------- clipping
+
+
+def ia_clip_workspace_size(count: int) -> int:
+    n = C.c_size_t()
+    _check(load().ia_clip_workspace_size(int(count), C.byref(n)))
+    return int(n.value)
+
+
+def ia_grad_norm(grads, max_norm: float, ws, stats, stream=None):
+    """grads: a ctypes array of Grad; stats: device float32 [3]."""
+    _check(load().ia_grad_norm(grads, len(grads), float(max_norm), _ptr(ws), _nbytes(ws), _ptr(stats),
+                               _stream(stream)))
+
+
+def ia_clip_grad_norm(grads, max_norm: float, ws, stats, stream=None):
+    _check(load().ia_clip_grad_norm(grads, len(grads), float(max_norm), _ptr(ws), _nbytes(ws), _ptr(stats),
+                                    _stream(stream)))
+
+
+def ia_adam_clip_step(groups, max_norm: float, beta1: float, beta2: float, eps: float, step: int, ws, stats,
+                      stream=None):
+    """groups: a ctypes array of AdamGroup; stats: device float32 [3]."""
+    _check(load().ia_adam_clip_step(groups, len(groups), float(max_norm), float(beta1), float(beta2), float(eps),
+                                    int(step), _ptr(ws), _nbytes(ws), _ptr(stats), _stream(stream)))
+
+
+# ----------------------------------------------------------------- MXFP4
+
+
+def mx4(codes, scales, rows: int, cols: int) -> Mx4:
+    return Mx4(_ptr(codes), _ptr(scales), rows, cols)
+
+
+def ia_mx4_quantize(x, dtype: int, rows: int, cols: int, ld: int, transpose: bool, out: Mx4, stream=None):
+    _check(load().ia_mx4_quantize(_ptr(x), dtype, rows, cols, ld, 1 if transpose else 0, C.byref(out),
+                                  _stream(stream)))
+
+
+def ia_mx4_dequantize(q: Mx4, dtype: int, x, ld: int, stream=None):
+    _check(load().ia_mx4_dequantize(C.byref(q), dtype, _ptr(x), ld, _stream(stream)))
+
+
+def ia_mx4_matmul_workspace_size(M: int, N: int, K: int) -> int:
+    n = C.c_size_t()
+    _check(load().ia_mx4_matmul_workspace_size(M, N, K, C.byref(n)))
+    return n.value
+
+
+def ia_mx4_matmul(a: Mx4, b: Mx4, bias, act: int, dtype: int, c, ldc: int, ws=None, stream=None):
+    _check(load().ia_mx4_matmul(C.byref(a), C.byref(b), _ptr(bias), act, dtype, _ptr(c), ldc, _ptr(ws), _nbytes(ws),
+                                _stream(stream)))
+
+
+def ia_mx4_linear_workspace_size(M: int, K: int, N: int) -> int:
+    n = C.c_size_t()
+    _check(load().ia_mx4_linear_workspace_size(M, K, N, C.byref(n)))
+    return n.value
+
+
+def ia_mx4_linear(x, dtype: int, M: int, ldx: int, w: Mx4, bias, act: int, y, ldy: int, ws=None, stream=None):
+    _check(load().ia_mx4_linear(_ptr(x), dtype, M, ldx, C.byref(w), _ptr(bias), act, _ptr(y), ldy, _ptr(ws),
+                                _nbytes(ws), _stream(stream)))
+
+
+def ia_mx4_linear_backward_workspace_size(M: int, N: int, K: int) -> int:
+    n = C.c_size_t()
+    _check(load().ia_mx4_linear_backward_workspace_size(M, N, K, C.byref(n)))
+    return n.value
+
+
+def ia_mx4_linear_backward(dy, lddy: int, y, ldy: int, x, ldx: int, dtype: int, M: int, N: int, K: int,
+                           wt: Mx4 | None, dx, lddx: int, dw, db, ws=None, stream=None):
+    _check(load().ia_mx4_linear_backward(_ptr(dy), lddy, _ptr(y), ldy, _ptr(x), ldx, dtype, M, N, K,
+                                         None if wt is None else C.byref(wt), _ptr(dx), lddx, _ptr(dw), _ptr(db),
+                                         _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 # ----------------------------------------------------------------- diagnostics

@@ -1,4 +1,5 @@
-"""Convenience objects over the C ABI: Decoder, HexPlane, Renderer.
+"""Convenience objects over the C ABI: Decoder, HexPlane, Renderer, Adam,
+gradient clipping and 4-bit (MXFP4) matrices and layers.
 
 Argument marshalling only (torch tensors in, torch tensors out); the work is
 done by libia.so.  Parameter objects are duck-typed like the ones in
@@ -390,9 +391,17 @@ class Adam:
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
         self.t = 0
 
-    def step(self, grads: dict):
-        """One update of every group that has a gradient in `grads` (name -> tensor)."""
+    def step(self, grads: dict, max_norm: float | None = None):
+        """One update of every group that has a gradient in `grads` (name -> tensor).
+
+        With max_norm the gradients count as clipped by their global norm over
+        the groups updated (they are not modified) and all groups go through
+        one ia_adam_clip_step; returns its stats, a device float32 tensor
+        {norm, factor, 1 if the norm is finite else 0}.  A step whose norm is
+        not finite changes no parameter and no moment."""
         self.t += 1
+        if max_norm is not None:
+            return self._clipped_step(grads, max_norm)
         for name, g in self.groups.items():
             grad = grads.get(name)
             if grad is None:
@@ -406,6 +415,102 @@ class Adam:
                 if g.get("f16") is not None:
                     raise ValueError(f"group {name}: an fp16 mirror needs a contiguous parameter")
                 ia.ia_adam_step_strided(p, grad.contiguous(), m, v, lr, self.beta1, self.beta2, self.eps, self.t)
+
+    def _clipped_step(self, grads: dict, max_norm: float):
+        names = [k for k in self.groups if grads.get(k) is not None]
+        arr = (ia.AdamGroup * len(names))()
+        keep, rates = [], {}  # contiguous copies live until the call has enqueued its reads
+        for d, name in zip(arr, names):
+            g, p = self.groups[name], self.groups[name]["param"]
+            m, v = self.state[name]
+            grad = grads[name]
+            if p.dtype != torch.float32 or grad.dtype != torch.float32 or grad.shape != p.shape:
+                raise ValueError(f"group {name}: parameter and gradient must be float32 of one shape")
+            if not grad.is_contiguous():
+                grad = grad.contiguous()
+                keep.append(grad)
+            f16 = g.get("f16")
+            if p.is_contiguous():
+                d.rows, d.dim, d.param_stride = p.numel(), 1, 1
+            elif p.dim() == 2 and p.stride(1) == 1 and p.stride(0) >= p.shape[1] and f16 is None:
+                d.rows, d.dim, d.param_stride = p.shape[0], p.shape[1], p.stride(0)
+            else:
+                raise ValueError(f"group {name}: the parameter must be contiguous, or [rows, dim] rows of a wider "
+                                 "array without an fp16 mirror")
+            if g["lr"] not in rates:
+                rates[g["lr"]] = lr_at(self.t - 1, g["lr"], self.warmup, self.total)
+            d.param, d.grad, d.m, d.v = p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr()
+            d.param_f16 = None if f16 is None else f16.data_ptr()
+            d.lr = rates[g["lr"]]
+        device = self.groups[names[0]]["param"].device if names else "cuda"
+        stats = torch.empty(3, device=device)
+        ws = torch.empty(ia.ia_clip_workspace_size(len(names)), dtype=torch.uint8, device=device)
+        ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t, ws, stats)
+        return stats
+
+
+_DTYPES = {torch.float32: ia.IA_DTYPE_F32, torch.float16: ia.IA_DTYPE_F16, torch.bfloat16: ia.IA_DTYPE_BF16}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"float32, float16 or bfloat16 expected, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("a tensor on the GPU expected")
+    return d
+
+
+class GradClip:
+    """Clipping of a list of gradient tensors by their global norm (Pascanu,
+    Mikolov & Bengio 2013): factor = max_norm / norm where norm > max_norm,
+    else 1.  The tensors (float32, float16 or bfloat16 in any mix; contiguous,
+    or [rows, dim] rows of a wider array) are described once and may be filled
+    anew before every call; `out` (same shapes and types) receives the clipped
+    values, without it they are scaled in place.
+
+    clip(max_norm) clips and norm() only measures; both return a new device
+    float32 tensor {norm, factor, 1 if the norm is finite else 0}."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        if self.out is not None and len(self.out) != len(self.grads):
+            raise ValueError("as many outputs as gradients expected")
+        self._arr = (ia.Grad * len(self.grads))()
+        for k, (d, g) in enumerate(zip(self._arr, self.grads)):
+            d.dtype = _dtype(g)
+            d.data = g.data_ptr()
+            o = g if self.out is None else self.out[k]
+            if o.dtype != g.dtype or o.shape != g.shape or o.device != g.device:
+                raise ValueError(f"output {k} differs from its gradient in type, shape or device")
+            if g.is_contiguous() and o.is_contiguous():
+                d.rows, d.dim, d.stride, d.out_stride = g.numel(), 1, 1, 1
+            elif g.dim() == 2 and all(t.shape[1] <= 1 or t.stride(1) == 1 for t in (g, o)):
+                d.rows, d.dim, d.stride, d.out_stride = g.shape[0], max(g.shape[1], 1), g.stride(0), o.stride(0)
+                if g.shape[1] == 0:
+                    d.rows, d.stride, d.out_stride = 0, 1, 1
+            else:
+                raise ValueError(f"gradient {k} must be contiguous or [rows, dim] with unit column stride")
+            d.out = None if self.out is None else o.data_ptr()
+        self.device = self.grads[0].device if self.grads else torch.device("cuda")
+        self._ws_bytes = ia.ia_clip_workspace_size(len(self.grads))
+
+    def _call(self, fn, max_norm):
+        stats = torch.empty(3, device=self.device)
+        fn(self._arr, max_norm, torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device), stats)
+        return stats
+
+    def __call__(self, max_norm: float):
+        return self._call(ia.ia_clip_grad_norm, max_norm)
+
+    def norm(self, max_norm: float = math.inf):
+        return self._call(ia.ia_grad_norm, max_norm)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None):
+    """Clip `grads` (a list of tensors) once; see GradClip.  Returns its stats."""
+    return GradClip(grads, out)(max_norm)
 
 
 def densify_positions(xyzt, grad_acc, grad_count, attrs: dict, m, v, noise, grad_threshold: float,
@@ -544,3 +649,156 @@ class FrameGraphs:
         """Replay the graphs of `frames` (default: all) in order on the current stream."""
         for f in (range(len(self.graphs)) if frames is None else frames):
             self.graphs[f].replay()
+
+
+_ACTS = {"none": ia.IA_ACT_NONE, "relu": ia.IA_ACT_RELU}
+
+
+def _matrix(t: torch.Tensor, name: str):
+    """(dtype, rows, cols, row stride) of a 2-D tensor with unit column stride; a row stride of 0 repeats one row."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
+    rows, cols = t.shape
+    return _dtype(t), rows, cols, (t.stride(0) if rows > 1 else cols)
+
+
+def _bytes(n: int, device):
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+class Mx4Tensor:
+    """A [rows, cols] matrix in MXFP4: codes uint8 [rows, 16 ceil(cols / 32)]
+    (two E2M1 codes a byte, the earlier value in the low half), scales uint8
+    [rows, ceil(cols / 32)] (2^(byte - 127), 255 = NaN)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        blocks = (cols + 31) // 32
+        rows = codes.shape[0]
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda or not scales.is_cuda:
+            raise ValueError("codes and scales must be uint8 tensors on the GPU")
+        if (tuple(codes.shape) != (rows, 16 * blocks) or tuple(scales.shape) != (rows, blocks)
+                or not codes.is_contiguous() or not scales.is_contiguous()):
+            raise ValueError(f"codes [{rows}, {16 * blocks}] and scales [{rows}, {blocks}] expected, contiguous")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+
+    @property
+    def c(self):
+        """The ia_mx4 that describes this matrix."""
+        return ia.mx4(self.codes, self.scales, self.rows, self.cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda"):
+        blocks = (cols + 31) // 32
+        return cls(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
+                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+
+    def dequantize(self, dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The values, rounded once to dtype (float32, float16 or bfloat16)."""
+        if out is None:
+            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
+        d, rows, cols, ld = _matrix(out, "out")
+        if (rows, cols) != (self.rows, self.cols):
+            raise ValueError("out has another shape")
+        ia.ia_mx4_dequantize(self.c, d, out, ld)
+        return out
+
+
+def mx4_quantize(x: torch.Tensor, transpose: bool = False, out: Mx4Tensor | None = None) -> Mx4Tensor:
+    """x [rows, cols] in MXFP4, blocks along its rows; with transpose the
+    matrix [cols, rows] of its columns, blocks along them."""
+    d, rows, cols, ld = _matrix(x, "x")
+    if out is None:
+        out = Mx4Tensor.empty(cols, rows, x.device) if transpose else Mx4Tensor.empty(rows, cols, x.device)
+    ia.ia_mx4_quantize(x, d, rows, cols, ld, transpose, out.c)
+    return out
+
+
+def _bias(bias, n: int):
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (n,) or not bias.is_contiguous()
+                             or not bias.is_cuda):
+        raise ValueError(f"bias must be a contiguous float32 [{n}] on the GPU")
+    return bias
+
+
+def mx4_matmul(a: Mx4Tensor, b: Mx4Tensor, bias: torch.Tensor | None = None, act: str = "none",
+               dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """act(a b^T + bias): a [M, K], b [N, K] -> [M, N] of dtype; act "none" or "relu"."""
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+    d, rows, cols, ld = _matrix(out, "out")
+    if (rows, cols) != (a.rows, b.rows):
+        raise ValueError("out has another shape")
+    ws = _bytes(ia.ia_mx4_matmul_workspace_size(a.rows, b.rows, a.cols), out.device)
+    ia.ia_mx4_matmul(a.c, b.c, _bias(bias, b.rows), _ACTS[act], d, out, ld, ws)
+    return out
+
+
+def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: torch.Tensor | None = None, act: str = "none",
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """A linear layer with MXFP4 weights: act(Q(x) w^T + bias), x [M, K]
+    quantised along its rows, w [N, K]; returns [M, N] of x's type."""
+    d, M, K, ldx = _matrix(x, "x")
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, the weights {w.cols}")
+    if out is None:
+        out = torch.empty((M, w.rows), dtype=x.dtype, device=x.device)
+    do, rows, cols, ldy = _matrix(out, "out")
+    if (do, rows, cols) != (d, M, w.rows):
+        raise ValueError("out has another shape or type")
+    ws = _bytes(ia.ia_mx4_linear_workspace_size(M, K, w.rows), x.device)
+    ia.ia_mx4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
+    return out
+
+
+def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, wt: Mx4Tensor | None, y: torch.Tensor | None = None,
+                        want_x: bool = True) -> dict:
+    """Gradients of mx4_linear for upstream dy [M, N]: x [M, K] of x's type
+    (with want_x), weight [N, K] and bias [N] in float32.  wt: the [N, K]
+    weights quantised along their outputs (mx4_quantize(w, transpose=True), so
+    [K, N]); y: the layer's output when its activation was ReLU."""
+    d, M, N, lddy = _matrix(dy, "dy")
+    dx_, Mx, K, ldx = _matrix(x, "x")
+    if dx_ != d or Mx != M:
+        raise ValueError("dy and x must have one type and number of rows")
+    ldy = 0
+    if y is not None:
+        dt, My, Ny, ldy = _matrix(y, "y")
+        if (dt, My, Ny) != (d, M, N):
+            raise ValueError("y must have dy's type and shape")
+    if want_x and (wt is None or (wt.rows, wt.cols) != (K, N)):
+        raise ValueError(f"wt must be [{K}, {N}]")
+    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
+    dw = torch.empty((N, K), device=x.device)
+    db = torch.empty(N, device=x.device)
+    ws = _bytes(ia.ia_mx4_linear_backward_workspace_size(M, N, K), x.device)
+    ia.ia_mx4_linear_backward(dy, lddy, y, ldy, x, ldx, d, M, N, K, wt.c if want_x else None, dx, K, dw, db, ws)
+    return {"x": dx, "weight": dw, "bias": db}
+
+
+class Mx4Linear:
+    """A linear layer trained with its products in MXFP4: fp32 master weight
+    [N, K] and bias [N] (an optimiser updates them in place, then update()
+    quantises them again) and the weight's two 4-bit forms, along its inputs
+    (forward) and along its outputs (the input's gradient)."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none"):
+        if act not in _ACTS:
+            raise ValueError("act must be 'none' or 'relu'")
+        self.weight, self.bias, self.act = weight, _bias(bias, weight.shape[0]), act
+        N, K = weight.shape
+        self.w = Mx4Tensor.empty(N, K, weight.device)
+        self.wt = Mx4Tensor.empty(K, N, weight.device)
+        self.update()
+
+    def update(self):
+        mx4_quantize(self.weight, out=self.w)
+        mx4_quantize(self.weight, transpose=True, out=self.wt)
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        return mx4_linear(x, self.w, self.bias, self.act)
+
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, y: torch.Tensor | None = None, want_x: bool = True) -> dict:
+        """Gradients {x, weight, bias} for upstream dy; y is this layer's output (needed for ReLU)."""
+        if self.act == "relu" and y is None:
+            raise ValueError("a ReLU layer's backward needs its output y")
+        return mx4_linear_backward(dy, x, self.wt, y if self.act == "relu" else None, want_x)

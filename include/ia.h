@@ -56,7 +56,9 @@ typedef int32_t ia_status;
 
 #define IA_DTYPE_F32 0
 #define IA_DTYPE_F16 1
+#define IA_DTYPE_BF16 2 /* gradient norm / clipping and MXFP4 entry points only */
 
+#define IA_ACT_NONE (-1) /* ia_mx4_matmul and ia_mx4_linear only                */
 #define IA_ACT_RELU 0
 #define IA_ACT_GELU 1 /* exact: 0.5 x (1 + erf(x / sqrt 2)) */
 
@@ -580,6 +582,161 @@ IA_API ia_status ia_densify(const float* xyzt, const float* grad_acc, const int3
                             float* out_m, float* out_v, int64_t out_capacity, int64_t* out_n, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Gradient norm, clipping and the clipped Adam step over many tensors       */
+/* ------------------------------------------------------------------------ */
+
+/* One gradient tensor: rows of `dim` values `stride` elements apart (dense:
+ * rows = its size, dim = stride = 1, or stride = dim). */
+typedef struct {
+    void* data;         /* device, dtype (written only where out is NULL)      */
+    void* out;          /* device, dtype: where ia_clip_grad_norm writes; NULL:
+                           in place.  Must not overlap data unless equal to it
+                           with the same stride                                */
+    int64_t rows;
+    int32_t dim;
+    int32_t stride;     /* >= dim                                              */
+    int32_t out_stride; /* >= dim, rows of out (unused without out)            */
+    int32_t dtype;      /* IA_DTYPE_F32, _F16 or _BF16; any mix in one call    */
+} ia_grad;
+
+/* Bytes of workspace for `count` tensors (ia_grad_norm, ia_clip_grad_norm,
+ * ia_adam_clip_step).  Errors: INVALID_ARG. */
+IA_API ia_status ia_clip_workspace_size(int32_t count, size_t* bytes);
+
+/* Global L2 norm of `count` gradient tensors and the factor that clips it
+ * (Pascanu, Mikolov & Bengio 2013, "On the difficulty of training recurrent
+ * neural networks", §3.2):
+ *   norm   = sqrt(sum over tensors and elements of g^2)
+ *   factor = max_norm / norm if norm > max_norm, else 1.
+ *   grads: host [count], read before the call returns; data and out are
+ *          device pointers aligned to their dtype (any element of a bucket);
+ *          empty tensors and count = 0 are allowed (norm 0, factor 1)
+ *   max_norm >= 0; +infinity never clips
+ *   stats: device float[3], overwritten: {norm, factor, 1 if norm is finite
+ *          else 0}.  The squares are summed in double in a fixed order (the
+ *          same on every run).  An infinite element gives norm = infinity and
+ *          factor 0, a NaN gives NaN for both.
+ *   ws, ws_bytes: device workspace of ia_clip_workspace_size(count) bytes,
+ *          256-byte aligned.
+ * Asynchronous on stream; no host synchronisation.
+ * Errors: INVALID_ARG (null, negative sizes, stride < dim, misalignment, over
+ * 2^40 elements, max_norm negative or NaN), UNSUPPORTED (dtype),
+ * WORKSPACE_TOO_SMALL, DEVICE. */
+IA_API ia_status ia_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes,
+                              float* stats, void* stream);
+
+/* ia_grad_norm, then out = factor * data (rounded once to dtype) for every
+ * tensor, in place where out is NULL (a factor of 1 then leaves the memory
+ * untouched).  A NaN factor makes every value NaN; a zero factor makes finite
+ * values zero and infinite ones NaN.  Errors: as ia_grad_norm. */
+IA_API ia_status ia_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes,
+                                   float* stats, void* stream);
+
+/* One parameter group of ia_adam_clip_step: ia_adam_step's arrays (param_f16
+ * nullable) with the parameter as rows of `dim` values `param_stride` floats
+ * apart, as in ia_adam_step_strided; grad, m, v, param_f16 dense [rows][dim]. */
+typedef struct {
+    float* param;
+    const float* grad;
+    float* m;
+    float* v;
+    uint16_t* param_f16;
+    int64_t rows;
+    int32_t dim;
+    int32_t param_stride;
+    float lr;
+} ia_adam_group;
+
+/* One Adam step over `count` groups with the gradients clipped by their
+ * global norm: ia_adam_step (or _strided) of every group on factor * grad,
+ * where norm and factor are those of ia_grad_norm over the groups' gradients
+ * (which are not modified).  With factor 1 the results are those of
+ * ia_adam_step bit for bit.  If the norm is not finite no parameter, moment or
+ * mirror changes (stats tells).  groups: host [count], read before the call
+ * returns; stats, ws as ia_grad_norm.
+ * Errors: INVALID_ARG (also step < 1, betas outside [0, 1), negative or NaN
+ * eps or lr, dim < 1, param_stride < dim), WORKSPACE_TOO_SMALL, DEVICE. */
+IA_API ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
+                                   float eps, int32_t step, void* ws, size_t ws_bytes, float* stats, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit microscaled floating point (MXFP4)                                  */
+/* ------------------------------------------------------------------------ */
+
+/* A matrix in MXFP4 (OCP Microscaling Formats specification v1.0): a row of
+ * `cols` values is ceil(cols / 32) blocks of 32 (zero past the row's end),
+ * each with one scale byte (2^(byte - 127), 255 = NaN) and 32 E2M1 codes
+ * (sign; 0 0.5 1 1.5 2 3 4 6), two to a byte, the earlier value in the low
+ * half.  17 bytes for 32 values. */
+typedef struct {
+    uint8_t* codes;  /* device [rows][ceil(cols/32) * 16], 16-byte aligned */
+    uint8_t* scales; /* device [rows][ceil(cols/32)]                       */
+    int64_t rows;
+    int64_t cols;
+} ia_mx4;
+
+/* Quantise x [rows][cols] (device, dtype F32, F16 or BF16, rows ld elements
+ * apart; ld = 0 repeats one row) to `out`:
+ *   transpose = 0: blocks along x's rows; out->rows = rows, out->cols = cols
+ *   transpose = 1: blocks along x's columns, out row j holding column j;
+ *                  out->rows = cols, out->cols = rows.
+ * Block scale 2^(floor(log2 max|x|) - 2) (at least 2^-127); codes rounded to
+ * nearest, ties to the even code, magnitudes of 6 and more scaled units give
+ * 6; zeros keep their sign.  A block with a NaN or an infinity gets the NaN
+ * scale and zero codes.  Empty matrices are allowed.
+ * Errors: INVALID_ARG (null, shapes that do not fit, 0 < ld < cols,
+ * misalignment, over 2^40 values), UNSUPPORTED (dtype), DEVICE. */
+IA_API ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 int32_t transpose, const ia_mx4* out, void* stream);
+
+/* x[rows][cols] (rows ld >= cols elements apart) = the values q stands for,
+ * rounded once to dtype; blocks with the NaN scale give NaN.
+ * Errors: as ia_mx4_quantize. */
+IA_API ia_status ia_mx4_dequantize(const ia_mx4* q, int32_t dtype, void* x, int64_t ld, void* stream);
+
+/* c[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]): a is [M][K], b is [N][K],
+ * c is [M][N] of dtype with rows ldc >= N elements apart.  Products and sums
+ * on the scaled matrix instructions with fp32 accumulation, rounded once to
+ * dtype.
+ *   bias: device fp32 [N] or NULL; act: IA_ACT_NONE or IA_ACT_RELU
+ *   ws, ws_bytes: device workspace of ia_mx4_matmul_workspace_size bytes,
+ *         256-byte aligned (may be NULL when that is 0).
+ * The sums are taken in a fixed order (the same on every run).  K = 0 gives
+ * act(bias).  A block with the NaN scale makes every sum it enters NaN.
+ * c must not overlap an input.  M, N, K < 2^31.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, act), WORKSPACE_TOO_SMALL, DEVICE. */
+IA_API ia_status ia_mx4_matmul_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+IA_API ia_status ia_mx4_matmul(const ia_mx4* a, const ia_mx4* b, const float* bias, int32_t act, int32_t dtype, void* c,
+                               int64_t ldc, void* ws, size_t ws_bytes, void* stream);
+
+/* A linear layer with MXFP4 weights: y = act(Q(x) w^T + bias), x [M][K] of
+ * dtype (rows ldx apart, 0 repeats one row) quantised along its rows as
+ * ia_mx4_quantize does, w [N][K], y [M][N] of dtype (rows ldy apart).  Any M
+ * from one row (serving) up.  Other arguments and errors as ia_mx4_matmul. */
+IA_API ia_status ia_mx4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes);
+IA_API ia_status ia_mx4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const ia_mx4* w, const float* bias,
+                               int32_t act, void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of ia_mx4_linear for upstream dy [M][N], the quantisations
+ * treated as the identity and every product in MXFP4:
+ *   d  = dy where y > 0, else 0 (ReLU), or dy when y is NULL
+ *   dx [M][K] (dtype) = Q(d) wt^T, blocks along N
+ *   dw [N][K] (fp32)  = Qc(d) Qc(x)^T, both in blocks along M (their columns)
+ *   db [N]    (fp32)  = sum over m of d (not quantised)
+ *   dy, y, x: device, dtype; rows lddy, ldy, ldx elements apart (0 repeats one
+ *        row); wt [K][N]: the weights quantised along their outputs
+ *        (ia_mx4_quantize of the [N][K] weights with transpose = 1); NULL
+ *        when dx is
+ *   dx (rows lddx >= K apart), dw, db: NULL skips that gradient
+ * Outputs are overwritten, in a fixed order of summation; M = 0 gives zero
+ * dw and db.  ws of ia_mx4_linear_backward_workspace_size bytes, 256-byte
+ * aligned.  Errors: as ia_mx4_matmul. */
+IA_API ia_status ia_mx4_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+IA_API ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void* y, int64_t ldy, const void* x,
+                                        int64_t ldx, int32_t dtype, int64_t M, int64_t N, int64_t K, const ia_mx4* wt,
+                                        void* dx, int64_t lddx, float* dw, float* db, void* ws, size_t ws_bytes,
+                                        void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics: per-kernel timing with HIP events                            */

@@ -129,3 +129,11 @@ def lr_schedule(step: int, base: float, warmup: int, total: int, final: float = 
         return base * (step + 1) / warmup
     t = min(max(step - warmup, 0), max(total - warmup, 1)) / max(total - warmup, 1)
     return final + 0.5 * (base - final) * (1.0 + math.cos(math.pi * t))
+
+
+def clip_factor(grads, max_norm: float):
+    """(norm, factor) of clipping by the global norm (Pascanu, Mikolov & Bengio, 2013, §3.2):
+    norm = sqrt of the sum of squares over every array, factor = max_norm / norm if norm > max_norm else 1."""
+    total = math.fsum(float(np.sum(np.asarray(g, np.float64) ** 2)) for g in grads)
+    norm = math.sqrt(total)
+    return norm, (max_norm / norm if norm > max_norm else 1.0)
