@@ -24,6 +24,8 @@
 // the first operand against row c of the second, accumulated in fp32.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ia_internal.h"
 
 namespace ia {
@@ -249,63 +251,244 @@ struct MatArgs {
     int64_t M, N, blocks;
     const float* bias;  // [N] or null
     int act;
-    void* c;            // [M][ldc]
+    void* c;            // [M][ldc]; with splits [splits][M][N] fp32
     int64_t ldc;
+    int64_t tiles_m, tiles_n, stages;  // tiles, and stages of 8 blocks a split takes
 };
 
 __device__ __forceinline__ intx8 widen(intx4 v) { return intx8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-__device__ __forceinline__ floatx4 mfma(intx4 a, int as, intx4 b, int bs, floatx4 c) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, 0, as, 0, bs);
+__device__ __forceinline__ float activate(float v, int act) {
+    return act == IA_ACT_RELU && v < 0.0f ? 0.0f : v;  // a NaN stays
 }
 
-// C[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]).  One wave per 64 x 64 tile.
-// The n rows are the MFMA's first operand: row 4 q + r of n tile j stands for
-// n = 16 q + 4 j + r, so that a lane ends with 16 consecutive n of one row m.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
-    const int64_t m0 = (int64_t)blockIdx.x * 128 + (wave & 1) * 64, n0 = (int64_t)blockIdx.y * 128 + (wave >> 1) * 64;
-    int64_t ra[4], rb[4];
+template <int BYTE>
+__device__ __forceinline__ floatx4 mfma(intx4 a, int as, intx4 b, int bs, floatx4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, BYTE, as, BYTE, bs);
+}
+
+// Tiled product.  A block of 2 x 2 waves computes a tile of 32 WT rows by 32
+// WT columns, a wave 16 WT by 16 WT of it in WT x WT accumulators.  The codes
+// of 8 blocks (256 values, one 128-byte line of a row) of every row pass
+// through LDS in two buffers, copied there by the LDS-DMA loads while the
+// other buffer is multiplied; the scales of 16 blocks follow in 16 bytes a
+// row, their 4 x 4 bytes transposed so that one 32-bit word holds a lane's
+// scales of four MFMA steps (block q of each), selected by the instruction.
+//   The block that stands in slot s of a row is s ^ key(row): the 16 rows that
+// one operand read touches then spread over all banks.
+//   The n rows are the MFMA's first operand: row 4 q + r of n tile j stands for
+// n = 64 (j / 4) + 16 q + 4 (j % 4) + r, so that a lane ends with 16
+// consecutive n of one row m and stores them together.
+//   Rows past the end repeat the last one (their results are not stored).
+// Blocks past the end of a row repeat its last block with scale byte 0 on both
+// sides: such a product is below 2^-240, under half of fp32's smallest value.
+constexpr int kStageBlocks = 8;
+
+__device__ __forceinline__ int key_a(int row) { return row & 7; }
+__device__ __forceinline__ int key_b(int row) { return (row & 3) | ((row >> 2) & 4); }
+
+// LDS row (within a wave's n rows) of lane c's row of n tile j.
+__device__ __forceinline__ int n_row(int j, int c) { return 64 * (j >> 2) + 16 * (c >> 2) + 4 * (j & 3) + (c & 3); }
+
+// The rows of one operand's tile: byte offsets of the lanes' rows from the
+// tile's first row, and the copies of their stages into LDS.  OFF is 32 bits
+// wide in the large tile, where registers are short (rows below 2^24 bytes).
+template <int ROWS, bool B, typename OFF>
+struct Codes {
+    const uint8_t* base;  // first block of the tile's first row
+    int blocks;
+    OFF row[ROWS / 32];
+    int slot;  // the block of a stage that this lane copies
+
+    __device__ __forceinline__ Codes(const uint8_t* codes, int64_t row0, int64_t rows, int64_t nblocks, int wave,
+                                     int lane) {
+        base = codes + row0 * nblocks * 16;
+        blocks = (int)nblocks;
+        const int64_t last = rows - 1 - row0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ra[i] = min(m0 + 16 * i + c, p.M - 1);
-        rb[i] = min(n0 + 16 * (c >> 2) + 4 * i + (c & 3), p.N - 1);
+        for (int i = 0; i < ROWS / 32; ++i)
+            row[i] = (OFF)(min((int64_t)(32 * i + 8 * wave + (lane >> 3)), last) * nblocks * 16);
+        const int r = 8 * wave + (lane >> 3);
+        slot = (lane & 7) ^ (B ? key_b(r) : key_a(r));
     }
-    floatx4 acc[4][4] = {};
-    for (int64_t k = 0; k < p.blocks; k += 4) {
-        const int64_t kb = k + q;
-        const bool in = kb < p.blocks;
-        intx4 a[4], b[4];
-        int as[4], bs[4];
+
+    // blocks 8 t .. 8 t + 7
+    __device__ __forceinline__ void copy(intx4* buf, int t, int wave) const {
+        const uint8_t* at = base + min(t * kStageBlocks + slot, blocks - 1) * (int64_t)16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t ia = ra[i] * p.blocks + kb, ib = rb[i] * p.blocks + kb;
-            a[i] = in ? *reinterpret_cast<const intx4*>(p.a + ia * 16) : intx4{0, 0, 0, 0};
-            b[i] = in ? *reinterpret_cast<const intx4*>(p.b + ib * 16) : intx4{0, 0, 0, 0};
-            as[i] = in ? (int)p.as[ia] : 127;
-            bs[i] = in ? (int)p.bs[ib] : 127;
+        for (int i = 0; i < ROWS / 32; ++i)
+            // key_b takes bit 4 of the row, which is the same for rows 32 apart
+            __builtin_amdgcn_global_load_lds((const void*)(at + row[i]),
+                                             (__attribute__((address_space(3))) void*)(buf + (4 * i + wave) * 64), 16,
+                                             0, 0);
+    }
+};
+
+// Scale bytes k0 .. k0 + 15 of a row, zero past its end.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int k0, int blocks) {
+    uint4 v;
+    if (k0 + 16 <= blocks) {
+        __builtin_memcpy(&v, row + k0, 16);
+        return v;
+    }
+    uint64_t w[2] = {0, 0};
+#pragma unroll 1
+    for (int i = 0; i < 16 && k0 + i < blocks; ++i) {
+        const uint64_t byte = (uint64_t)row[k0 + i] << (8 * (i & 7));
+        w[0] |= i < 8 ? byte : 0;
+        w[1] |= i < 8 ? 0 : byte;
+    }
+    return make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+}
+
+// Byte matrix [4][4] (word = row) transposed.
+__device__ __forceinline__ uint4 transpose4(uint4 v) {
+    const uint32_t lo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u), hi = __builtin_amdgcn_perm(v.w, v.z, 0x05010400u);
+    const uint32_t lo2 = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u), hi2 = __builtin_amdgcn_perm(v.w, v.z, 0x07030602u);
+    return make_uint4(__builtin_amdgcn_perm(hi, lo, 0x05040100u), __builtin_amdgcn_perm(hi, lo, 0x07060302u),
+                      __builtin_amdgcn_perm(hi2, lo2, 0x05040100u), __builtin_amdgcn_perm(hi2, lo2, 0x07060302u));
+}
+
+template <int WT, int HALF>
+__device__ __forceinline__ void multiply_stage(const intx4* la, const intx4* lb, const int (&sa)[WT],
+                                               const int (&sb)[WT], int wm, int wn, int q, int c,
+                                               floatx4 (&acc)[WT][WT]) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const int slot = (4 * ks + q) ^ (c & 7);
+        intx4 a[WT], b[WT];
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+            a[i] = la[(wm + 16 * i + c) * 8 + slot];
+            b[i] = lb[(wn + n_row(i, c)) * 8 + slot];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma(b[j], bs[j], a[i], as[i], acc[i][j]);
-    }
-    T* out = reinterpret_cast<T*>(p.c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + c;
-        if (m >= p.M) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t n = n0 + 16 * q + 4 * j + r;
-                if (n >= p.N) continue;
-                float v = acc[i][j][r] + (p.bias ? p.bias[n] : 0.0f);
-                if (p.act == IA_ACT_RELU) v = v < 0.0f ? 0.0f : v;  // a NaN stays
-                out[m * p.ldc + n] = (T)v;
+            for (int j = 0; j < WT; ++j) {
+                acc[i][j] = ks == 0 ? mfma<2 * HALF>(b[j], sb[j], a[i], sa[i], acc[i][j])
+                                    : mfma<2 * HALF + 1>(b[j], sb[j], a[i], sa[i], acc[i][j]);
             }
+    }
+}
+
+// 16 consecutive values of one output row from column n on.
+template <typename T>
+__device__ __forceinline__ void store_run(T* row, int64_t n, int64_t N, const float (&v)[16]) {
+    T o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = (T)v[k];
+    if (n + 16 <= N) {
+        __builtin_memcpy(row + n, o, sizeof(o));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (n + k < N) row[n + k] = o[k];
+    }
+}
+
+// Tile index of a block so that blocks of one XCD (every eighth block) take
+// neighbouring tiles: runs of 8 tile rows, column by column.
+__device__ __forceinline__ void tile_of(int64_t b, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
+    const int64_t total = tm * tn, per = total / 8, rest = total % 8, x = b % 8;
+    int64_t t = x * per + min(x, rest) + b / 8;
+    const int64_t group = 8 * tn, g = t / group, h = min((int64_t)8, tm - 8 * g);
+    t -= g * group;
+    im = 8 * g + t % h;
+    in = t / h;
+}
+
+template <typename T, int WT>
+__global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
+    constexpr int R = 32 * WT;  // tile rows
+    __shared__ intx4 a0[R * 8], a1[R * 8], b0[R * 8], b1[R * 8];
+    __shared__ uint4 sca[2][R], scb[2][R];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    int64_t im, in;
+    tile_of(blockIdx.x, p.tiles_m, p.tiles_n, im, in);
+    const int64_t m0 = im * R, n0 = in * R;
+    const int wm = (wave & 1) * 16 * WT, wn = (wave >> 1) * 16 * WT;
+    const int blocks = (int)p.blocks;
+    const int t0 = (int)(blockIdx.y * p.stages), t1 = min(t0 + (int)p.stages, (blocks + kStageBlocks - 1) / kStageBlocks);
+    typedef typename std::conditional<WT == 8, uint32_t, int64_t>::type Off;
+    const Codes<R, false, Off> ca(p.a, m0, p.M, p.blocks, wave, lane);
+    const Codes<R, true, Off> cb(p.b, n0, p.N, p.blocks, wave, lane);
+    const bool scaler = (int)threadIdx.x < R;
+    const uint8_t* rsa = p.as + min(m0 + (int)(threadIdx.x % R), p.M - 1) * p.blocks;
+    const uint8_t* rsb = p.bs + min(n0 + (int)(threadIdx.x % R), p.N - 1) * p.blocks;
+    floatx4 acc[WT][WT] = {};
+
+    // Stages go in pairs that share a group of scales; the missing second half
+    // of a last pair has zero scales.
+    if (t0 < t1) {
+        ca.copy(a0, t0, wave);
+        cb.copy(b0, t0, wave);
+        if (scaler) {
+            sca[0][threadIdx.x] = transpose4(load_scales(rsa, t0 * kStageBlocks, blocks));
+            scb[0][threadIdx.x] = transpose4(load_scales(rsb, t0 * kStageBlocks, blocks));
+        }
+    }
+    int buf = 0;
+    for (int t = t0; t < t1; t += 2, buf ^= 1) {
+        // stage t's codes and scales are in LDS after this barrier, and every
+        // wave has read the other buffers for the last time
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        uint4 na = {0, 0, 0, 0}, nb = {0, 0, 0, 0};
+        if (scaler) {
+            na = load_scales(rsa, (t + 2) * kStageBlocks, blocks);
+            nb = load_scales(rsb, (t + 2) * kStageBlocks, blocks);
+        }
+        ca.copy(a1, t + 1, wave);
+        cb.copy(b1, t + 1, wave);
+        int sa[WT], sb[WT];
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+            sa[i] = reinterpret_cast<const int*>(&sca[buf][wm + 16 * i + c])[q];
+            sb[i] = reinterpret_cast<const int*>(&scb[buf][wn + n_row(i, c)])[q];
+        }
+        multiply_stage<WT, 0>(a0, b0, sa, sb, wm, wn, q, c, acc);
+        if (scaler) {
+            sca[buf ^ 1][threadIdx.x] = transpose4(na);
+            scb[buf ^ 1][threadIdx.x] = transpose4(nb);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (t + 2 < t1) {
+            ca.copy(a0, t + 2, wave);
+            cb.copy(b0, t + 2, wave);
+        }
+        multiply_stage<WT, 1>(a1, b1, sa, sb, wm, wn, q, c, acc);
+    }
+    T* out = reinterpret_cast<T*>(p.c) + (int64_t)blockIdx.y * p.M * p.N;
+#pragma unroll
+    for (int g = 0; g < WT / 4; ++g) {
+        const int64_t n = n0 + wn + 64 * g + 16 * q;
+        if (n >= p.N) continue;
+        float bias[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) bias[k] = p.bias ? p.bias[min(n + k, p.N - 1)] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+            const int64_t m = m0 + wm + 16 * i + c;
+            if (m >= p.M) continue;
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = activate(acc[i][4 * g + (k >> 2)][k & 3] + bias[k], p.act);
+            store_run(out + m * p.ldc, n, p.N, v);
+        }
+    }
+}
+
+// The splits of a long sum added in order: c = act(sum of part[s] + bias).
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* part, int splits) {
+    const int64_t total = p.M * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / p.N, n = i - m * p.N;
+        float v = 0.0f;
+        for (int s = 0; s < splits; ++s) v += part[s * total + i];
+        reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
     }
 }
 
@@ -369,10 +552,56 @@ hipError_t dequantize_t(const Mx4View& q, void* x, int64_t ldx, hipStream_t s) {
     return hipGetLastError();
 }
 
+// How a product is cut: tiles of 256 x 256 where they fill the 256 CUs, else
+// of 128 x 128, and when those are few the sum over k in up to `splits` parts
+// of at least 4 stages (1,024 values) each, joined in order.
+struct MatPlan {
+    int wt;
+    int64_t tiles_m, tiles_n, stages;
+    int splits;
+};
+MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
+    MatPlan p{};
+    p.wt = ceil_div(M, 256) * ceil_div(N, 256) >= 192 && blocks < (int64_t)1 << 20 ? 8 : 4;
+    p.tiles_m = ceil_div(M, 32 * p.wt);
+    p.tiles_n = ceil_div(N, 32 * p.wt);
+    const int64_t all = ceil_div(blocks, kStageBlocks), tiles = p.tiles_m * p.tiles_n;
+    int64_t splits = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
+    if (splits > all / 4) splits = all / 4;
+    if (splits < 1) splits = 1;
+    p.stages = ceil_div(ceil_div(all, splits), 2) * 2;  // whole groups of 16 scales
+    if (p.stages < 2) p.stages = 2;
+    p.splits = (int)ceil_div(all, p.stages);
+    if (p.splits < 1) p.splits = 1;
+    return p;
+}
+
 template <typename T>
-hipError_t matmul_t(const MatArgs& p, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div(p.M, 128), (unsigned)ceil_div(p.N, 128));
-    IA_LAUNCH("mx4_matmul_kernel", mx4_matmul_kernel<T>, grid, dim3(256), 0, s, p);
+hipError_t launch_tiles(const MatArgs& p, const MatPlan& plan, hipStream_t s) {
+    const dim3 grid((unsigned)(plan.tiles_m * plan.tiles_n), (unsigned)plan.splits);
+    if (plan.wt == 8)
+        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 8>), grid, dim3(256), 0, s, p);
+    else
+        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 4>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t matmul_t(MatArgs p, void* ws, hipStream_t s) {
+    const MatPlan plan = mat_plan(p.M, p.N, p.blocks);
+    p.tiles_m = plan.tiles_m;
+    p.tiles_n = plan.tiles_n;
+    p.stages = plan.stages;
+    if (plan.splits == 1) return launch_tiles<T>(p, plan, s);
+    MatArgs part = p;
+    part.bias = nullptr;
+    part.act = IA_ACT_NONE;
+    part.c = ws;
+    part.ldc = p.N;
+    hipError_t e = launch_tiles<float>(part, plan, s);
+    if (e != hipSuccess) return e;
+    IA_LAUNCH("mx4_join_kernel", mx4_join_kernel<T>, dim3(grid_for(p.M * p.N)), dim3(256), 0, s, p, (const float*)ws,
+              plan.splits);
     return hipGetLastError();
 }
 
@@ -419,28 +648,34 @@ hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64
     return IA_BY_DTYPE(dtype, dequantize_t, q, x, ldx, s);
 }
 
-size_t mx4_matmul_workspace(int64_t M, int64_t N, int64_t K) { return 0; }
+size_t mx4_matmul_workspace(int64_t M, int64_t N, int64_t K) {
+    const int splits = mat_plan(M, N, mx4_blocks(K)).splits;
+    return splits > 1 ? round_up((size_t)splits * (size_t)M * (size_t)N * sizeof(float)) : 0;
+}
 
 hipError_t launch_mx4_matmul(const Mx4View& a, const Mx4View& b, const float* bias, int32_t act, int32_t dtype, void* c,
                              int64_t ldc, void* ws, hipStream_t s) {
     if (a.rows == 0 || b.rows == 0) return hipSuccess;
-    const MatArgs p{a.codes, a.scales, b.codes, b.scales, a.rows, b.rows, mx4_blocks(a.cols), bias, act, c, ldc};
-    return IA_BY_DTYPE(dtype, matmul_t, p, s);
+    const MatArgs p{a.codes, a.scales, b.codes, b.scales, a.rows, b.rows, mx4_blocks(a.cols), bias, act, c, ldc, 0, 0, 0};
+    return IA_BY_DTYPE(dtype, matmul_t, p, ws, s);
 }
 
-size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) { return scratch_bytes(M, K); }
+size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) {
+    return scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+}
 
 hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
                              int64_t ldy, void* ws, hipStream_t s) {
     const Mx4View q = scratch_view(ws, x.rows, x.cols);
     hipError_t e = launch_mx4_quantize(x, false, q, s);
     if (e != hipSuccess) return e;
-    return launch_mx4_matmul(q, w, bias, act, x.dtype, y, ldy, nullptr, s);
+    return launch_mx4_matmul(q, w, bias, act, x.dtype, y, ldy, (char*)ws + scratch_bytes(x.rows, x.cols), s);
 }
 
 size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
+    const size_t x = mx4_matmul_workspace(M, K, N), w = mx4_matmul_workspace(N, K, M);
     return scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
-           round_up((size_t)ceil_div(M, kSumRows) * (size_t)N * sizeof(float));
+           round_up((size_t)ceil_div(M, kSumRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
 }
 
 hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
@@ -450,15 +685,16 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     const Mx4View dr = scratch_view(at, M, N), dc = scratch_view(at += scratch_bytes(M, N), N, M),
                   xc = scratch_view(at += scratch_bytes(N, M), K, M);
     float* part = (float*)(at += scratch_bytes(K, M));
+    void* mat = at + round_up((size_t)ceil_div(M, kSumRows) * (size_t)N * sizeof(float));
     hipError_t e = hipSuccess;
     if (dx) {
         e = launch_mx4_quantize(dy, false, dr, s);
-        if (e == hipSuccess) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, nullptr, s);
+        if (e == hipSuccess) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
     }
     if (e == hipSuccess && dw) {
         e = launch_mx4_quantize(dy, true, dc, s);
         if (e == hipSuccess) e = launch_mx4_quantize(x, true, xc, s);
-        if (e == hipSuccess) e = launch_mx4_matmul(dc, xc, nullptr, kMx4NoAct, IA_DTYPE_F32, dw, K, nullptr, s);
+        if (e == hipSuccess) e = launch_mx4_matmul(dc, xc, nullptr, kMx4NoAct, IA_DTYPE_F32, dw, K, mat, s);
     }
     if (e == hipSuccess && db) e = IA_BY_DTYPE(dy.dtype, colsum_t, dy, part, db, s);
     return e;
