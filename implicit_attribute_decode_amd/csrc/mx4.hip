@@ -158,6 +158,15 @@ struct Source {
     int64_t rows, cols, ldx, ldy;
 };
 
+// Row of block i of a matrix with `blocks` blocks a row, where i is at most 255
+// past `base`, which is the same for all threads: one 64-bit division for the
+// workgroup and a 32-bit one a thread.
+__device__ __forceinline__ int64_t row_of(int64_t i, int64_t blocks, int64_t base) {
+    const int64_t r = base / blocks;
+    const int64_t k = i - r * blocks;
+    return r + (blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)k / (uint32_t)blocks) : k / blocks);
+}
+
 // One thread per block of a row.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Source<T> s, int64_t blocks, uint8_t* codes,
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Source<T> s, int
     for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
         const int64_t i = base + threadIdx.x;
         if (i >= total) return;
-        const int64_t r = i / blocks, k0 = (i - r * blocks) * kBlock;
+        const int64_t r = row_of(i, blocks, base), k0 = (i - r * blocks) * kBlock;
         Values<T> v = load_values(s.x + r * s.ldx, k0, s.cols);
         if (s.y) mask(v, load_values(s.y + r * s.ldy, k0, s.cols));
         uint32_t byte;
@@ -176,67 +185,174 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Source<T> s, int
     }
 }
 
-// Blocks along the columns of x: output row j holds column j.  One thread per
-// (column, block of 32 rows), neighbouring threads on neighbouring columns.
+// Blocks along the columns of x (output row j holds column j) and, from the
+// same reading of x, its column sums and blocks along the rows.  A tile of 256
+// rows and 128 bytes of columns is read in whole lines, masked, and laid in
+// LDS with a row pitch of 144 bytes: 16-byte reads along a row and reads down
+// the columns both touch every bank once.  A thread takes one block of a
+// column at a time; the column codes go back through LDS so that a column's
+// eight blocks leave as one line.
+constexpr int kTileRows = 256;
+constexpr int kTilePitch = 144;
+
+struct ColumnOut {
+    uint8_t* codes;   // [cols][blocks] along x's columns, or null
+    uint8_t* scales;
+    int64_t blocks;
+    uint8_t* rcodes;  // [rows][rblocks] along x's rows, or null
+    uint8_t* rscales;
+    int64_t rblocks;
+    float* sums;      // [tile row][cols] sums of 256 rows, or null
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_quantize_cols_kernel(Source<T> s, int64_t blocks, uint8_t* codes,
-                                                                uint8_t* scales) {
-    const int64_t total = s.cols * blocks;
-    for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
-        const int64_t i = base + threadIdx.x;
-        if (i >= total) return;
-        const int64_t b = i / s.cols, j = i - b * s.cols, r0 = b * kBlock;
+__device__ __forceinline__ void quantize_tile(const Source<T>& s, const ColumnOut& o, int64_t it, int64_t jt) {
+    constexpr int C = 128 / (int)sizeof(T), E = 16 / (int)sizeof(T);  // columns of a tile, of a 16-byte piece
+    __shared__ __attribute__((aligned(16))) uint8_t tile[kTileRows * kTilePitch];
+    __shared__ uint8_t cscale[C][8];
+    __shared__ float sum[8][C];
+    const int t = threadIdx.x;
+    const int64_t r0 = it * kTileRows, c0 = jt * C;
+    const int piece = t & 7;
+    struct Piece {
+        T e[E];
+    };
+    Piece x[8], y[8];
+    const int64_t j0 = c0 + piece * E;
+    const bool whole = j0 + E <= s.cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 32 * i + (t >> 3);
+        if (r < s.rows && whole) {
+            __builtin_memcpy(&x[i], s.x + r * s.ldx + j0, 16);
+            if (s.y) __builtin_memcpy(&y[i], s.y + r * s.ldy + j0, 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const bool in = r < s.rows && j0 + k < s.cols;
+                x[i].e[k] = in ? s.x[r * s.ldx + j0 + k] : (T)0.0f;
+                if (s.y) y[i].e[k] = in ? s.y[r * s.ldy + j0 + k] : (T)0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (s.y) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[i].e[k] = (float)y[i].e[k] > 0.0f ? x[i].e[k] : (T)0.0f;
+        }
+        __builtin_memcpy(tile + (32 * i + (t >> 3)) * kTilePitch + 16 * piece, &x[i], 16);
+    }
+    __syncthreads();
+    if (o.rcodes) {
+#pragma unroll
+        for (int i = 0; i < C / 32; ++i) {
+            const int p = t + 256 * i, row = p / (C / 32), b = p % (C / 32);
+            const int64_t r = r0 + row, kb = c0 / 32 + b;
+            Values<T> v;
+            __builtin_memcpy(&v, tile + row * kTilePitch + b * (int)sizeof(v), sizeof(v));
+            uint32_t byte;
+            const intx4 q = quantize(v, byte);
+            if (r < s.rows && kb < o.rblocks) {
+                *reinterpret_cast<intx4*>(o.rcodes + (r * o.rblocks + kb) * 16) = q;
+                o.rscales[r * o.rblocks + kb] = (uint8_t)byte;
+            }
+        }
+    }
+    if (!o.codes && !o.sums) return;
+    intx4 q[C / 32];
+#pragma unroll
+    for (int i = 0; i < C / 32; ++i) {
+        const int col = t % C, b = t / C + (256 / C) * i;
         Values<T> v;
 #pragma unroll
-        for (int k = 0; k < kBlock; ++k) {
-            const int64_t r = r0 + k;
-            T e = (T)0.0f;
-            if (r < s.rows) {
-                e = s.x[r * s.ldx + j];
-                if (s.y && !((float)s.y[r * s.ldy + j] > 0.0f)) e = (T)0.0f;
-            }
-            v.p[k >> 1][k & 1] = e;
-        }
+        for (int k = 0; k < kBlock; ++k)
+            v.p[k >> 1][k & 1] = *reinterpret_cast<const T*>(tile + (32 * b + k) * kTilePitch + col * (int)sizeof(T));
         uint32_t byte;
-        const intx4 c = quantize(v, byte);
-        *reinterpret_cast<intx4*>(codes + (j * blocks + b) * 16) = c;
-        scales[j * blocks + b] = (uint8_t)byte;
+        q[i] = quantize(v, byte);
+        cscale[col][b] = (uint8_t)byte;
+        float a = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) a += (float)v.p[k >> 1][k & 1];
+        sum[b][col] = a;
+    }
+    __syncthreads();  // the tile has been read
+    if (o.sums && t < C && c0 + t < s.cols) {
+        float a = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) a += sum[b][t];
+        o.sums[it * s.cols + c0 + t] = a;
+    }
+    if (!o.codes) return;
+    const int64_t b0 = r0 / kBlock;
+#pragma unroll
+    for (int i = 0; i < C / 32; ++i)
+        *reinterpret_cast<intx4*>(tile + ((t % C) * 8 + t / C + (256 / C) * i) * 16) = q[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C / 32; ++i) {
+        const int p = t + 256 * i, col = p >> 3, b = p & 7;
+        if (c0 + col < s.cols && b0 + b < o.blocks) {
+            const int64_t at = (c0 + col) * o.blocks + b0 + b;
+            *reinterpret_cast<intx4*>(o.codes + at * 16) = *reinterpret_cast<const intx4*>(tile + p * 16);
+            o.scales[at] = cscale[col][b];
+        }
     }
 }
 
-// Value 2^(byte - 127) * code, in fp32; a NaN scale gives NaN.
-__device__ __forceinline__ float value_of(uint32_t code, float scale) {
-    const uint32_t m = code & 7u;
-    const float a = m < 4u ? 0.5f * (float)m : (m < 6u ? (float)m - 2.0f : 2.0f * (float)m - 8.0f);
-    return (code & 8u ? -a : a) * scale;
+// Tiles column by column within a run of rows, so that neighbouring blocks
+// read neighbouring lines of a row.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_quantize_tile_kernel(Source<T> s, ColumnOut o) {
+    constexpr int C = 128 / (int)sizeof(T);
+    const int64_t across = (s.cols + C - 1) / C, total = across * ((s.rows + kTileRows - 1) / kTileRows);
+    for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
+        quantize_tile(s, o, k / across, k % across);
+        __syncthreads();
+    }
 }
 
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-    if (byte == (uint32_t)kNaNByte) return __builtin_nanf("");
-    return __builtin_bit_cast(float, byte ? byte << 23 : 0x00400000u);  // 2^-127 is subnormal
+template <int BYTE>
+__device__ __forceinline__ pair_t<float> value_pair(uint32_t codes, float scale, float) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, BYTE);
+}
+template <int BYTE>
+__device__ __forceinline__ pair_t<_Float16> value_pair(uint32_t codes, float scale, _Float16) {
+    const pair_t<float> v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, BYTE);
+    return pair_t<_Float16>{(_Float16)v[0], (_Float16)v[1]};
+}
+template <int BYTE>
+__device__ __forceinline__ pair_t<__bf16> value_pair(uint32_t codes, float scale, __bf16) {
+    const pair_t<float> v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, scale, BYTE);
+    return pair_t<__bf16>{(__bf16)v[0], (__bf16)v[1]};
 }
 
+// One thread per 8 values: a wave reads 256 bytes of codes and writes whole
+// lines.  The conversion to fp32 is exact, then one rounding to T.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
                                                              int64_t rows, int64_t cols, int64_t blocks, T* x,
                                                              int64_t ldx) {
-    const int64_t total = rows * blocks;
+    const int64_t total = rows * blocks * 4;
     for (int64_t base = (int64_t)blockIdx.x * 256; base < total; base += (int64_t)gridDim.x * 256) {
         const int64_t i = base + threadIdx.x;
         if (i >= total) return;
-        const int64_t r = i / blocks, k0 = (i - r * blocks) * kBlock;
-        const intx4 c = *reinterpret_cast<const intx4*>(codes + i * 16);
-        const float s = scale_of(scales[i]);
+        const int64_t block = i >> 2, r = row_of(block, blocks, base >> 2), k0 = (block - r * blocks) * kBlock + 8 * (i & 3);
+        const uint32_t c = reinterpret_cast<const uint32_t*>(codes)[i], byte = scales[block];
+        const float s = __builtin_bit_cast(float, byte << 23);
+        pair_t<T> v[4] = {value_pair<0>(c, s, T()), value_pair<1>(c, s, T()), value_pair<2>(c, s, T()),
+                          value_pair<3>(c, s, T())};
+        if (byte == (uint32_t)kNaNByte) {
+            const T nan = (T)__builtin_nanf("");
+            v[0] = v[1] = v[2] = v[3] = pair_t<T>{nan, nan};
+        }
         T* out = x + r * ldx + k0;
-        T v[kBlock];
-#pragma unroll
-        for (int k = 0; k < kBlock; ++k) v[k] = (T)value_of((uint32_t)c[k >> 3] >> (4 * (k & 7)), s);
-        if (k0 + kBlock <= cols) {
+        if (k0 + 8 <= cols) {
             __builtin_memcpy(out, v, sizeof(v));
         } else {
 #pragma unroll
-            for (int k = 0; k < kBlock; ++k)
-                if (k0 + k < cols) out[k] = v[k];
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < cols) out[k] = v[k >> 1][k & 1];
         }
     }
 }
@@ -480,43 +596,52 @@ __global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
     }
 }
 
-// The splits of a long sum added in order: c = act(sum of part[s] + bias).
+// The splits of a long sum added in a fixed order: c = act(sum of part[s] +
+// bias).  A wave takes every fourth split of 64 neighbouring outputs.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* part, int splits) {
+    __shared__ float sum[4][64];
     const int64_t total = p.M * p.N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / p.N, n = i - m * p.N;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t base = (int64_t)blockIdx.x * 64; base < total; base += (int64_t)gridDim.x * 64) {
+        const int64_t i = base + lane;
         float v = 0.0f;
-        for (int s = 0; s < splits; ++s) v += part[s * total + i];
-        reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
+        if (i < total) {
+#pragma unroll 8
+            for (int s = wave; s < splits; s += 4) v += part[s * total + i];
+        }
+        sum[wave][lane] = v;
+        __syncthreads();
+        if (wave == 0 && i < total) {
+            const int64_t m = i / p.N, n = i - m * p.N;
+            v = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+            reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
+        }
+        __syncthreads();
     }
 }
 
-// ------------------------------------------------------------- bias gradient
+// ------------------------------------------------------------- column sums
 
-constexpr int kSumRows = 1024;  // rows per partial sum
-
-// part[chunk][col]: sums of kSumRows rows, one thread per column.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_colsum_kernel(Source<T> s, float* part) {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (j >= s.cols) return;
-    const int64_t r0 = (int64_t)blockIdx.y * kSumRows, r1 = min(r0 + kSumRows, s.rows);
-    float sum = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        const float v = (float)s.x[r * s.ldx + j];
-        sum += s.y && !((float)s.y[r * s.ldy + j] > 0.0f) ? 0.0f : v;
+// out[col] = sum over the tile rows of part[chunk][col], in double: 16 waves
+// each take every sixteenth chunk of 64 columns.
+__global__ void __launch_bounds__(1024) mx4_column_sums_kernel(const float* part, int64_t chunks, int64_t cols,
+                                                               float* out) {
+    __shared__ double sum[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t j = (int64_t)blockIdx.x * 64 + lane;
+    double a = 0.0;
+    if (j < cols) {
+#pragma unroll 8
+        for (int64_t k = wave; k < chunks; k += 16) a += (double)part[k * cols + j];
     }
-    part[(int64_t)blockIdx.y * s.cols + j] = sum;
-}
-
-__global__ void __launch_bounds__(256) mx4_colsum_finish_kernel(const float* part, int64_t chunks, int64_t cols,
-                                                                float* out) {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (j >= cols) return;
-    double sum = 0.0;
-    for (int64_t k = 0; k < chunks; ++k) sum += (double)part[k * cols + j];
-    out[j] = (float)sum;
+    sum[wave][lane] = a;
+    __syncthreads();
+    if (wave == 0 && j < cols) {
+        a = 0.0;
+        for (int w = 0; w < 16; ++w) a += sum[w][lane];
+        out[j] = (float)a;
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -530,16 +655,22 @@ unsigned grid_for(int64_t threads) {
 }
 
 template <typename T>
-hipError_t quantize_t(const Mx4Source& x, bool transpose, const Mx4View& out, hipStream_t s) {
+hipError_t quantize_rows_t(const Mx4Source& x, const Mx4View& out, hipStream_t s) {
     const Source<T> src{(const T*)x.x, (const T*)x.y, x.rows, x.cols, x.ldx, x.ldy};
     const int64_t blocks = mx4_blocks(out.cols);
     if (out.rows == 0 || blocks == 0) return hipSuccess;
-    if (transpose)
-        IA_LAUNCH("mx4_quantize_cols_kernel", mx4_quantize_cols_kernel<T>, dim3(grid_for(out.rows * blocks)), dim3(256),
-                  0, s, src, blocks, out.codes, out.scales);
-    else
-        IA_LAUNCH("mx4_quantize_rows_kernel", mx4_quantize_rows_kernel<T>, dim3(grid_for(out.rows * blocks)), dim3(256),
-                  0, s, src, blocks, out.codes, out.scales);
+    IA_LAUNCH("mx4_quantize_rows_kernel", mx4_quantize_rows_kernel<T>, dim3(grid_for(out.rows * blocks)), dim3(256), 0, s,
+              src, blocks, out.codes, out.scales);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t quantize_tile_t(const Mx4Source& x, const ColumnOut& o, hipStream_t s) {
+    if (x.rows == 0 || x.cols == 0) return hipSuccess;
+    const Source<T> src{(const T*)x.x, (const T*)x.y, x.rows, x.cols, x.ldx, x.ldy};
+    const int64_t tiles = ceil_div(x.rows, kTileRows) * ceil_div(x.cols, 128 / (int64_t)sizeof(T));
+    IA_LAUNCH("mx4_quantize_tile_kernel", mx4_quantize_tile_kernel<T>, dim3(grid_for(tiles * 256)), dim3(256), 0, s, src,
+              o);
     return hipGetLastError();
 }
 
@@ -547,7 +678,7 @@ template <typename T>
 hipError_t dequantize_t(const Mx4View& q, void* x, int64_t ldx, hipStream_t s) {
     const int64_t blocks = mx4_blocks(q.cols);
     if (q.rows == 0 || blocks == 0) return hipSuccess;
-    IA_LAUNCH("mx4_dequantize_kernel", mx4_dequantize_kernel<T>, dim3(grid_for(q.rows * blocks)), dim3(256), 0, s,
+    IA_LAUNCH("mx4_dequantize_kernel", mx4_dequantize_kernel<T>, dim3(grid_for(q.rows * blocks * 4)), dim3(256), 0, s,
               (const uint8_t*)q.codes, (const uint8_t*)q.scales, q.rows, q.cols, blocks, (T*)x, ldx);
     return hipGetLastError();
 }
@@ -600,24 +731,8 @@ hipError_t matmul_t(MatArgs p, void* ws, hipStream_t s) {
     part.ldc = p.N;
     hipError_t e = launch_tiles<float>(part, plan, s);
     if (e != hipSuccess) return e;
-    IA_LAUNCH("mx4_join_kernel", mx4_join_kernel<T>, dim3(grid_for(p.M * p.N)), dim3(256), 0, s, p, (const float*)ws,
+    IA_LAUNCH("mx4_join_kernel", mx4_join_kernel<T>, dim3(grid_for(p.M * p.N * 4)), dim3(256), 0, s, p, (const float*)ws,
               plan.splits);
-    return hipGetLastError();
-}
-
-template <typename T>
-hipError_t colsum_t(const Mx4Source& x, float* part, float* out, hipStream_t s) {
-    const Source<T> src{(const T*)x.x, (const T*)x.y, x.rows, x.cols, x.ldx, x.ldy};
-    const int64_t chunks = ceil_div(x.rows, kSumRows), cb = ceil_div(x.cols, 256);
-    if (x.cols == 0) return hipSuccess;
-    if (chunks > 0) {
-        IA_LAUNCH("mx4_colsum_kernel", mx4_colsum_kernel<T>, dim3((unsigned)cb, (unsigned)chunks), dim3(256), 0, s, src,
-                  part);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    IA_LAUNCH("mx4_colsum_finish_kernel", mx4_colsum_finish_kernel, dim3((unsigned)cb), dim3(256), 0, s,
-              (const float*)part, chunks, x.cols, out);
     return hipGetLastError();
 }
 
@@ -641,7 +756,9 @@ Mx4View scratch_view(void* at, int64_t rows, int64_t cols) {
 int64_t mx4_blocks(int64_t cols) { return ceil_div(cols, kBlock); }
 
 hipError_t launch_mx4_quantize(const Mx4Source& x, bool transpose, const Mx4View& out, hipStream_t s) {
-    return IA_BY_DTYPE(x.dtype, quantize_t, x, transpose, out, s);
+    if (!transpose) return IA_BY_DTYPE(x.dtype, quantize_rows_t, x, out, s);
+    const ColumnOut o{out.codes, out.scales, mx4_blocks(out.cols), nullptr, nullptr, 0, nullptr};
+    return IA_BY_DTYPE(x.dtype, quantize_tile_t, x, o, s);
 }
 
 hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s) {
@@ -675,7 +792,7 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
 size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
     const size_t x = mx4_matmul_workspace(M, K, N), w = mx4_matmul_workspace(N, K, M);
     return scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
-           round_up((size_t)ceil_div(M, kSumRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
+           round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
 }
 
 hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
@@ -685,18 +802,30 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     const Mx4View dr = scratch_view(at, M, N), dc = scratch_view(at += scratch_bytes(M, N), N, M),
                   xc = scratch_view(at += scratch_bytes(N, M), K, M);
     float* part = (float*)(at += scratch_bytes(K, M));
-    void* mat = at + round_up((size_t)ceil_div(M, kSumRows) * (size_t)N * sizeof(float));
-    hipError_t e = hipSuccess;
+    void* mat = at + round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float));
+    ColumnOut o{};
     if (dx) {
-        e = launch_mx4_quantize(dy, false, dr, s);
-        if (e == hipSuccess) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
+        o.rcodes = dr.codes;
+        o.rscales = dr.scales;
+        o.rblocks = mx4_blocks(N);
     }
+    if (dw) {
+        o.codes = dc.codes;
+        o.scales = dc.scales;
+        o.blocks = mx4_blocks(M);
+    }
+    if (db) o.sums = part;
+    hipError_t e = IA_BY_DTYPE(dy.dtype, quantize_tile_t, dy, o, s);
+    if (e == hipSuccess && dx) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
     if (e == hipSuccess && dw) {
-        e = launch_mx4_quantize(dy, true, dc, s);
-        if (e == hipSuccess) e = launch_mx4_quantize(x, true, xc, s);
+        e = launch_mx4_quantize(x, true, xc, s);
         if (e == hipSuccess) e = launch_mx4_matmul(dc, xc, nullptr, kMx4NoAct, IA_DTYPE_F32, dw, K, mat, s);
     }
-    if (e == hipSuccess && db) e = IA_BY_DTYPE(dy.dtype, colsum_t, dy, part, db, s);
+    if (e == hipSuccess && db && N > 0) {
+        IA_LAUNCH("mx4_column_sums_kernel", mx4_column_sums_kernel, dim3((unsigned)ceil_div(N, 64)), dim3(1024), 0, s,
+                  (const float*)part, ceil_div(M, kTileRows), N, db);
+        e = hipGetLastError();
+    }
     return e;
 }
 
