@@ -383,6 +383,12 @@ __device__ __forceinline__ floatx4 mfma(intx4 a, int as, intx4 b, int bs, floatx
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, BYTE, as, BYTE, bs);
 }
 
+// The first operand's scale in byte BYTE of its word, the second's in the lowest.
+template <int BYTE>
+__device__ __forceinline__ floatx4 mfma_pick(intx4 a, int as, intx4 b, int bs, floatx4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, BYTE, as, 0, bs);
+}
+
 // Tiled product.  A block of 2 x 2 waves computes a tile of 32 WT rows by 32
 // WT columns, a wave 16 WT by 16 WT of it in WT x WT accumulators.  The codes
 // of 8 blocks (256 values, one 128-byte line of a row) of every row pass
@@ -596,6 +602,100 @@ __global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
     }
 }
 
+// ------------------------------------------------------- narrow layers, fused
+
+// act(Q(x) w^T + bias) for layers of up to 256 outputs whose weights fit LDS.
+// A lane's share of the MFMA operand is one block of one row, so a wave
+// quantises 16 rows of x in its registers on the way to the matrix cores: x is
+// read once and only y is written.  Bound by those bytes.
+struct NarrowArgs {
+    const uint8_t* w;   // [N][blocks]
+    const uint8_t* ws;
+    int N, blocks, steps;  // steps of 4 blocks
+    const float* bias;
+    int act;
+    void* y;
+    int64_t ldy;
+};
+
+constexpr int kNarrowUnits = 14;  // 64 outputs x 128 inputs: 4 KiB of codes, 256 B of scales; within 64 KiB
+
+size_t narrow_lds(int groups, int steps) {
+    return (size_t)groups * steps * (4096 + 256) + (size_t)groups * 64 * sizeof(float);
+}
+
+// Column n of register r of n tile j in a group of 64, for lane group q: a
+// lane's 16 values are 16-byte runs, the four lanes of a row side by side.
+template <typename T>
+__device__ __forceinline__ int narrow_column(int j, int q, int r) {
+    constexpr int E = 16 / (int)sizeof(T);
+    const int p = 4 * j + r;
+    return p / E * (4 * E) + q * E + p % E;
+}
+
+template <typename T, int G, bool MASK>
+__global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, NarrowArgs p) {
+    constexpr int NT = 4 * G, E = 16 / (int)sizeof(T);
+    extern __shared__ intx4 shared[];
+    intx4* wc = shared;                                                         // [step][tile][lane]
+    uint8_t* wsc = reinterpret_cast<uint8_t*>(shared + (size_t)p.steps * NT * 64);  // [step][lane][tile]
+    float* sbias = reinterpret_cast<float*>(wsc + (size_t)p.steps * 64 * NT);       // [group][64]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    for (int i = threadIdx.x; i < p.steps * NT * 64; i += 256) {
+        const int l = i & 63, j = (i >> 6) % NT, step = (i >> 6) / NT;
+        const int n = 64 * (j >> 2) + narrow_column<T>(j & 3, (l & 15) >> 2, l & 3), b = 4 * step + (l >> 4);
+        const bool in = n < p.N && b < p.blocks;
+        const int64_t at = (int64_t)n * p.blocks + b;
+        wc[i] = in ? *reinterpret_cast<const intx4*>(p.w + at * 16) : intx4{0, 0, 0, 0};
+        wsc[(step * 64 + l) * NT + j] = in ? p.ws[at] : (uint8_t)0;
+    }
+    for (int n = threadIdx.x; n < 64 * G; n += 256) sbias[n] = p.bias && n < p.N ? p.bias[n] : 0.0f;
+    __syncthreads();
+    T* out = reinterpret_cast<T*>(p.y);
+    for (int64_t m0 = ((int64_t)blockIdx.x * 4 + wave) * 16; m0 < s.rows; m0 += (int64_t)gridDim.x * 64) {
+        const int64_t row = min(m0 + c, s.rows - 1);
+        const T* x = s.x + row * s.ldx;
+        const T* y = s.y + row * s.ldy;
+        floatx4 acc[NT] = {};
+        for (int step = 0; step < p.steps; ++step) {
+            const int64_t k0 = (int64_t)(4 * step + q) * kBlock;
+            Values<T> v = load_values(x, k0, s.cols);
+            if (MASK) mask(v, load_values(y, k0, s.cols));
+            uint32_t xs;
+            const intx4 xc = quantize(v, xs);
+            int sc[G];
+            __builtin_memcpy(sc, wsc + (step * 64 + lane) * NT, NT);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const intx4* w = wc + (step * NT + 4 * g) * 64 + lane;
+                acc[4 * g] = mfma_pick<0>(w[0], sc[g], xc, (int)xs, acc[4 * g]);
+                acc[4 * g + 1] = mfma_pick<1>(w[64], sc[g], xc, (int)xs, acc[4 * g + 1]);
+                acc[4 * g + 2] = mfma_pick<2>(w[128], sc[g], xc, (int)xs, acc[4 * g + 2]);
+                acc[4 * g + 3] = mfma_pick<3>(w[192], sc[g], xc, (int)xs, acc[4 * g + 3]);
+            }
+        }
+        if (m0 + c >= s.rows) continue;
+        T* to = out + (m0 + c) * p.ldy;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int h = 0; h < 16 / E; ++h) {  // runs of 16 bytes
+                const int n = 64 * g + 4 * E * h + E * q;
+                T o[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[e] = (T)activate(acc[4 * g + (E * h + e) / 4][(E * h + e) % 4] + sbias[n + e], p.act);
+                if (n + E <= p.N) {
+                    __builtin_memcpy(to + n, o, sizeof(o));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (n + e < p.N) to[n + e] = o[e];
+                }
+            }
+    }
+}
+
 // The splits of a long sum added in a fixed order: c = act(sum of part[s] +
 // bias).  A wave takes every fourth split of 64 neighbouring outputs.
 template <typename T>
@@ -736,6 +836,36 @@ hipError_t matmul_t(MatArgs p, void* ws, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T, bool MASK>
+hipError_t narrow_linear_masked(const Source<T>& src, const NarrowArgs& p, hipStream_t s) {
+    const int groups = (p.N + 63) / 64;
+    const size_t lds = narrow_lds(groups, p.steps);
+    // each block reads the weights once; as many blocks as fit the CUs
+    const int64_t tiles = ceil_div(src.rows, 64), most = 256 * (int64_t)(163840 / lds < 8 ? 163840 / lds : 8);
+    const dim3 grid((unsigned)(tiles < most ? tiles : most));
+    switch (groups) {
+        case 1:
+            IA_LAUNCH("mx4_narrow_linear_kernel", (mx4_narrow_linear_kernel<T, 1, MASK>), grid, dim3(256), lds, s, src, p);
+            break;
+        case 2:
+            IA_LAUNCH("mx4_narrow_linear_kernel", (mx4_narrow_linear_kernel<T, 2, MASK>), grid, dim3(256), lds, s, src, p);
+            break;
+        case 3:
+            IA_LAUNCH("mx4_narrow_linear_kernel", (mx4_narrow_linear_kernel<T, 3, MASK>), grid, dim3(256), lds, s, src, p);
+            break;
+        default:
+            IA_LAUNCH("mx4_narrow_linear_kernel", (mx4_narrow_linear_kernel<T, 4, MASK>), grid, dim3(256), lds, s, src, p);
+            break;
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t narrow_linear_t(const Mx4Source& x, const NarrowArgs& p, hipStream_t s) {
+    const Source<T> src{(const T*)x.x, (const T*)x.y, x.rows, x.cols, x.ldx, x.ldy};
+    return x.y ? narrow_linear_masked<T, true>(src, p, s) : narrow_linear_masked<T, false>(src, p, s);
+}
+
 #define IA_BY_DTYPE(dtype, fn, ...)                                   \
     ((dtype) == IA_DTYPE_F32   ? fn<float>(__VA_ARGS__)               \
      : (dtype) == IA_DTYPE_F16 ? fn<_Float16>(__VA_ARGS__)            \
@@ -777,12 +907,23 @@ hipError_t launch_mx4_matmul(const Mx4View& a, const Mx4View& b, const float* bi
     return IA_BY_DTYPE(dtype, matmul_t, p, ws, s);
 }
 
+// Whether a layer of K inputs and N outputs goes through the fused kernel.
+bool is_narrow(int64_t K, int64_t N) {
+    return N <= 256 && K > 0 && ceil_div(N, 64) * ceil_div(mx4_blocks(K), 4) <= kNarrowUnits;
+}
+
 size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) {
-    return scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+    return is_narrow(K, N) ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
 }
 
 hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
                              int64_t ldy, void* ws, hipStream_t s) {
+    if (x.rows == 0 || w.rows == 0) return hipSuccess;
+    if (is_narrow(x.cols, w.rows)) {
+        const int64_t blocks = mx4_blocks(x.cols);
+        const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy};
+        return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
+    }
     const Mx4View q = scratch_view(ws, x.rows, x.cols);
     hipError_t e = launch_mx4_quantize(x, false, q, s);
     if (e != hipSuccess) return e;
@@ -804,7 +945,8 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     float* part = (float*)(at += scratch_bytes(K, M));
     void* mat = at + round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float));
     ColumnOut o{};
-    if (dx) {
+    const bool narrow = dx && M > 0 && is_narrow(N, K);  // dx is a layer of N inputs and K outputs on d
+    if (dx && !narrow) {
         o.rcodes = dr.codes;
         o.rscales = dr.scales;
         o.rblocks = mx4_blocks(N);
@@ -816,7 +958,8 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     }
     if (db) o.sums = part;
     hipError_t e = IA_BY_DTYPE(dy.dtype, quantize_tile_t, dy, o, s);
-    if (e == hipSuccess && dx) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
+    if (e == hipSuccess && narrow) e = launch_mx4_linear(dy, wt, nullptr, kMx4NoAct, dx, lddx, nullptr, s);
+    if (e == hipSuccess && dx && !narrow) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
     if (e == hipSuccess && dw) {
         e = launch_mx4_quantize(x, true, xc, s);
         if (e == hipSuccess) e = launch_mx4_matmul(dc, xc, nullptr, kMx4NoAct, IA_DTYPE_F32, dw, K, mat, s);
