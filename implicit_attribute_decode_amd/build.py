@@ -24,13 +24,13 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 
-# Per-source flags.  The decoder MLP kernels (forward, branches, backward) need
+# Per-source flags.  The decoder MLP and MXFP4 product kernels need
 # far fewer than 256 registers per lane, so their MFMA accumulators stay in
 # ordinary VGPRs: with accumulation registers the compiler moves every result
 # out with one v_accvgpr_read before its activation (about a tenth of the
 # backward's VALU instructions).
 EXTRA_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-               for name in ("decode.hip", "decode_branch.hip", "decode_bwd.hip")}
+               for name in ("decode.hip", "decode_branch.hip", "decode_bwd.hip", "mx4.hip")}
 
 
 def sources() -> list[str]:

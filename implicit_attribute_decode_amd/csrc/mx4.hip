@@ -139,6 +139,26 @@ __device__ __forceinline__ Values<T> load_values(const T* row, int64_t k0, int64
     return v;
 }
 
+// The ReLU mask of 16 rows (lanes c) by 128 columns (32 in each lane group q)
+// turned to bits along the rows: bit c of word [column] of `words`.  A
+// comparison's lane mask holds the column 32 q + k of all four q.
+template <typename T>
+__device__ __forceinline__ void store_mask(const Values<T>& y, uint16_t* words, int lane) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int k = 0; k < kBlock; ++k) {
+        const uint64_t b = __ballot((float)y.p[k >> 1][k & 1] > 0.0f);
+        lo = lane == k ? (uint32_t)b : lo;
+        hi = lane == k ? (uint32_t)(b >> 32) : hi;
+    }
+    if (lane < kBlock) {
+        words[lane] = (uint16_t)lo;
+        words[32 + lane] = (uint16_t)(lo >> 16);
+        words[64 + lane] = (uint16_t)hi;
+        words[96 + lane] = (uint16_t)(hi >> 16);
+    }
+}
+
 // v where the matching value of y is above zero, else zero (a ReLU's gradient)
 template <typename T>
 __device__ __forceinline__ void mask(Values<T>& v, const Values<T>& y) {
@@ -402,7 +422,7 @@ __device__ __forceinline__ floatx4 mfma_pick(intx4 a, int as, intx4 b, int bs, f
 // n = 64 (j / 4) + 16 q + 4 (j % 4) + r, so that a lane ends with 16
 // consecutive n of one row m and stores them together.
 //   Rows past the end repeat the last one (their results are not stored).
-// Blocks past the end of a row repeat its last block with scale byte 0 on both
+// Blocks past the end of a row are other rows' codes with scale byte 0 on both
 // sides: such a product is below 2^-240, under half of fp32's smallest value.
 constexpr int kStageBlocks = 8;
 
@@ -412,56 +432,41 @@ __device__ __forceinline__ int key_b(int row) { return (row & 3) | ((row >> 2) &
 // LDS row (within a wave's n rows) of lane c's row of n tile j.
 __device__ __forceinline__ int n_row(int j, int c) { return 64 * (j >> 2) + 16 * (c >> 2) + 4 * (j & 3) + (c & 3); }
 
-// The rows of one operand's tile: byte offsets of the lanes' rows from the
-// tile's first row, and the copies of their stages into LDS.  OFF is 32 bits
-// wide in the large tile, where registers are short (rows below 2^24 bytes).
-template <int ROWS, bool B, typename OFF>
+// The copies of one operand's tile rows into LDS: a uniform base that follows
+// the stages, and 32-bit lane offsets (a tile's rows span less than 2^32
+// bytes).  Blocks past the end of a row are the next row's, or for the last
+// row the operand's last block.
+template <int ROWS, int WAVES, bool B>
 struct Codes {
+    static constexpr int N = ROWS / 8 / WAVES;  // copies of 8 rows a wave
     const uint8_t* base;  // first block of the tile's first row
-    int blocks;
-    OFF row[ROWS / 32];
-    int slot;  // the block of a stage that this lane copies
+    int64_t bytes;        // from there to the operand's end, less one block
+    uint32_t off[N];
 
-    __device__ __forceinline__ Codes(const uint8_t* codes, int64_t row0, int64_t rows, int64_t nblocks, int wave,
+    __device__ __forceinline__ Codes(const uint8_t* codes, int64_t row0, int64_t rows, int64_t blocks, int wave,
                                      int lane) {
-        base = codes + row0 * nblocks * 16;
-        blocks = (int)nblocks;
+        base = codes + row0 * blocks * 16;
+        bytes = (rows - row0) * blocks * 16 - 16;
         const int64_t last = rows - 1 - row0;
+        // key_b takes bit 4 of the row, which is the same for the wave's rows
+        const int r = 8 * wave + (lane >> 3), slot = (lane & 7) ^ (B ? key_b(r) : key_a(r));
 #pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i)
-            row[i] = (OFF)(min((int64_t)(32 * i + 8 * wave + (lane >> 3)), last) * nblocks * 16);
-        const int r = 8 * wave + (lane >> 3);
-        slot = (lane & 7) ^ (B ? key_b(r) : key_a(r));
+        for (int i = 0; i < N; ++i)
+            off[i] = (uint32_t)(min((int64_t)(8 * WAVES * i + r), last) * blocks * 16) + (uint32_t)slot * 16u;
     }
 
     // blocks 8 t .. 8 t + 7
     __device__ __forceinline__ void copy(intx4* buf, int t, int wave) const {
-        const uint8_t* at = base + min(t * kStageBlocks + slot, blocks - 1) * (int64_t)16;
+        const int64_t skip = (int64_t)t * (kStageBlocks * 16), left = bytes - skip;
+        const uint8_t* at = base + skip;
+        const uint32_t most = (uint32_t)min(max(left, (int64_t)0), (int64_t)0xffffffff);
 #pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i)
-            // key_b takes bit 4 of the row, which is the same for rows 32 apart
-            __builtin_amdgcn_global_load_lds((const void*)(at + row[i]),
-                                             (__attribute__((address_space(3))) void*)(buf + (4 * i + wave) * 64), 16,
-                                             0, 0);
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_global_load_lds((const void*)(at + min(off[i], most)),
+                                             (__attribute__((address_space(3))) void*)(buf + (WAVES * i + wave) * 64),
+                                             16, 0, 0);
     }
 };
-
-// Scale bytes k0 .. k0 + 15 of a row, zero past its end.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int k0, int blocks) {
-    uint4 v;
-    if (k0 + 16 <= blocks) {
-        __builtin_memcpy(&v, row + k0, 16);
-        return v;
-    }
-    uint64_t w[2] = {0, 0};
-#pragma unroll 1
-    for (int i = 0; i < 16 && k0 + i < blocks; ++i) {
-        const uint64_t byte = (uint64_t)row[k0 + i] << (8 * (i & 7));
-        w[0] |= i < 8 ? byte : 0;
-        w[1] |= i < 8 ? 0 : byte;
-    }
-    return make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
-}
 
 // Byte matrix [4][4] (word = row) transposed.
 __device__ __forceinline__ uint4 transpose4(uint4 v) {
@@ -471,27 +476,88 @@ __device__ __forceinline__ uint4 transpose4(uint4 v) {
                       __builtin_amdgcn_perm(hi2, lo2, 0x05040100u), __builtin_amdgcn_perm(hi2, lo2, 0x07060302u));
 }
 
-template <int WT, int HALF>
-__device__ __forceinline__ void multiply_stage(const intx4* la, const intx4* lb, const int (&sa)[WT],
-                                               const int (&sb)[WT], int wm, int wn, int q, int c,
-                                               floatx4 (&acc)[WT][WT]) {
+// Scale bytes of one row of a tile.
+struct ScaleRow {
+    const uint8_t* base;  // uniform: the tile's first row
+    uint32_t off;
+    int64_t left;  // bytes from base to the operand's end
+    int blocks;
+
+    __device__ __forceinline__ ScaleRow(const uint8_t* scales, int64_t row0, int64_t rows, int64_t nblocks, int row) {
+        base = scales + row0 * nblocks;
+        off = (uint32_t)(min((int64_t)row, rows - 1 - row0) * nblocks);
+        left = (rows - row0) * nblocks;
+        blocks = (int)nblocks;
+    }
+
+    // Bytes k0 .. k0 + 15 of the row: one 16-byte load, from before its place
+    // where it would pass the operand's end (finish() shifts it).  An operand
+    // with less than 16 bytes left is read byte by byte (only with k0 = 0).
+    __device__ __forceinline__ uint4 load(int k0) const {
+        uint64_t v[2] = {0, 0};
+        if (k0 >= blocks) {
+        } else if (left < 16) {
+#pragma unroll 1
+            for (int i = 0; i < blocks; ++i) {
+                const uint64_t byte = (uint64_t)base[off + (uint32_t)i] << (8 * (i & 7));
+                v[0] |= i < 8 ? byte : 0;
+                v[1] |= i < 8 ? 0 : byte;
+            }
+        } else {
+            const int64_t room = left - 16 - k0;
+            __builtin_memcpy(v, base + k0 + min(room, (int64_t)0) + min(off, most(room)), 16);
+        }
+        return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
+    }
+
+    // The loaded bytes in their places, zero past the row's end, transposed.
+    __device__ __forceinline__ uint4 finish(uint4 w, int k0) const {
+        uint64_t v[2] = {(uint64_t)w.y << 32 | w.x, (uint64_t)w.w << 32 | w.z};
+        if (left >= 16) {
+            const int64_t room = left - 16 - k0;
+            const uint32_t s = 8 * (off - min(off, most(room)) - (uint32_t)min(room, (int64_t)0)) & 127u;
+            const uint64_t up = (v[1] << 1) << (63 - (s & 63));
+            v[0] = s < 64 ? v[0] >> s | up : v[1] >> (s & 63);
+            v[1] = s < 64 ? v[1] >> s : 0;
+        }
+        const int n = max(blocks - k0, 0);  // uniform
+        v[0] &= n < 8 ? ((uint64_t)1 << (8 * n)) - 1 : ~(uint64_t)0;
+        v[1] &= n < 16 ? ((uint64_t)1 << (8 * max(n - 8, 0))) - 1 : ~(uint64_t)0;
+        return transpose4(make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)));
+    }
+
+    static __device__ __forceinline__ uint32_t most(int64_t room) {
+        return (uint32_t)min(max(room, (int64_t)0), (int64_t)0xffffffff);
+    }
+};
+
+template <int TM, int TN, int HALF>
+__device__ __forceinline__ void multiply_stage(const intx4* la, const intx4* lb, const int (&sa)[TM],
+                                               const int (&sb)[TN], int wm, int wn, int q, int c,
+                                               floatx4 (&acc)[TM][TN]) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         const int slot = (4 * ks + q) ^ (c & 7);
-        intx4 a[WT], b[WT];
+        intx4 a[TM], b[TN];
 #pragma unroll
-        for (int i = 0; i < WT; ++i) {
-            a[i] = la[(wm + 16 * i + c) * 8 + slot];
-            b[i] = lb[(wn + n_row(i, c)) * 8 + slot];
-        }
+        for (int i = 0; i < TM; ++i) a[i] = la[(wm + 16 * i + c) * 8 + slot];
 #pragma unroll
-        for (int i = 0; i < WT; ++i)
+        for (int j = 0; j < TN; ++j) b[j] = lb[(wn + n_row(j, c)) * 8 + slot];
 #pragma unroll
-            for (int j = 0; j < WT; ++j) {
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
                 acc[i][j] = ks == 0 ? mfma<2 * HALF>(b[j], sb[j], a[i], sa[i], acc[i][j])
                                     : mfma<2 * HALF + 1>(b[j], sb[j], a[i], sa[i], acc[i][j]);
             }
+        __builtin_amdgcn_sched_barrier(0);
     }
+    // the sums exist here: left to the compiler, the products of both stages
+    // sink behind the second one's barrier
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
 // 16 consecutive values of one output row from column n on.
@@ -520,35 +586,32 @@ __device__ __forceinline__ void tile_of(int64_t b, int64_t tm, int64_t tn, int64
     in = t / h;
 }
 
-template <typename T, int WT>
-__global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
-    constexpr int R = 32 * WT;  // tile rows
+template <typename T, int R, int WAVES_M, int WAVES_N>
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) mx4_matmul_kernel(MatArgs p) {
+    constexpr int WAVES = WAVES_M * WAVES_N, TM = R / WAVES_M / 16, TN = R / WAVES_N / 16;
     __shared__ intx4 a0[R * 8], a1[R * 8], b0[R * 8], b1[R * 8];
-    __shared__ uint4 sca[2][R], scb[2][R];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    __shared__ uint4 scales[2][2 * R];  // the rows of a, then of b
+    static_assert(64 * WAVES == 2 * R, "a thread for every row's scales");
+    const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t im, in;
     tile_of(blockIdx.x, p.tiles_m, p.tiles_n, im, in);
     const int64_t m0 = im * R, n0 = in * R;
-    const int wm = (wave & 1) * 16 * WT, wn = (wave >> 1) * 16 * WT;
+    const int wm = wave % WAVES_M * 16 * TM, wn = wave / WAVES_M * 16 * TN;
     const int blocks = (int)p.blocks;
     const int t0 = (int)(blockIdx.y * p.stages), t1 = min(t0 + (int)p.stages, (blocks + kStageBlocks - 1) / kStageBlocks);
-    typedef typename std::conditional<WT == 8, uint32_t, int64_t>::type Off;
-    const Codes<R, false, Off> ca(p.a, m0, p.M, p.blocks, wave, lane);
-    const Codes<R, true, Off> cb(p.b, n0, p.N, p.blocks, wave, lane);
-    const bool scaler = (int)threadIdx.x < R;
-    const uint8_t* rsa = p.as + min(m0 + (int)(threadIdx.x % R), p.M - 1) * p.blocks;
-    const uint8_t* rsb = p.bs + min(n0 + (int)(threadIdx.x % R), p.N - 1) * p.blocks;
-    floatx4 acc[WT][WT] = {};
+    const Codes<R, WAVES, false> ca(p.a, m0, p.M, p.blocks, wave, lane);
+    const Codes<R, WAVES, true> cb(p.b, n0, p.N, p.blocks, wave, lane);
+    const bool of_a = wave < WAVES / 2;
+    const ScaleRow row(of_a ? p.as : p.bs, of_a ? m0 : n0, of_a ? p.M : p.N, p.blocks, (int)threadIdx.x % R);
+    floatx4 acc[TM][TN] = {};
 
     // Stages go in pairs that share a group of scales; the missing second half
     // of a last pair has zero scales.
     if (t0 < t1) {
         ca.copy(a0, t0, wave);
         cb.copy(b0, t0, wave);
-        if (scaler) {
-            sca[0][threadIdx.x] = transpose4(load_scales(rsa, t0 * kStageBlocks, blocks));
-            scb[0][threadIdx.x] = transpose4(load_scales(rsb, t0 * kStageBlocks, blocks));
-        }
+        scales[0][threadIdx.x] = row.finish(row.load(t0 * kStageBlocks), t0 * kStageBlocks);
     }
     int buf = 0;
     for (int t = t0; t < t1; t += 2, buf ^= 1) {
@@ -556,42 +619,34 @@ __global__ void __launch_bounds__(256) mx4_matmul_kernel(MatArgs p) {
         // wave has read the other buffers for the last time
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        uint4 na = {0, 0, 0, 0}, nb = {0, 0, 0, 0};
-        if (scaler) {
-            na = load_scales(rsa, (t + 2) * kStageBlocks, blocks);
-            nb = load_scales(rsb, (t + 2) * kStageBlocks, blocks);
-        }
+        const uint4 next = row.load((t + 2) * kStageBlocks);
         ca.copy(a1, t + 1, wave);
         cb.copy(b1, t + 1, wave);
-        int sa[WT], sb[WT];
+        int sa[TM], sb[TN];
 #pragma unroll
-        for (int i = 0; i < WT; ++i) {
-            sa[i] = reinterpret_cast<const int*>(&sca[buf][wm + 16 * i + c])[q];
-            sb[i] = reinterpret_cast<const int*>(&scb[buf][wn + n_row(i, c)])[q];
-        }
-        multiply_stage<WT, 0>(a0, b0, sa, sb, wm, wn, q, c, acc);
-        if (scaler) {
-            sca[buf ^ 1][threadIdx.x] = transpose4(na);
-            scb[buf ^ 1][threadIdx.x] = transpose4(nb);
-        }
+        for (int i = 0; i < TM; ++i) sa[i] = reinterpret_cast<const int*>(&scales[buf][wm + 16 * i + c])[q];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sb[j] = reinterpret_cast<const int*>(&scales[buf][R + wn + n_row(j, c)])[q];
+        multiply_stage<TM, TN, 0>(a0, b0, sa, sb, wm, wn, q, c, acc);
+        scales[buf ^ 1][threadIdx.x] = row.finish(next, (t + 2) * kStageBlocks);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         if (t + 2 < t1) {
             ca.copy(a0, t + 2, wave);
             cb.copy(b0, t + 2, wave);
         }
-        multiply_stage<WT, 1>(a1, b1, sa, sb, wm, wn, q, c, acc);
+        multiply_stage<TM, TN, 1>(a1, b1, sa, sb, wm, wn, q, c, acc);
     }
     T* out = reinterpret_cast<T*>(p.c) + (int64_t)blockIdx.y * p.M * p.N;
 #pragma unroll
-    for (int g = 0; g < WT / 4; ++g) {
+    for (int g = 0; g < TN / 4; ++g) {
         const int64_t n = n0 + wn + 64 * g + 16 * q;
         if (n >= p.N) continue;
         float bias[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) bias[k] = p.bias ? p.bias[min(n + k, p.N - 1)] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < WT; ++i) {
+        for (int i = 0; i < TM; ++i) {
             const int64_t m = m0 + wm + 16 * i + c;
             if (m >= p.M) continue;
             float v[16];
@@ -616,6 +671,7 @@ struct NarrowArgs {
     int act;
     void* y;
     int64_t ldy;
+    uint16_t* bits;     // with a mask: [rows / 16][128 steps] words of store_mask, or null
 };
 
 constexpr int kNarrowUnits = 14;  // 64 outputs x 128 inputs: 4 KiB of codes, 256 B of scales; within 64 KiB
@@ -660,7 +716,11 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
         for (int step = 0; step < p.steps; ++step) {
             const int64_t k0 = (int64_t)(4 * step + q) * kBlock;
             Values<T> v = load_values(x, k0, s.cols);
-            if (MASK) mask(v, load_values(y, k0, s.cols));
+            if (MASK) {
+                const Values<T> r = load_values(y, k0, s.cols);
+                if (p.bits) store_mask(r, p.bits + ((m0 >> 4) * p.steps + step) * 128, lane);
+                mask(v, r);
+            }
             uint32_t xs;
             const intx4 xc = quantize(v, xs);
             int sc[G];
@@ -693,6 +753,270 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
                         if (n + e < p.N) to[n + e] = o[e];
                 }
             }
+    }
+}
+
+// The mask words alone, for a backward that needs no input gradient.
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_mask_kernel(Source<T> s, int steps, uint16_t* bits) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    const int64_t total = (s.rows + 15) / 16 * steps;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + wave; i < total; i += (int64_t)gridDim.x * 4) {
+        const int64_t m = i / steps * 16 + c;
+        const int step = (int)(i % steps);
+        store_mask(load_values(s.y + min(m, s.rows - 1) * s.ldy, (int64_t)(4 * step + q) * kBlock, s.cols),
+                   bits + i * 128, lane);
+    }
+}
+
+// dw = Qc(d)^T Qc(x) and db = column sums of d for up to 256 x 256 weights:
+// both matrices are read once and quantised along their rows m in registers.
+// A block of 8 waves takes a run of rows in steps of 128.  The columns are cut
+// into panels of 16 lanes x 8 bytes (64 columns, 32 in fp32); in a step each
+// wave loads its panels, lane (q, c) the rows 32 q .. 32 q + 31 of its 8
+// bytes, which hold 4 (2) whole blocks, one for each of 4 (2) MFMA tiles whose
+// row c is the lane's column.  The codes meet in LDS (two buffers, one barrier
+// a step); wave w multiplies the n tiles 2 w, 2 w + 1 with every k tile.  The
+// next step's loads are in flight meanwhile.  The blocks' sums go to `part` in
+// register order and are added in a fixed order by mx4_narrow_join_kernel.
+// Bound by the bytes of d and x.
+template <typename T>
+struct NarrowGradArgs {
+    const T* d;
+    int64_t ldd;
+    const uint16_t* bits;  // mask words, `words` to a group of 16 rows, or null
+    int64_t words;
+    const T* x;
+    int64_t ldx;
+    int64_t M, run;  // rows, rows a block takes
+    int N, K;
+    floatx4* part;  // [block][n tile][k tile][lane]
+    float* sums;    // [block][N]
+};
+
+constexpr int kGradRows = 128;
+constexpr int kGradTiles = 32;  // n and k tiles of 16 columns
+
+// A lane's share of a panel: 32 rows of 8 bytes, as words.
+template <typename T>
+struct Panel {
+    static constexpr int E = 8 / (int)sizeof(T), COLS = 16 * E;
+    uint32_t w[kBlock][2];
+    uint32_t bits[2][E / 2];  // mask words of rows 0..15 and 16..31
+};
+
+// Rows row0 + 32 q + k of the lane's columns, zero from row `end` and column
+// `cols` on.  The rows' addresses are uniform, the lane adds 32 bits: `ld` is
+// below kMaxGradStride.  A piece that crosses the last column is read from 8
+// bytes before the row's end and shifted (cols is at least 8 bytes' worth).
+constexpr int64_t kMaxGradStride = 1 << 22;
+
+template <typename T>
+__device__ __forceinline__ void load_panel(Panel<T>& v, const T* m, int64_t ld, int cols, int panel, int q, int c,
+                                           int64_t row0, int64_t end) {
+    constexpr int E = Panel<T>::E, COLS = Panel<T>::COLS;
+    const int col = panel * COLS + E * c, from = min(col, cols - E);
+    const char* base = reinterpret_cast<const char*>(m + row0 * ld);
+    const int64_t pitch = ld * (int64_t)sizeof(T);
+    if (row0 + kGradRows <= end) {
+        // the offset is opaque: else 32 loop-invariant addresses take 64 registers
+        uint32_t off = (uint32_t)((32 * q * (int)ld + from) * (int)sizeof(T));
+        asm volatile("" : "+v"(off));
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) __builtin_memcpy(v.w[k], base + k * pitch + off, 8);
+    } else {
+        const int last = (int)(end - row0) - 1;
+        int r = 32 * q;
+        asm volatile("" : "+v"(r));
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) {
+            const uint32_t off = (uint32_t)((min(r + k, last) * (int)ld + from) * (int)sizeof(T));
+            uint32_t w[2];
+            __builtin_memcpy(w, base + off, 8);
+            const uint32_t keep = (uint32_t)((r + k - last - 1) >> 31);
+            v.w[k][0] = w[0] & keep;
+            v.w[k][1] = w[1] & keep;
+        }
+    }
+}
+
+// The columns of a piece that load_panel read from before its place.
+template <typename T>
+__device__ __forceinline__ void shift_panel(Panel<T>& v, int cols, int panel, int c) {
+    constexpr int E = Panel<T>::E, COLS = Panel<T>::COLS;
+    if ((panel + 1) * COLS <= cols) return;
+    const int col = panel * COLS + E * c, shift = (col - min(col, cols - E)) * 8 * (int)sizeof(T);
+#pragma unroll
+    for (int k = 0; k < kBlock; ++k) {
+        const uint64_t w = ((uint64_t)v.w[k][1] << 32 | v.w[k][0]) >> (shift & 63);
+        v.w[k][0] = shift < 64 ? (uint32_t)w : 0u;
+        v.w[k][1] = shift < 64 ? (uint32_t)(w >> 32) : 0u;
+    }
+}
+
+// The mask words of the lane's columns (`words` to a group of 16 rows; a
+// multiple of 128, so the piece is whole; past the last row or column any
+// words will do, the values there are zero).
+template <typename T>
+__device__ __forceinline__ void load_bits(Panel<T>& v, const uint16_t* bits, int64_t words, int col, int64_t r0,
+                                          int64_t end) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t group = min(r0 / 16 + i, (end - 1) / 16);
+        __builtin_memcpy(v.bits[i], bits + group * words + min(col, (int)words - Panel<T>::E), sizeof(v.bits[i]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mask_bits(const Panel<T>& v, int e) {
+    return __builtin_amdgcn_perm(v.bits[1][e >> 1], v.bits[0][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+}
+
+// Rows 2 i, 2 i + 1 of column e.
+__device__ __forceinline__ pair_t<float> panel_pair(const Panel<float>& v, int i, int e) {
+    return pair_t<float>{__builtin_bit_cast(float, v.w[2 * i][e]), __builtin_bit_cast(float, v.w[2 * i + 1][e])};
+}
+template <typename T>
+__device__ __forceinline__ pair_t<T> panel_pair(const Panel<T>& v, int i, int e) {
+    return __builtin_bit_cast(pair_t<T>, __builtin_amdgcn_perm(v.w[2 * i + 1][e >> 1], v.w[2 * i][e >> 1],
+                                                               e & 1 ? 0x07060302u : 0x05040100u));
+}
+// The pair where its bits 2 i, 2 i + 1 of m are set, else zero.
+__device__ __forceinline__ pair_t<float> keep_pair(pair_t<float> v, uint32_t m, int i) {
+    return pair_t<float>{m >> (2 * i) & 1u ? v[0] : 0.0f, m >> (2 * i + 1) & 1u ? v[1] : 0.0f};
+}
+template <typename T>
+__device__ __forceinline__ T keep_pair(T v, uint32_t m, int i) {
+    const uint32_t lo = (uint32_t)((int32_t)(m << (31 - 2 * i)) >> 31), hi = (uint32_t)((int32_t)(m << (30 - 2 * i)) >> 31);
+    return __builtin_bit_cast(T, __builtin_bit_cast(uint32_t, v) & ((lo & 0xffffu) | (hi & 0xffff0000u)));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> p) {
+    constexpr int E = Panel<T>::E, COLS = Panel<T>::COLS, SUBS = kGradTiles / E / 8;  // panels a wave takes
+    __shared__ intx4 codes[2][kGradTiles][64];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[2][64][kGradTiles];
+    const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int np = (p.N + COLS - 1) / COLS, kp = (p.K + COLS - 1) / COLS, tn = np * E, tk = kp * E;
+    const int64_t begin = (int64_t)blockIdx.x * p.run, end = min(begin + p.run, p.M);
+    floatx4 acc[2][16] = {};
+    float sum[SUBS][E] = {};
+    Panel<T> v;
+    const int64_t steps = (end - begin + kGradRows - 1) / kGradRows;
+    auto load = [&](int64_t step, int sub) {  // panels from np on are x's
+        const int all = wave * SUBS + sub;
+        if (all >= np + kp) return;
+        const bool of_d = all < np;
+        const int panel = of_d ? all : all - np;
+        const int64_t row0 = begin + step * kGradRows;
+        load_panel(v, of_d ? p.d : p.x, of_d ? p.ldd : p.ldx, of_d ? p.N : p.K, panel, q, c, row0, end);
+        if (of_d && p.bits) load_bits(v, p.bits, p.words, panel * COLS + E * c, row0 + 32 * q, end);
+    };
+    if (steps > 0) load(0, 0);
+    for (int64_t step = 0; step < steps; ++step) {
+        const int buf = (int)(step & 1);
+#pragma unroll
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const int panel = wave * SUBS + sub;
+            if (panel < np + kp) {
+                uint32_t bytes = 0;
+                shift_panel(v, panel < np ? p.N : p.K, panel < np ? panel : panel - np, c);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    Values<T> b;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) b.p[i] = panel_pair(v, i, e);
+                    if (panel < np) {
+                        if (p.bits) {
+                            const uint32_t m = mask_bits(v, e);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) b.p[i] = keep_pair(b.p[i], m, i);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kBlock; ++k) sum[sub][e] += (float)b.p[k >> 1][k & 1];
+                    }
+                    uint32_t byte;
+                    codes[buf][panel * E + e][lane] = quantize(b, byte);
+                    bytes |= byte << (8 * e);
+                    __builtin_amdgcn_sched_barrier(0);  // one column's temporaries at a time
+                }
+                __builtin_memcpy(&scales[buf][lane][panel * E], &bytes, E);
+            }
+            if (sub + 1 < SUBS)
+                load(step, sub + 1);
+            else if (step + 1 < steps)
+                load(step + 1, 0);
+        }
+        __syncthreads();
+        if (2 * wave < tn) {
+            const intx4 d0 = codes[buf][2 * wave][lane], d1 = codes[buf][2 * wave + 1][lane];
+            const int s0 = scales[buf][lane][2 * wave], s1 = scales[buf][lane][2 * wave + 1];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (k < tk) {
+                    const intx4 xc = codes[buf][tn + k][lane];
+                    const int xs = scales[buf][lane][tn + k];
+                    acc[0][k] = mfma_pick<0>(xc, xs, d0, s0, acc[0][k]);
+                    acc[1][k] = mfma_pick<0>(xc, xs, d1, s1, acc[1][k]);
+                }
+        }
+    }
+    if (2 * wave < tn) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (k < tk) p.part[(((int64_t)blockIdx.x * tn + 2 * wave + h) * tk + k) * 64 + lane] = acc[h][k];
+    }
+    if (!p.sums) return;
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float a = sum[sub][e];
+            a += __shfl_xor(a, 16, 64);
+            a += __shfl_xor(a, 32, 64);
+            const int n = (wave * SUBS + sub) * COLS + E * c + e;
+            if (q == 0 && wave * SUBS + sub < np && n < p.N) p.sums[(int64_t)blockIdx.x * p.N + n] = a;
+        }
+}
+
+// The blocks' sums added in a fixed order, 16 waves each taking every
+// sixteenth.  Blocks below tn tk join one tile of dw, the others 64 columns of
+// db (in double).
+template <int E>
+__global__ void __launch_bounds__(1024) mx4_narrow_join_kernel(const floatx4* part, const float* sums, int blocks,
+                                                               int tn, int tk, int N, int K, float* dw, float* db) {
+    __shared__ floatx4 tile[16][64];
+    __shared__ double column[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    if ((int)blockIdx.x < tn * tk) {
+        const int nt = blockIdx.x / tk, kt = blockIdx.x % tk;
+        floatx4 a = {0, 0, 0, 0};
+#pragma unroll 8
+        for (int b = wave; b < blocks; b += 16) a += part[((int64_t)b * tn * tk + blockIdx.x) * 64 + lane];
+        tile[wave][lane] = a;
+        __syncthreads();
+        if (wave != 0) return;
+        for (int w = 1; w < 16; ++w) a += tile[w][lane];
+        const int n = nt / E * (16 * E) + E * c + nt % E;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int k = kt / E * (16 * E) + E * (4 * q + r) + kt % E;
+            if (n < N && k < K) dw[(int64_t)n * K + k] = a[r];
+        }
+    } else {
+        const int n = ((int)blockIdx.x - tn * tk) * 64 + lane;
+        double a = 0.0;
+        if (n < N) {
+#pragma unroll 8
+            for (int b = wave; b < blocks; b += 16) a += (double)sums[(int64_t)b * N + n];
+        }
+        column[wave][lane] = a;
+        __syncthreads();
+        if (wave != 0 || n >= N) return;
+        for (int w = 1; w < 16; ++w) a += column[w][lane];
+        db[n] = (float)a;
     }
 }
 
@@ -787,15 +1111,15 @@ hipError_t dequantize_t(const Mx4View& q, void* x, int64_t ldx, hipStream_t s) {
 // of 128 x 128, and when those are few the sum over k in up to `splits` parts
 // of at least 4 stages (1,024 values) each, joined in order.
 struct MatPlan {
-    int wt;
+    int tile;
     int64_t tiles_m, tiles_n, stages;
     int splits;
 };
 MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
     MatPlan p{};
-    p.wt = ceil_div(M, 256) * ceil_div(N, 256) >= 192 && blocks < (int64_t)1 << 20 ? 8 : 4;
-    p.tiles_m = ceil_div(M, 32 * p.wt);
-    p.tiles_n = ceil_div(N, 32 * p.wt);
+    p.tile = ceil_div(M, 256) * ceil_div(N, 256) >= 192 && blocks < (int64_t)1 << 19 ? 256 : 128;
+    p.tiles_m = ceil_div(M, p.tile);
+    p.tiles_n = ceil_div(N, p.tile);
     const int64_t all = ceil_div(blocks, kStageBlocks), tiles = p.tiles_m * p.tiles_n;
     int64_t splits = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
     if (splits > all / 4) splits = all / 4;
@@ -810,10 +1134,10 @@ MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
 template <typename T>
 hipError_t launch_tiles(const MatArgs& p, const MatPlan& plan, hipStream_t s) {
     const dim3 grid((unsigned)(plan.tiles_m * plan.tiles_n), (unsigned)plan.splits);
-    if (plan.wt == 8)
-        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 8>), grid, dim3(256), 0, s, p);
+    if (plan.tile == 256)
+        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 256, 4, 2>), grid, dim3(512), 0, s, p);
     else
-        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 4>), grid, dim3(256), 0, s, p);
+        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 128, 2, 2>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -864,6 +1188,71 @@ template <typename T>
 hipError_t narrow_linear_t(const Mx4Source& x, const NarrowArgs& p, hipStream_t s) {
     const Source<T> src{(const T*)x.x, (const T*)x.y, x.rows, x.cols, x.ldx, x.ldy};
     return x.y ? narrow_linear_masked<T, true>(src, p, s) : narrow_linear_masked<T, false>(src, p, s);
+}
+
+// Blocks and rows a block takes of a narrow gradient: one block a CU, whole
+// blocks of 32 rows.
+constexpr int64_t kGradBlocks = 256;
+struct GradPlan {
+    int64_t run, blocks;
+    int tn, tk;  // tiles
+};
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, size_t es) {
+    GradPlan g;
+    g.run = ceil_div(ceil_div(M, kGradBlocks), kBlock) * kBlock;
+    if (g.run < kGradRows) g.run = kGradRows;
+    g.blocks = ceil_div(M, g.run);
+    const int64_t e = 8 / (int64_t)es, cols = 16 * e;
+    g.tn = (int)(ceil_div(N, cols) * e);
+    g.tk = (int)(ceil_div(K, cols) * e);
+    return g;
+}
+
+// Scratch of a narrow gradient: mask words, tiles, column sums.
+struct GradScratch {
+    size_t bits, part, sums, total;
+};
+GradScratch grad_scratch(int64_t M, int64_t N, const GradPlan& g) {
+    GradScratch s;
+    s.bits = 0;
+    s.part = round_up((size_t)ceil_div(M, 16) * (size_t)ceil_div(N, 128) * 256);
+    s.sums = s.part + round_up((size_t)g.blocks * g.tn * g.tk * 64 * sizeof(floatx4));
+    s.total = s.sums + round_up((size_t)g.blocks * (size_t)N * sizeof(float));
+    return s;
+}
+
+template <typename T>
+hipError_t narrow_grad_t(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx, float* dw,
+                         float* db, void* ws, hipStream_t s) {
+    const int64_t M = dy.rows, N = dy.cols, K = x.cols, blocks = mx4_blocks(N);
+    const GradPlan g = grad_plan(M, N, K, sizeof(T));
+    const GradScratch at = grad_scratch(M, N, g);
+    const int steps = (int)ceil_div(blocks, 4);
+    const Source<T> src{(const T*)dy.x, (const T*)dy.y, M, N, dy.ldx, dy.ldy};
+    uint16_t* bits = dy.y && (dw || db) ? (uint16_t*)((char*)ws + at.bits) : nullptr;
+    hipError_t e = hipSuccess;
+    if (dx) {
+        const NarrowArgs p{wt.codes, wt.scales, (int)K, (int)blocks, steps, nullptr, IA_ACT_NONE, dx, lddx, bits};
+        e = narrow_linear_t<T>(dy, p, s);
+    } else if (bits) {
+        IA_LAUNCH("mx4_mask_kernel", mx4_mask_kernel<T>, dim3(grid_for(ceil_div(M, 16) * steps * 64)), dim3(256), 0, s,
+                  src, steps, bits);
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess || !(dw || db)) return e;
+    floatx4* part = (floatx4*)((char*)ws + at.part);
+    float* sums = db ? (float*)((char*)ws + at.sums) : nullptr;
+    const NarrowGradArgs<T> p{src.x, src.ldx, bits, steps * 128, (const T*)x.x, x.ldx, M, g.run, (int)N,
+                              dw ? (int)K : 0, part, sums};
+    const int tk = dw ? g.tk : 0;
+    IA_LAUNCH("mx4_narrow_grad_kernel", mx4_narrow_grad_kernel<T>, dim3((unsigned)g.blocks), dim3(512), 0, s, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    constexpr int E = Panel<T>::E;
+    const int columns = db ? (int)ceil_div(N, 64) : 0;
+    IA_LAUNCH("mx4_narrow_join_kernel", mx4_narrow_join_kernel<E>, dim3((unsigned)(g.tn * tk + columns)), dim3(1024), 0,
+              s, (const floatx4*)part, (const float*)sums, (int)g.blocks, g.tn, tk, (int)N, (int)K, dw, db);
+    return hipGetLastError();
 }
 
 #define IA_BY_DTYPE(dtype, fn, ...)                                   \
@@ -921,7 +1310,8 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
     if (x.rows == 0 || w.rows == 0) return hipSuccess;
     if (is_narrow(x.cols, w.rows)) {
         const int64_t blocks = mx4_blocks(x.cols);
-        const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy};
+        const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy,
+                           nullptr};
         return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
     }
     const Mx4View q = scratch_view(ws, x.rows, x.cols);
@@ -930,15 +1320,27 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
     return launch_mx4_matmul(q, w, bias, act, x.dtype, y, ldy, (char*)ws + scratch_bytes(x.rows, x.cols), s);
 }
 
+// Whether a layer's gradients go through the fused kernels.
+bool is_narrow_grad(int64_t M, int64_t N, int64_t K) { return M > 0 && N >= 4 && K >= 4 && N <= 256 && K <= 256; }
+
 size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
+    size_t narrow = 0;
+    if (is_narrow_grad(M, N, K)) {
+        const size_t a = grad_scratch(M, N, grad_plan(M, N, K, 2)).total, b = grad_scratch(M, N, grad_plan(M, N, K, 4)).total;
+        narrow = a > b ? a : b;
+    }
+    // wide row strides take the general path
     const size_t x = mx4_matmul_workspace(M, K, N), w = mx4_matmul_workspace(N, K, M);
-    return scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
-           round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
+    const size_t general = scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
+                           round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
+    return narrow > general ? narrow : general;
 }
 
 hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
                                       float* dw, float* db, void* ws, hipStream_t s) {
     const int64_t M = dy.rows, N = dy.cols, K = x.cols;
+    if (is_narrow_grad(M, N, K) && dy.ldx < kMaxGradStride && (!dw || x.ldx < kMaxGradStride))
+        return IA_BY_DTYPE(dy.dtype, narrow_grad_t, dy, x, wt, dx, lddx, dw, db, ws, s);
     char* at = (char*)ws;
     const Mx4View dr = scratch_view(at, M, N), dc = scratch_view(at += scratch_bytes(M, N), N, M),
                   xc = scratch_view(at += scratch_bytes(N, M), K, M);
