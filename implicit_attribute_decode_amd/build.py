@@ -30,7 +30,8 @@ ARCH = "gfx950"
 # out with one v_accvgpr_read before its activation (about a tenth of the
 # backward's VALU instructions).
 EXTRA_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-               for name in ("decode.hip", "decode_branch.hip", "decode_bwd.hip", "mx4.hip")}
+               for name in ("decode.hip", "decode_branch.hip", "decode_bwd.hip", "mx4.hip",
+                            "mx4_matmul.hip")}
 
 
 def sources() -> list[str]:

@@ -341,14 +341,13 @@ struct Mx4Source {
     int32_t dtype;
 };
 
-// codes [rows][mx4_blocks(cols)][16], scales [rows][mx4_blocks(cols)]
+// codes [rows][ceil(cols / 32)][16], scales [rows][ceil(cols / 32)]
 struct Mx4View {
     uint8_t* codes;
     uint8_t* scales;
     int64_t rows, cols;
 };
 
-int64_t mx4_blocks(int64_t cols);
 // transpose: out.rows = x.cols, blocks along x's columns
 hipError_t launch_mx4_quantize(const Mx4Source& x, bool transpose, const Mx4View& out, hipStream_t s);
 hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s);

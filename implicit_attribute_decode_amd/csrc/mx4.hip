@@ -24,21 +24,10 @@
 // the first operand against row c of the second, accumulated in fp32.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
-#include "ia_internal.h"
+#include "mx4_common.h"
 
 namespace ia {
 namespace {
-
-typedef int intx4 __attribute__((ext_vector_type(4)));
-typedef int intx8 __attribute__((ext_vector_type(8)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
-
-constexpr int kBlock = 32;   // values per scale
-constexpr int kFp4 = 4;      // the MFMA's format code of E2M1
-constexpr int kNaNByte = 255;
 
 template <typename T>
 struct Pair;
@@ -377,286 +366,6 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* code
     }
 }
 
-// ------------------------------------------------------------------ product
-
-struct MatArgs {
-    const uint8_t* a;   // M rows of `blocks` blocks
-    const uint8_t* as;
-    const uint8_t* b;   // N rows
-    const uint8_t* bs;
-    int64_t M, N, blocks;
-    const float* bias;  // [N] or null
-    int act;
-    void* c;            // [M][ldc]; with splits [splits][M][N] fp32
-    int64_t ldc;
-    int64_t tiles_m, tiles_n, stages;  // tiles, and stages of 8 blocks a split takes
-};
-
-__device__ __forceinline__ intx8 widen(intx4 v) { return intx8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
-
-__device__ __forceinline__ float activate(float v, int act) {
-    return act == IA_ACT_RELU && v < 0.0f ? 0.0f : v;  // a NaN stays
-}
-
-template <int BYTE>
-__device__ __forceinline__ floatx4 mfma(intx4 a, int as, intx4 b, int bs, floatx4 c) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, BYTE, as, BYTE, bs);
-}
-
-// The first operand's scale in byte BYTE of its word, the second's in the lowest.
-template <int BYTE>
-__device__ __forceinline__ floatx4 mfma_pick(intx4 a, int as, intx4 b, int bs, floatx4 c) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(a), widen(b), c, kFp4, kFp4, BYTE, as, 0, bs);
-}
-
-// Tiled product.  A block of 2 x 2 waves computes a tile of 32 WT rows by 32
-// WT columns, a wave 16 WT by 16 WT of it in WT x WT accumulators.  The codes
-// of 8 blocks (256 values, one 128-byte line of a row) of every row pass
-// through LDS in two buffers, copied there by the LDS-DMA loads while the
-// other buffer is multiplied; the scales of 16 blocks follow in 16 bytes a
-// row, their 4 x 4 bytes transposed so that one 32-bit word holds a lane's
-// scales of four MFMA steps (block q of each), selected by the instruction.
-//   The block that stands in slot s of a row is s ^ key(row): the 16 rows that
-// one operand read touches then spread over all banks.
-//   The n rows are the MFMA's first operand: row 4 q + r of n tile j stands for
-// n = 64 (j / 4) + 16 q + 4 (j % 4) + r, so that a lane ends with 16
-// consecutive n of one row m and stores them together.
-//   Rows past the end repeat the last one (their results are not stored).
-// Blocks past the end of a row are other rows' codes with scale byte 0 on both
-// sides: such a product is below 2^-240, under half of fp32's smallest value.
-constexpr int kStageBlocks = 8;
-
-__device__ __forceinline__ int key_a(int row) { return row & 7; }
-__device__ __forceinline__ int key_b(int row) { return (row & 3) | ((row >> 2) & 4); }
-
-// LDS row (within a wave's n rows) of lane c's row of n tile j.
-__device__ __forceinline__ int n_row(int j, int c) { return 64 * (j >> 2) + 16 * (c >> 2) + 4 * (j & 3) + (c & 3); }
-
-// The copies of one operand's tile rows into LDS: a uniform base that follows
-// the stages, and 32-bit lane offsets (a tile's rows span less than 2^32
-// bytes).  Blocks past the end of a row are the next row's, or for the last
-// row the operand's last block.
-template <int ROWS, int WAVES, bool B>
-struct Codes {
-    static constexpr int N = ROWS / 8 / WAVES;  // copies of 8 rows a wave
-    const uint8_t* base;  // first block of the tile's first row
-    int64_t bytes;        // from there to the operand's end, less one block
-    uint32_t off[N];
-
-    __device__ __forceinline__ Codes(const uint8_t* codes, int64_t row0, int64_t rows, int64_t blocks, int wave,
-                                     int lane) {
-        base = codes + row0 * blocks * 16;
-        bytes = (rows - row0) * blocks * 16 - 16;
-        const int64_t last = rows - 1 - row0;
-        // key_b takes bit 4 of the row, which is the same for the wave's rows
-        const int r = 8 * wave + (lane >> 3), slot = (lane & 7) ^ (B ? key_b(r) : key_a(r));
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            off[i] = (uint32_t)(min((int64_t)(8 * WAVES * i + r), last) * blocks * 16) + (uint32_t)slot * 16u;
-    }
-
-    // blocks 8 t .. 8 t + 7
-    __device__ __forceinline__ void copy(intx4* buf, int t, int wave) const {
-        const int64_t skip = (int64_t)t * (kStageBlocks * 16), left = bytes - skip;
-        const uint8_t* at = base + skip;
-        const uint32_t most = (uint32_t)min(max(left, (int64_t)0), (int64_t)0xffffffff);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            __builtin_amdgcn_global_load_lds((const void*)(at + min(off[i], most)),
-                                             (__attribute__((address_space(3))) void*)(buf + (WAVES * i + wave) * 64),
-                                             16, 0, 0);
-    }
-};
-
-// Byte matrix [4][4] (word = row) transposed.
-__device__ __forceinline__ uint4 transpose4(uint4 v) {
-    const uint32_t lo = __builtin_amdgcn_perm(v.y, v.x, 0x05010400u), hi = __builtin_amdgcn_perm(v.w, v.z, 0x05010400u);
-    const uint32_t lo2 = __builtin_amdgcn_perm(v.y, v.x, 0x07030602u), hi2 = __builtin_amdgcn_perm(v.w, v.z, 0x07030602u);
-    return make_uint4(__builtin_amdgcn_perm(hi, lo, 0x05040100u), __builtin_amdgcn_perm(hi, lo, 0x07060302u),
-                      __builtin_amdgcn_perm(hi2, lo2, 0x05040100u), __builtin_amdgcn_perm(hi2, lo2, 0x07060302u));
-}
-
-// Scale bytes of one row of a tile.
-struct ScaleRow {
-    const uint8_t* base;  // uniform: the tile's first row
-    uint32_t off;
-    int64_t left;  // bytes from base to the operand's end
-    int blocks;
-
-    __device__ __forceinline__ ScaleRow(const uint8_t* scales, int64_t row0, int64_t rows, int64_t nblocks, int row) {
-        base = scales + row0 * nblocks;
-        off = (uint32_t)(min((int64_t)row, rows - 1 - row0) * nblocks);
-        left = (rows - row0) * nblocks;
-        blocks = (int)nblocks;
-    }
-
-    // Bytes k0 .. k0 + 15 of the row: one 16-byte load, from before its place
-    // where it would pass the operand's end (finish() shifts it).  An operand
-    // with less than 16 bytes left is read byte by byte (only with k0 = 0).
-    __device__ __forceinline__ uint4 load(int k0) const {
-        uint64_t v[2] = {0, 0};
-        if (k0 >= blocks) {
-        } else if (left < 16) {
-#pragma unroll 1
-            for (int i = 0; i < blocks; ++i) {
-                const uint64_t byte = (uint64_t)base[off + (uint32_t)i] << (8 * (i & 7));
-                v[0] |= i < 8 ? byte : 0;
-                v[1] |= i < 8 ? 0 : byte;
-            }
-        } else {
-            const int64_t room = left - 16 - k0;
-            __builtin_memcpy(v, base + k0 + min(room, (int64_t)0) + min(off, most(room)), 16);
-        }
-        return make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32));
-    }
-
-    // The loaded bytes in their places, zero past the row's end, transposed.
-    __device__ __forceinline__ uint4 finish(uint4 w, int k0) const {
-        uint64_t v[2] = {(uint64_t)w.y << 32 | w.x, (uint64_t)w.w << 32 | w.z};
-        if (left >= 16) {
-            const int64_t room = left - 16 - k0;
-            const uint32_t s = 8 * (off - min(off, most(room)) - (uint32_t)min(room, (int64_t)0)) & 127u;
-            const uint64_t up = (v[1] << 1) << (63 - (s & 63));
-            v[0] = s < 64 ? v[0] >> s | up : v[1] >> (s & 63);
-            v[1] = s < 64 ? v[1] >> s : 0;
-        }
-        const int n = max(blocks - k0, 0);  // uniform
-        v[0] &= n < 8 ? ((uint64_t)1 << (8 * n)) - 1 : ~(uint64_t)0;
-        v[1] &= n < 16 ? ((uint64_t)1 << (8 * max(n - 8, 0))) - 1 : ~(uint64_t)0;
-        return transpose4(make_uint4((uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)));
-    }
-
-    static __device__ __forceinline__ uint32_t most(int64_t room) {
-        return (uint32_t)min(max(room, (int64_t)0), (int64_t)0xffffffff);
-    }
-};
-
-template <int TM, int TN, int HALF>
-__device__ __forceinline__ void multiply_stage(const intx4* la, const intx4* lb, const int (&sa)[TM],
-                                               const int (&sb)[TN], int wm, int wn, int q, int c,
-                                               floatx4 (&acc)[TM][TN]) {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        const int slot = (4 * ks + q) ^ (c & 7);
-        intx4 a[TM], b[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) a[i] = la[(wm + 16 * i + c) * 8 + slot];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) b[j] = lb[(wn + n_row(j, c)) * 8 + slot];
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                acc[i][j] = ks == 0 ? mfma<2 * HALF>(b[j], sb[j], a[i], sa[i], acc[i][j])
-                                    : mfma<2 * HALF + 1>(b[j], sb[j], a[i], sa[i], acc[i][j]);
-            }
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    // the sums exist here: left to the compiler, the products of both stages
-    // sink behind the second one's barrier
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(acc[i][j]));
-}
-
-// 16 consecutive values of one output row from column n on.
-template <typename T>
-__device__ __forceinline__ void store_run(T* row, int64_t n, int64_t N, const float (&v)[16]) {
-    T o[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = (T)v[k];
-    if (n + 16 <= N) {
-        __builtin_memcpy(row + n, o, sizeof(o));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            if (n + k < N) row[n + k] = o[k];
-    }
-}
-
-// Tile index of a block so that blocks of one XCD (every eighth block) take
-// neighbouring tiles: runs of 8 tile rows, column by column.
-__device__ __forceinline__ void tile_of(int64_t b, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
-    const int64_t total = tm * tn, per = total / 8, rest = total % 8, x = b % 8;
-    int64_t t = x * per + min(x, rest) + b / 8;
-    const int64_t group = 8 * tn, g = t / group, h = min((int64_t)8, tm - 8 * g);
-    t -= g * group;
-    im = 8 * g + t % h;
-    in = t / h;
-}
-
-template <typename T, int R, int WAVES_M, int WAVES_N>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) mx4_matmul_kernel(MatArgs p) {
-    constexpr int WAVES = WAVES_M * WAVES_N, TM = R / WAVES_M / 16, TN = R / WAVES_N / 16;
-    __shared__ intx4 a0[R * 8], a1[R * 8], b0[R * 8], b1[R * 8];
-    __shared__ uint4 scales[2][2 * R];  // the rows of a, then of b
-    static_assert(64 * WAVES == 2 * R, "a thread for every row's scales");
-    const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t im, in;
-    tile_of(blockIdx.x, p.tiles_m, p.tiles_n, im, in);
-    const int64_t m0 = im * R, n0 = in * R;
-    const int wm = wave % WAVES_M * 16 * TM, wn = wave / WAVES_M * 16 * TN;
-    const int blocks = (int)p.blocks;
-    const int t0 = (int)(blockIdx.y * p.stages), t1 = min(t0 + (int)p.stages, (blocks + kStageBlocks - 1) / kStageBlocks);
-    const Codes<R, WAVES, false> ca(p.a, m0, p.M, p.blocks, wave, lane);
-    const Codes<R, WAVES, true> cb(p.b, n0, p.N, p.blocks, wave, lane);
-    const bool of_a = wave < WAVES / 2;
-    const ScaleRow row(of_a ? p.as : p.bs, of_a ? m0 : n0, of_a ? p.M : p.N, p.blocks, (int)threadIdx.x % R);
-    floatx4 acc[TM][TN] = {};
-
-    // Stages go in pairs that share a group of scales; the missing second half
-    // of a last pair has zero scales.
-    if (t0 < t1) {
-        ca.copy(a0, t0, wave);
-        cb.copy(b0, t0, wave);
-        scales[0][threadIdx.x] = row.finish(row.load(t0 * kStageBlocks), t0 * kStageBlocks);
-    }
-    int buf = 0;
-    for (int t = t0; t < t1; t += 2, buf ^= 1) {
-        // stage t's codes and scales are in LDS after this barrier, and every
-        // wave has read the other buffers for the last time
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        const uint4 next = row.load((t + 2) * kStageBlocks);
-        ca.copy(a1, t + 1, wave);
-        cb.copy(b1, t + 1, wave);
-        int sa[TM], sb[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = reinterpret_cast<const int*>(&scales[buf][wm + 16 * i + c])[q];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) sb[j] = reinterpret_cast<const int*>(&scales[buf][R + wn + n_row(j, c)])[q];
-        multiply_stage<TM, TN, 0>(a0, b0, sa, sb, wm, wn, q, c, acc);
-        scales[buf ^ 1][threadIdx.x] = row.finish(next, (t + 2) * kStageBlocks);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (t + 2 < t1) {
-            ca.copy(a0, t + 2, wave);
-            cb.copy(b0, t + 2, wave);
-        }
-        multiply_stage<TM, TN, 1>(a1, b1, sa, sb, wm, wn, q, c, acc);
-    }
-    T* out = reinterpret_cast<T*>(p.c) + (int64_t)blockIdx.y * p.M * p.N;
-#pragma unroll
-    for (int g = 0; g < TN / 4; ++g) {
-        const int64_t n = n0 + wn + 64 * g + 16 * q;
-        if (n >= p.N) continue;
-        float bias[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) bias[k] = p.bias ? p.bias[min(n + k, p.N - 1)] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t m = m0 + wm + 16 * i + c;
-            if (m >= p.M) continue;
-            float v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = activate(acc[i][4 * g + (k >> 2)][k & 3] + bias[k], p.act);
-            store_run(out + m * p.ldc, n, p.N, v);
-        }
-    }
-}
-
 // ------------------------------------------------------- narrow layers, fused
 
 // act(Q(x) w^T + bias) for layers of up to 256 outputs whose weights fit LDS.
@@ -728,10 +437,10 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const intx4* w = wc + (step * NT + 4 * g) * 64 + lane;
-                acc[4 * g] = mfma_pick<0>(w[0], sc[g], xc, (int)xs, acc[4 * g]);
-                acc[4 * g + 1] = mfma_pick<1>(w[64], sc[g], xc, (int)xs, acc[4 * g + 1]);
-                acc[4 * g + 2] = mfma_pick<2>(w[128], sc[g], xc, (int)xs, acc[4 * g + 2]);
-                acc[4 * g + 3] = mfma_pick<3>(w[192], sc[g], xc, (int)xs, acc[4 * g + 3]);
+                acc[4 * g] = mfma16<0>(w[0], sc[g], xc, (int)xs, acc[4 * g]);
+                acc[4 * g + 1] = mfma16<1>(w[64], sc[g], xc, (int)xs, acc[4 * g + 1]);
+                acc[4 * g + 2] = mfma16<2>(w[128], sc[g], xc, (int)xs, acc[4 * g + 2]);
+                acc[4 * g + 3] = mfma16<3>(w[192], sc[g], xc, (int)xs, acc[4 * g + 3]);
             }
         }
         if (m0 + c >= s.rows) continue;
@@ -956,8 +665,8 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
                 if (k < tk) {
                     const intx4 xc = codes[buf][tn + k][lane];
                     const int xs = scales[buf][lane][tn + k];
-                    acc[0][k] = mfma_pick<0>(xc, xs, d0, s0, acc[0][k]);
-                    acc[1][k] = mfma_pick<0>(xc, xs, d1, s1, acc[1][k]);
+                    acc[0][k] = mfma16<0>(xc, xs, d0, s0, acc[0][k]);
+                    acc[1][k] = mfma16<0>(xc, xs, d1, s1, acc[1][k]);
                 }
         }
     }
@@ -1020,31 +729,6 @@ __global__ void __launch_bounds__(1024) mx4_narrow_join_kernel(const floatx4* pa
     }
 }
 
-// The splits of a long sum added in a fixed order: c = act(sum of part[s] +
-// bias).  A wave takes every fourth split of 64 neighbouring outputs.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* part, int splits) {
-    __shared__ float sum[4][64];
-    const int64_t total = p.M * p.N;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t base = (int64_t)blockIdx.x * 64; base < total; base += (int64_t)gridDim.x * 64) {
-        const int64_t i = base + lane;
-        float v = 0.0f;
-        if (i < total) {
-#pragma unroll 8
-            for (int s = wave; s < splits; s += 4) v += part[s * total + i];
-        }
-        sum[wave][lane] = v;
-        __syncthreads();
-        if (wave == 0 && i < total) {
-            const int64_t m = i / p.N, n = i - m * p.N;
-            v = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
-            reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
-        }
-        __syncthreads();
-    }
-}
-
 // ------------------------------------------------------------- column sums
 
 // out[col] = sum over the tile rows of part[chunk][col], in double: 16 waves
@@ -1069,14 +753,6 @@ __global__ void __launch_bounds__(1024) mx4_column_sums_kernel(const float* part
 }
 
 // ------------------------------------------------------------------- host
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
-
-unsigned grid_for(int64_t threads) {
-    const int64_t b = ceil_div(threads, 256);
-    return (unsigned)(b < (int64_t)1 << 22 ? b : (int64_t)1 << 22);
-}
 
 template <typename T>
 hipError_t quantize_rows_t(const Mx4Source& x, const Mx4View& out, hipStream_t s) {
@@ -1104,59 +780,6 @@ hipError_t dequantize_t(const Mx4View& q, void* x, int64_t ldx, hipStream_t s) {
     if (q.rows == 0 || blocks == 0) return hipSuccess;
     IA_LAUNCH("mx4_dequantize_kernel", mx4_dequantize_kernel<T>, dim3(grid_for(q.rows * blocks * 4)), dim3(256), 0, s,
               (const uint8_t*)q.codes, (const uint8_t*)q.scales, q.rows, q.cols, blocks, (T*)x, ldx);
-    return hipGetLastError();
-}
-
-// How a product is cut: tiles of 256 x 256 where they fill the 256 CUs, else
-// of 128 x 128, and when those are few the sum over k in up to `splits` parts
-// of at least 4 stages (1,024 values) each, joined in order.
-struct MatPlan {
-    int tile;
-    int64_t tiles_m, tiles_n, stages;
-    int splits;
-};
-MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
-    MatPlan p{};
-    p.tile = ceil_div(M, 256) * ceil_div(N, 256) >= 192 && blocks < (int64_t)1 << 19 ? 256 : 128;
-    p.tiles_m = ceil_div(M, p.tile);
-    p.tiles_n = ceil_div(N, p.tile);
-    const int64_t all = ceil_div(blocks, kStageBlocks), tiles = p.tiles_m * p.tiles_n;
-    int64_t splits = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
-    if (splits > all / 4) splits = all / 4;
-    if (splits < 1) splits = 1;
-    p.stages = ceil_div(ceil_div(all, splits), 2) * 2;  // whole groups of 16 scales
-    if (p.stages < 2) p.stages = 2;
-    p.splits = (int)ceil_div(all, p.stages);
-    if (p.splits < 1) p.splits = 1;
-    return p;
-}
-
-template <typename T>
-hipError_t launch_tiles(const MatArgs& p, const MatPlan& plan, hipStream_t s) {
-    const dim3 grid((unsigned)(plan.tiles_m * plan.tiles_n), (unsigned)plan.splits);
-    if (plan.tile == 256)
-        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 256, 4, 2>), grid, dim3(512), 0, s, p);
-    else
-        IA_LAUNCH("mx4_matmul_kernel", (mx4_matmul_kernel<T, 128, 2, 2>), grid, dim3(256), 0, s, p);
-    return hipGetLastError();
-}
-
-template <typename T>
-hipError_t matmul_t(MatArgs p, void* ws, hipStream_t s) {
-    const MatPlan plan = mat_plan(p.M, p.N, p.blocks);
-    p.tiles_m = plan.tiles_m;
-    p.tiles_n = plan.tiles_n;
-    p.stages = plan.stages;
-    if (plan.splits == 1) return launch_tiles<T>(p, plan, s);
-    MatArgs part = p;
-    part.bias = nullptr;
-    part.act = IA_ACT_NONE;
-    part.c = ws;
-    part.ldc = p.N;
-    hipError_t e = launch_tiles<float>(part, plan, s);
-    if (e != hipSuccess) return e;
-    IA_LAUNCH("mx4_join_kernel", mx4_join_kernel<T>, dim3(grid_for(p.M * p.N * 4)), dim3(256), 0, s, p, (const float*)ws,
-              plan.splits);
     return hipGetLastError();
 }
 
@@ -1255,11 +878,6 @@ hipError_t narrow_grad_t(const Mx4Source& dy, const Mx4Source& x, const Mx4View&
     return hipGetLastError();
 }
 
-#define IA_BY_DTYPE(dtype, fn, ...)                                   \
-    ((dtype) == IA_DTYPE_F32   ? fn<float>(__VA_ARGS__)               \
-     : (dtype) == IA_DTYPE_F16 ? fn<_Float16>(__VA_ARGS__)            \
-                               : fn<__bf16>(__VA_ARGS__))
-
 // Scratch of one quantised matrix: codes, then scales.
 size_t scratch_bytes(int64_t rows, int64_t cols) {
     const size_t n = (size_t)rows * (size_t)mx4_blocks(cols);
@@ -1272,8 +890,6 @@ Mx4View scratch_view(void* at, int64_t rows, int64_t cols) {
 
 }  // namespace
 
-int64_t mx4_blocks(int64_t cols) { return ceil_div(cols, kBlock); }
-
 hipError_t launch_mx4_quantize(const Mx4Source& x, bool transpose, const Mx4View& out, hipStream_t s) {
     if (!transpose) return IA_BY_DTYPE(x.dtype, quantize_rows_t, x, out, s);
     const ColumnOut o{out.codes, out.scales, mx4_blocks(out.cols), nullptr, nullptr, 0, nullptr};
@@ -1282,18 +898,6 @@ hipError_t launch_mx4_quantize(const Mx4Source& x, bool transpose, const Mx4View
 
 hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s) {
     return IA_BY_DTYPE(dtype, dequantize_t, q, x, ldx, s);
-}
-
-size_t mx4_matmul_workspace(int64_t M, int64_t N, int64_t K) {
-    const int splits = mat_plan(M, N, mx4_blocks(K)).splits;
-    return splits > 1 ? round_up((size_t)splits * (size_t)M * (size_t)N * sizeof(float)) : 0;
-}
-
-hipError_t launch_mx4_matmul(const Mx4View& a, const Mx4View& b, const float* bias, int32_t act, int32_t dtype, void* c,
-                             int64_t ldc, void* ws, hipStream_t s) {
-    if (a.rows == 0 || b.rows == 0) return hipSuccess;
-    const MatArgs p{a.codes, a.scales, b.codes, b.scales, a.rows, b.rows, mx4_blocks(a.cols), bias, act, c, ldc, 0, 0, 0};
-    return IA_BY_DTYPE(dtype, matmul_t, p, ws, s);
 }
 
 // Whether a layer of K inputs and N outputs goes through the fused kernel.
