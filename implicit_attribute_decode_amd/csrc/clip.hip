@@ -8,13 +8,14 @@
 //   factor = max_norm / norm if norm > max_norm, else 1
 //
 // All three are bound by memory: a call reads each gradient once for the norm
-// and once for its use.  Tensors are cut into chunks of kChunk elements; one
-// launch covers up to kNormTensors (kScaleTensors, kAdamGroups) tensors, whose
-// descriptors travel as kernel arguments, so that a decoder's fourteen groups
-// take one launch and no table has to be uploaded.  Squares are summed in
-// double (fp32 squares overflow from 1.8e19 on; the conversions and double
-// multiply-adds hide behind the loads), per block, then over the blocks in a
-// fixed order: the norm is the same on every run.
+// and once for its use.  Tensors are cut into chunks of kChunk elements, and
+// as many tensors as their descriptors fit into 4 KB of kernel arguments go
+// into one launch (kNormTensors, kScaleTensors, kGroups), so that a decoder's
+// fourteen groups take one and no table has to be uploaded.  Squares are
+// summed in double (fp32 squares overflow from 1.8e19 on; the conversions and
+// double multiply-adds hide behind the loads), per block.  Every block of the
+// pass that uses the factor adds the blocks' sums itself, all in one order:
+// the norm is the same on every run, and no third launch stands between.
 #include <hip/hip_runtime.h>
 
 #include "adam_common.h"
@@ -25,24 +26,55 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 4096;      // elements
-constexpr int kMaxBlocks = 2048;  // 8 blocks per CU
-constexpr int kTensors = 80;      // descriptors in 4 KB of kernel arguments
+constexpr int kNormBlocks = 1024;  // most blocks of a norm launch (each leaves one sum)
+constexpr int kUseBlocks = 2048;   // of a launch that uses the factor
+constexpr int kMostParts = 2048;   // sums that every block adds by itself
+constexpr int kNormTensors = 240;
+constexpr int kScaleTensors = 160;
+constexpr int kStridedTensors = 80;
 constexpr int kGroups = 48;
 
-struct Tensor {
+// A dense tensor to read: its size is its chunks, less `slack` elements of the
+// last one.
+struct Dense {
+    const void* src;
+    uint32_t dtype_slack;  // dtype | slack << 2
+    int32_t first;         // its first chunk in the launch
+};
+struct DenseArgs {
+    int32_t count, chunks;
+    Dense t[kNormTensors];
+};
+static_assert(sizeof(DenseArgs) <= 3968, "descriptors and the other arguments fit 4 KB");
+
+// A dense tensor to scale.
+struct Scaled {
+    const void* src;
+    void* dst;
+    uint32_t dtype_slack;
+    int32_t first;
+};
+struct ScaledArgs {
+    int32_t count, chunks;
+    Scaled t[kScaleTensors];
+};
+static_assert(sizeof(ScaledArgs) <= 3968, "descriptors and the other arguments fit 4 KB");
+
+// Rows of dim elements, sstride (dstride) apart.
+struct Strided {
     const void* src;
     void* dst;
     int64_t n;
-    int32_t dim, sstride, dstride;  // rows of dim elements stride apart (dim == stride: dense)
+    int32_t dim, sstride, dstride;
     int32_t dtype;
+    int32_t first;
+    int32_t pad;
 };
-
-struct TensorArgs {
-    int32_t count;
-    int32_t first[kTensors + 1];  // first chunk of each tensor, then the number of chunks
-    Tensor t[kTensors];
+struct StridedArgs {
+    int32_t count, chunks;
+    Strided t[kStridedTensors];
 };
-static_assert(sizeof(TensorArgs) <= 3900, "descriptors and the other arguments fit 4 KB");
+static_assert(sizeof(StridedArgs) <= 3968, "descriptors and the other arguments fit 4 KB");
 
 struct Group {
     float* p;
@@ -51,25 +83,23 @@ struct Group {
     float* v;
     uint16_t* p16;
     int64_t n;
-    int32_t dim, stride;
+    int32_t dim, stride;  // the parameter's rows (dim == stride: dense)
     float step_size;
-    int32_t pad;
+    int32_t first;
 };
-
 struct GroupArgs {
-    int32_t count;
-    int32_t first[kGroups + 1];
+    int32_t count, chunks;
     Group t[kGroups];
 };
 static_assert(sizeof(GroupArgs) <= 3900, "descriptors and the other arguments fit 4 KB");
 
-// The tensor that holds chunk c (uniform over the block).
+// The tensor that holds chunk c (uniform over the block), at or after `from`.
 template <typename A>
-__device__ __forceinline__ int find(const A& a, int c) {
-    int lo = 0, hi = a.count - 1;
+__device__ __forceinline__ int find(const A& a, int c, int from) {
+    int lo = from, hi = a.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a.first[mid] <= c)
+        if (a.t[mid].first <= c)
             lo = mid;
         else
             hi = mid - 1;
@@ -134,13 +164,11 @@ __device__ double chunk_squares_strided(const T* src, int64_t i0, int n, int dim
     return s;
 }
 
-template <typename T>
-__device__ __forceinline__ double squares(const Tensor& t, int64_t i0, int n) {
-    const T* src = reinterpret_cast<const T*>(t.src);
-    if (t.dim == t.sstride) return chunk_squares(src + i0, n);
-    return chunk_squares_strided(src, i0, n, t.dim, t.sstride);
-}
+// Elements of chunk c of the tensor with descriptor word w and chunks up to
+// `next`.
+__device__ __forceinline__ int elements(uint32_t w, int c, int next) { return c + 1 == next ? kChunk - (int)(w >> 2) : kChunk; }
 
+// The sum over the block, on all threads.
 __device__ __forceinline__ double block_sum(double s) {
     __shared__ double red[kThreads / 64];
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
@@ -149,55 +177,84 @@ __device__ __forceinline__ double block_sum(double s) {
     return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(TensorArgs a, double* part) {
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(DenseArgs a, double* part) {
     double s = 0.0;
-    for (int c = blockIdx.x; c < a.first[a.count]; c += gridDim.x) {
-        const int k = find(a, c);
-        const Tensor& t = a.t[k];
-        const int64_t i0 = (int64_t)(c - a.first[k]) * kChunk;
-        const int n = (int)min((int64_t)kChunk, t.n - i0);
-        if (t.dtype == IA_DTYPE_F32)
-            s += squares<float>(t, i0, n);
-        else if (t.dtype == IA_DTYPE_F16)
-            s += squares<_Float16>(t, i0, n);
+    int k = 0;
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        k = find(a, c, k);
+        const uint32_t w = a.t[k].dtype_slack;
+        const int n = elements(w, c, k + 1 < a.count ? a.t[k + 1].first : a.chunks);
+        const int64_t i0 = (int64_t)(c - a.t[k].first) * kChunk;
+        if ((w & 3) == IA_DTYPE_F32)
+            s += chunk_squares(reinterpret_cast<const float*>(a.t[k].src) + i0, n);
+        else if ((w & 3) == IA_DTYPE_F16)
+            s += chunk_squares(reinterpret_cast<const _Float16*>(a.t[k].src) + i0, n);
         else
-            s += squares<__bf16>(t, i0, n);
+            s += chunk_squares(reinterpret_cast<const __bf16*>(a.t[k].src) + i0, n);
     }
     s = block_sum(s);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
-// One block: the partial sums added in a fixed order.  stats = {norm, factor,
-// 1 if the norm is finite else 0}, rounded once from double.
-__global__ void __launch_bounds__(kThreads) norm_finish_kernel(const double* part, int n, float max_norm,
-                                                               float* stats) {
+__global__ void __launch_bounds__(kThreads) grad_norm_strided_kernel(StridedArgs a, double* part) {
     double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) s += part[i];
-    s = block_sum(s);
-    if (threadIdx.x == 0) {
-        const double norm = sqrt(s);
-        // a NaN norm passes NaN on; an infinite one gives 0
-        const double f = norm > (double)max_norm ? (double)max_norm / norm : (norm == norm ? 1.0 : norm);
-        stats[0] = (float)norm;
-        stats[1] = (float)f;
-        stats[2] = isfinite(norm) ? 1.0f : 0.0f;
+    int k = 0;
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        k = find(a, c, k);
+        const Strided& t = a.t[k];
+        const int64_t i0 = (int64_t)(c - t.first) * kChunk;
+        const int n = (int)min((int64_t)kChunk, t.n - i0);
+        if (t.dtype == IA_DTYPE_F32)
+            s += chunk_squares_strided(reinterpret_cast<const float*>(t.src), i0, n, t.dim, t.sstride);
+        else if (t.dtype == IA_DTYPE_F16)
+            s += chunk_squares_strided(reinterpret_cast<const _Float16*>(t.src), i0, n, t.dim, t.sstride);
+        else
+            s += chunk_squares_strided(reinterpret_cast<const __bf16*>(t.src), i0, n, t.dim, t.sstride);
     }
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// The norm launches' sums and what comes of them.
+struct Norm {
+    const double* part;
+    int32_t parts;
+    float max_norm;
+    float* stats;  // {norm, factor, 1 if the norm is finite else 0}
+};
+
+// The factor, on all threads; the first block writes stats, each value rounded
+// once from double.
+__device__ __forceinline__ float clip_factor(const Norm& m, bool& finite) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < m.parts; i += kThreads) s += m.part[i];
+    const double norm = sqrt(block_sum(s)), most = (double)m.max_norm;
+    // a NaN norm passes NaN on; an infinite one gives 0
+    const float f = (float)(norm > most ? most / norm : (norm == norm ? 1.0 : norm));
+    finite = isfinite(norm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        m.stats[0] = (float)norm;
+        m.stats[1] = f;
+        m.stats[2] = finite ? 1.0f : 0.0f;
+    }
+    return f;
+}
+
+__global__ void __launch_bounds__(kThreads) norm_collect_kernel(double* part, int32_t parts) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[0] = s;
+}
+
+__global__ void __launch_bounds__(kThreads) norm_finish_kernel(Norm m) {
+    bool finite;
+    (void)clip_factor(m, finite);
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t i0, int n, float f) {
+__device__ __forceinline__ void scale_chunk(const T* src, T* dst, int n, float f) {
     constexpr int E = Vec<T>::N, V = kChunk / (kThreads * E);
-    const T* src = reinterpret_cast<const T*>(t.src);
-    T* dst = reinterpret_cast<T*>(t.dst);
-    if (t.dim != t.sstride || t.dim != t.dstride) {
-        for (int k = threadIdx.x; k < n; k += kThreads) {
-            const int64_t row = (i0 + k) / t.dim, col = i0 + k - row * t.dim;
-            dst[row * t.dstride + col] = (T)((float)src[row * t.sstride + col] * f);
-        }
-        return;
-    }
-    src += i0;
-    dst += i0;
     const int nv = n / E;
     Vec<T> v[V];
 #pragma unroll
@@ -218,20 +275,53 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t i0, int n, 
     if (r < n) dst[r] = (T)((float)src[r] * f);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(TensorArgs a, const float* stats) {
-    const float f = stats[1];
-    for (int c = blockIdx.x; c < a.first[a.count]; c += gridDim.x) {
-        const int k = find(a, c);
-        const Tensor& t = a.t[k];
-        if (f == 1.0f && t.src == t.dst) continue;  // in place: every product is its own value
-        const int64_t i0 = (int64_t)(c - a.first[k]) * kChunk;
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(ScaledArgs a, Norm m) {
+    bool finite;
+    const float f = clip_factor(m, finite);
+    int k = 0;
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        k = find(a, c, k);
+        const void* src = a.t[k].src;
+        void* dst = a.t[k].dst;
+        if (f == 1.0f && src == dst) continue;  // in place: every product is its own value
+        const uint32_t w = a.t[k].dtype_slack;
+        const int n = elements(w, c, k + 1 < a.count ? a.t[k + 1].first : a.chunks);
+        const int64_t i0 = (int64_t)(c - a.t[k].first) * kChunk;
+        if ((w & 3) == IA_DTYPE_F32)
+            scale_chunk(reinterpret_cast<const float*>(src) + i0, reinterpret_cast<float*>(dst) + i0, n, f);
+        else if ((w & 3) == IA_DTYPE_F16)
+            scale_chunk(reinterpret_cast<const _Float16*>(src) + i0, reinterpret_cast<_Float16*>(dst) + i0, n, f);
+        else
+            scale_chunk(reinterpret_cast<const __bf16*>(src) + i0, reinterpret_cast<__bf16*>(dst) + i0, n, f);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_strided(const Strided& t, int64_t i0, int n, float f) {
+    const T* src = reinterpret_cast<const T*>(t.src);
+    T* dst = reinterpret_cast<T*>(t.dst);
+    for (int k = threadIdx.x; k < n; k += kThreads) {
+        const int64_t row = (i0 + k) / t.dim, col = i0 + k - row * t.dim;
+        dst[row * t.dstride + col] = (T)((float)src[row * t.sstride + col] * f);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) grad_scale_strided_kernel(StridedArgs a, Norm m) {
+    bool finite;
+    const float f = clip_factor(m, finite);
+    int k = 0;
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        k = find(a, c, k);
+        const Strided& t = a.t[k];
+        if (f == 1.0f && t.src == t.dst) continue;
+        const int64_t i0 = (int64_t)(c - t.first) * kChunk;
         const int n = (int)min((int64_t)kChunk, t.n - i0);
         if (t.dtype == IA_DTYPE_F32)
-            scale_chunk<float>(t, i0, n, f);
+            scale_strided<float>(t, i0, n, f);
         else if (t.dtype == IA_DTYPE_F16)
-            scale_chunk<_Float16>(t, i0, n, f);
+            scale_strided<_Float16>(t, i0, n, f);
         else
-            scale_chunk<__bf16>(t, i0, n, f);
+            scale_strided<__bf16>(t, i0, n, f);
     }
 }
 
@@ -280,120 +370,160 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
     }
 }
 
-__global__ void __launch_bounds__(kThreads) adam_clip_kernel(GroupArgs a, AdamConsts c, const float* stats) {
-    const float f = stats[1];
-    if (stats[2] == 0.0f) return;  // gradients that are not finite change nothing
-    for (int k = blockIdx.x; k < a.first[a.count]; k += gridDim.x) {
-        const int t = find(a, k);
-        const int64_t i0 = (int64_t)(k - a.first[t]) * kChunk;
+__global__ void __launch_bounds__(kThreads) adam_clip_kernel(GroupArgs a, AdamConsts c, Norm m) {
+    bool finite;
+    const float f = clip_factor(m, finite);
+    if (!finite) return;  // gradients that are not finite change nothing
+    int t = 0;
+    for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
+        t = find(a, k, t);
+        const int64_t i0 = (int64_t)(k - a.t[t].first) * kChunk;
         adam_chunk(a.t[t], i0, (int)min((int64_t)kChunk, a.t[t].n - i0), f, c);
     }
 }
 
-int chunks(int64_t n) { return (int)((n + kChunk - 1) / kChunk); }
+int64_t chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+uint32_t dtype_slack(int32_t dtype, int64_t n) { return (uint32_t)dtype | (uint32_t)(chunks(n) * kChunk - n) << 2; }
 
 // Calls launch(args, blocks) for consecutive runs of tensors that fit one
 // launch's descriptors; fill(k, args.t[i]) describes tensor k and returns its
-// size.  Empty tensors are left out.
+// size (0: it is left out).
 template <typename A, typename Fill, typename Launch>
-hipError_t each_launch(int count, int capacity, Fill fill, Launch launch) {
+hipError_t each_launch(int count, int capacity, int most, Fill fill, Launch launch) {
     A a;
-    a.count = 0;
-    a.first[0] = 0;
+    a.count = a.chunks = 0;
     for (int k = 0; k <= count; ++k) {
         if (k < count) {
             const int64_t n = fill(k, a.t[a.count]);
-            if (n == 0) continue;
-            a.first[a.count + 1] = a.first[a.count] + chunks(n);
-            ++a.count;
+            if (n > 0) {
+                a.t[a.count].first = a.chunks;
+                a.chunks += (int32_t)chunks(n);
+                ++a.count;
+            }
         }
-        if (a.count == capacity || (k == count && a.count > 0)) {
-            const int c = a.first[a.count];
-            launch(a, c < kMaxBlocks ? c : kMaxBlocks);
+        if (a.count > 0 && (a.count == capacity || k == count)) {
+            launch(a, a.chunks < most ? a.chunks : most);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            a.count = 0;
+            a.count = a.chunks = 0;
         }
     }
     return hipSuccess;
 }
 
-int64_t fill_tensor(const ia_grad& g, Tensor& t) {
-    const bool dense = g.stride == g.dim && (!g.out || g.out_stride == g.dim);
-    t.src = g.data;
-    t.dst = g.out ? g.out : g.data;
-    t.n = g.rows * g.dim;
-    t.dim = dense ? 1 : g.dim;
-    t.sstride = dense ? 1 : g.stride;
-    t.dstride = dense ? 1 : (g.out ? g.out_stride : g.stride);
-    t.dtype = g.dtype;
+bool is_dense(const ia_grad& g) { return g.stride == g.dim && (!g.out || g.out_stride == g.dim); }
+
+int64_t fill_strided(const ia_grad& g, Strided& t) {
+    if (is_dense(g)) return 0;
+    t = Strided{g.data, g.out ? g.out : g.data, g.rows * g.dim, g.dim, g.stride, g.out ? g.out_stride : g.stride, g.dtype,
+                0, 0};
     return t.n;
 }
 
-hipError_t norm_passes(const ia_grad* grads, int count, float max_norm, double* part, float* stats, hipStream_t s) {
-    int parts = 0;
-    hipError_t e = each_launch<TensorArgs>(
-        count, kTensors, [&](int k, Tensor& t) { return fill_tensor(grads[k], t); },
-        [&](const TensorArgs& a, int blocks) {
-            IA_LAUNCH("grad_norm_kernel", grad_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, a, part + parts);
-            parts += blocks;
+int64_t fill_dense(const void* src, int32_t dtype, int64_t n, Dense& t) {
+    t.src = src;
+    t.dtype_slack = dtype_slack(dtype, n);
+    return n;
+}
+
+// Leaves every block's sum in part; returns how many through m.parts.
+hipError_t norm_passes(const ia_grad* grads, int count, double* part, Norm& m, hipStream_t s) {
+    hipError_t e = each_launch<DenseArgs>(
+        count, kNormTensors, kNormBlocks,
+        [&](int k, Dense& t) {
+            return is_dense(grads[k]) ? fill_dense(grads[k].data, grads[k].dtype, grads[k].rows * grads[k].dim, t) : 0;
+        },
+        [&](const DenseArgs& a, int blocks) {
+            IA_LAUNCH("grad_norm_kernel", grad_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, a, part + m.parts);
+            m.parts += blocks;
         });
     if (e != hipSuccess) return e;
-    IA_LAUNCH("norm_finish_kernel", norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, (const double*)part, parts,
-              max_norm, stats);
+    return each_launch<StridedArgs>(
+        count, kStridedTensors, kNormBlocks, [&](int k, Strided& t) { return fill_strided(grads[k], t); },
+        [&](const StridedArgs& a, int blocks) {
+            IA_LAUNCH("grad_norm_strided_kernel", grad_norm_strided_kernel, dim3(blocks), dim3(kThreads), 0, s, a,
+                      part + m.parts);
+            m.parts += blocks;
+        });
+}
+
+// Very many tensors leave so many sums that adding them in every block would
+// cost more than a launch: one block joins them first.
+hipError_t collect(double* part, Norm& m, hipStream_t s) {
+    if (m.parts <= kMostParts) return hipSuccess;
+    IA_LAUNCH("norm_collect_kernel", norm_collect_kernel, dim3(1), dim3(kThreads), 0, s, part, m.parts);
+    m.parts = 1;
+    return hipGetLastError();
+}
+
+hipError_t finish(const Norm& m, hipStream_t s) {
+    IA_LAUNCH("norm_finish_kernel", norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, m);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// One double per block of every norm launch
+// One double per block of every norm launch: tensors of more than
+// kNormTensors, or strided ones between dense ones, take several.
 size_t clip_workspace(int32_t tensors) {
-    return ((size_t)tensors / kTensors + 1) * kMaxBlocks * sizeof(double);
+    return ((size_t)tensors / kNormTensors + (size_t)tensors / kStridedTensors + 2) * kNormBlocks * sizeof(double);
 }
-
-int64_t clip_chunk() { return kChunk; }
 
 hipError_t launch_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, float* stats,
                             hipStream_t s) {
-    return norm_passes(grads, count, max_norm, reinterpret_cast<double*>(ws), stats, s);
+    double* part = reinterpret_cast<double*>(ws);
+    Norm m{part, 0, max_norm, stats};
+    hipError_t e = norm_passes(grads, count, part, m, s);
+    return e != hipSuccess ? e : finish(m, s);
 }
 
 hipError_t launch_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, float* stats,
                                  hipStream_t s) {
-    hipError_t e = norm_passes(grads, count, max_norm, reinterpret_cast<double*>(ws), stats, s);
+    double* part = reinterpret_cast<double*>(ws);
+    Norm m{part, 0, max_norm, stats};
+    hipError_t e = norm_passes(grads, count, part, m, s);
+    if (e == hipSuccess) e = collect(part, m, s);
     if (e != hipSuccess) return e;
-    return each_launch<TensorArgs>(
-        count, kTensors, [&](int k, Tensor& t) { return fill_tensor(grads[k], t); },
-        [&](const TensorArgs& a, int blocks) {
-            IA_LAUNCH("grad_scale_kernel", grad_scale_kernel, dim3(blocks), dim3(kThreads), 0, s, a,
-                      (const float*)stats);
+    if (m.parts == 0) return finish(m, s);
+    e = each_launch<ScaledArgs>(
+        count, kScaleTensors, kUseBlocks,
+        [&](int k, Scaled& t) {
+            const ia_grad& g = grads[k];
+            if (!is_dense(g)) return (int64_t)0;
+            t.src = g.data;
+            t.dst = g.out ? g.out : g.data;
+            t.dtype_slack = dtype_slack(g.dtype, g.rows * g.dim);
+            return g.rows * g.dim;
+        },
+        [&](const ScaledArgs& a, int blocks) {
+            IA_LAUNCH("grad_scale_kernel", grad_scale_kernel, dim3(blocks), dim3(kThreads), 0, s, a, m);
+        });
+    if (e != hipSuccess) return e;
+    return each_launch<StridedArgs>(
+        count, kStridedTensors, kUseBlocks, [&](int k, Strided& t) { return fill_strided(grads[k], t); },
+        [&](const StridedArgs& a, int blocks) {
+            IA_LAUNCH("grad_scale_strided_kernel", grad_scale_strided_kernel, dim3(blocks), dim3(kThreads), 0, s, a, m);
         });
 }
 
 hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
                             float eps, int32_t step, void* ws, float* stats, hipStream_t s) {
     double* part = reinterpret_cast<double*>(ws);
-    int parts = 0;
-    hipError_t e = each_launch<TensorArgs>(
-        count, kTensors,
-        [&](int k, Tensor& t) {
-            const int64_t n = groups[k].rows * groups[k].dim;
-            t = Tensor{groups[k].grad, nullptr, n, 1, 1, 1, IA_DTYPE_F32};
-            return n;
-        },
-        [&](const TensorArgs& a, int blocks) {
-            IA_LAUNCH("grad_norm_kernel", grad_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, a, part + parts);
-            parts += blocks;
+    Norm m{part, 0, max_norm, stats};
+    hipError_t e = each_launch<DenseArgs>(
+        count, kNormTensors, kNormBlocks,
+        [&](int k, Dense& t) { return fill_dense(groups[k].grad, IA_DTYPE_F32, groups[k].rows * groups[k].dim, t); },
+        [&](const DenseArgs& a, int blocks) {
+            IA_LAUNCH("grad_norm_kernel", grad_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, a, part + m.parts);
+            m.parts += blocks;
         });
+    if (e == hipSuccess) e = collect(part, m, s);
     if (e != hipSuccess) return e;
-    IA_LAUNCH("norm_finish_kernel", norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, (const double*)part, parts,
-              max_norm, stats);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (m.parts == 0) return finish(m, s);
     const AdamConsts c{beta1, beta2, eps, (float)(1.0 / (1.0 - pow((double)beta2, (double)step)))};
     const double correction = 1.0 - pow((double)beta1, (double)step);
     return each_launch<GroupArgs>(
-        count, kGroups,
+        count, kGroups, kUseBlocks,
         [&](int k, Group& t) {
             const ia_adam_group& g = groups[k];
             const bool dense = g.dim == g.param_stride;
@@ -402,8 +532,7 @@ hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float ma
             return t.n;
         },
         [&](const GroupArgs& a, int blocks) {
-            IA_LAUNCH("adam_clip_kernel", adam_clip_kernel, dim3(blocks), dim3(kThreads), 0, s, a, c,
-                      (const float*)stats);
+            IA_LAUNCH("adam_clip_kernel", adam_clip_kernel, dim3(blocks), dim3(kThreads), 0, s, a, c, m);
         });
 }
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -103,6 +104,10 @@ class AdamGroup(C.Structure):
     _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
                 ("param_f16", C.c_void_p), ("rows", C.c_int64), ("dim", C.c_int32), ("param_stride", C.c_int32),
                 ("lr", C.c_float)]
+    PACK = struct.Struct("@5Pqiif4x")  # the same fields, to write a whole element at once
+
+
+assert AdamGroup.PACK.size == C.sizeof(AdamGroup)
 
 
 class Mx4(C.Structure):
@@ -197,7 +202,7 @@ def _stream(stream=None) -> int:
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 

@@ -419,30 +419,31 @@ class Adam:
     def _clipped_step(self, grads: dict, max_norm: float):
         names = [k for k in self.groups if grads.get(k) is not None]
         arr = (ia.AdamGroup * len(names))()
+        at, pack = 0, ia.AdamGroup.PACK
         keep, rates = [], {}  # contiguous copies live until the call has enqueued its reads
-        for d, name in zip(arr, names):
-            g, p = self.groups[name], self.groups[name]["param"]
+        for name in names:
+            g, grad = self.groups[name], grads[name]
+            p, f16, lr = g["param"], g.get("f16"), g["lr"]
             m, v = self.state[name]
-            grad = grads[name]
-            if p.dtype != torch.float32 or grad.dtype != torch.float32 or grad.shape != p.shape:
+            if p.dtype is not torch.float32 or grad.dtype is not torch.float32 or grad.shape != p.shape:
                 raise ValueError(f"group {name}: parameter and gradient must be float32 of one shape")
             if not grad.is_contiguous():
                 grad = grad.contiguous()
                 keep.append(grad)
-            f16 = g.get("f16")
             if p.is_contiguous():
-                d.rows, d.dim, d.param_stride = p.numel(), 1, 1
+                rows, dim, stride = p.numel(), 1, 1
             elif p.dim() == 2 and p.stride(1) == 1 and p.stride(0) >= p.shape[1] and f16 is None:
-                d.rows, d.dim, d.param_stride = p.shape[0], p.shape[1], p.stride(0)
+                rows, dim, stride = p.shape[0], p.shape[1], p.stride(0)
             else:
                 raise ValueError(f"group {name}: the parameter must be contiguous, or [rows, dim] rows of a wider "
                                  "array without an fp16 mirror")
-            if g["lr"] not in rates:
-                rates[g["lr"]] = lr_at(self.t - 1, g["lr"], self.warmup, self.total)
-            d.param, d.grad, d.m, d.v = p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr()
-            d.param_f16 = None if f16 is None else f16.data_ptr()
-            d.lr = rates[g["lr"]]
-        device = self.groups[names[0]]["param"].device if names else "cuda"
+            rate = rates.get(lr)
+            if rate is None:
+                rate = rates[lr] = lr_at(self.t - 1, lr, self.warmup, self.total)
+            pack.pack_into(arr, at, p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr(),
+                           0 if f16 is None else f16.data_ptr(), rows, dim, stride, rate)
+            at += pack.size
+        device = p.device if names else "cuda"
         stats = torch.empty(3, device=device)
         ws = torch.empty(ia.ia_clip_workspace_size(len(names)), dtype=torch.uint8, device=device)
         ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t, ws, stats)
