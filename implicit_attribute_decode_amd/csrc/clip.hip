@@ -127,6 +127,29 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T>& v) {
     __builtin_memcpy(p, &v, sizeof(v));
 }
 
+// The same for data that this call reads or writes once: it does not displace
+// what the memory-side cache holds (the gradients, between their two readings).
+// Parameters and moments so: an Adam step over 16.8M, 50M and 158M parameters
+// 113 -> 104, 340 -> 295 and 1072 -> 1036 us; clipped copies so: 16.8M and 67M
+// gradients 40 -> 35 and 151 -> 135 us.  The gradients themselves are read in
+// the ordinary way: read once only, the norm is faster (149 -> 110 us at 158M)
+// and the step slower by as much or more (295 -> 325 us in all at 50M).
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t loose_uintx4 __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T>
+__device__ __forceinline__ Vec<T> load_once(const T* p) {
+    Vec<T> v;
+    const uintx4 w = __builtin_nontemporal_load(reinterpret_cast<const loose_uintx4*>(p));
+    __builtin_memcpy(&v, &w, sizeof(v));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void store_once(T* p, const Vec<T>& v) {
+    uintx4 w;
+    __builtin_memcpy(&w, &v, sizeof(w));
+    __builtin_nontemporal_store(w, reinterpret_cast<loose_uintx4*>(p));
+}
+
 __device__ __forceinline__ double square(float g) {
     const double d = (double)g;
     return d * d;
@@ -268,7 +291,10 @@ __device__ __forceinline__ void scale_chunk(const T* src, T* dst, int n, float f
         if (i < nv) {
 #pragma unroll
             for (int e = 0; e < E; ++e) v[j].e[e] = (T)((float)v[j].e[e] * f);
-            store_vec(dst + (size_t)i * E, v[j]);
+            if (src == dst)
+                store_vec(dst + (size_t)i * E, v[j]);
+            else
+                store_once(dst + (size_t)i * E, v[j]);
         }
     }
     const int r = nv * E + (int)threadIdx.x;
@@ -346,7 +372,7 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
     float* p = t.p + i0;
     const int nv = n / 4;
     for (int i = threadIdx.x; i < nv; i += kThreads) {
-        Vec<float> pv = load_vec(p + 4 * i), mv = load_vec(m + 4 * i), vv = load_vec(v + 4 * i);
+        Vec<float> pv = load_once(p + 4 * i), mv = load_once(m + 4 * i), vv = load_once(v + 4 * i);
         const Vec<float> gv = load_vec(g + 4 * i);
         uint16_t h[4];
 #pragma unroll
@@ -354,9 +380,9 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
             pv.e[e] = adam_element(pv.e[e], gv.e[e] * f, mv.e[e], vv.e[e], c, t.step_size);
             h[e] = __builtin_bit_cast(uint16_t, (_Float16)pv.e[e]);
         }
-        store_vec(p + 4 * i, pv);
-        store_vec(m + 4 * i, mv);
-        store_vec(v + 4 * i, vv);
+        store_once(p + 4 * i, pv);
+        store_once(m + 4 * i, mv);
+        store_once(v + 4 * i, vv);
         if (p16) __builtin_memcpy(p16 + 4 * i, h, 8);
     }
     const int k = nv * 4 + (int)threadIdx.x;
