@@ -465,6 +465,85 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
     }
 }
 
+// ------------------------------------------------------------ few rows
+
+// act(Q(x) w^T + bias) for up to 64 rows (16 MT), where the weights are what
+// there is to read: a block of 8 waves takes 16 outputs, each wave every eighth
+// step of 128 inputs.  The weights of a chunk are loaded first; while they come,
+// the block quantises the chunk of x once, one block of 32 a thread, into LDS,
+// where every wave takes it as its operand.  The waves' sums meet in LDS and
+// are added in order.
+struct FewArgs {
+    const uint8_t* w;  // [N][blocks]
+    const uint8_t* ws;
+    int64_t N, blocks;
+    const float* bias;
+    int act;
+    void* y;
+    int64_t ldy;
+};
+
+constexpr int kFewRows = 64;
+constexpr int kFewWaves = 8;
+constexpr int kFewUnits = 2048;  // blocks of x in LDS
+
+template <typename T, int MT>
+__global__ void __launch_bounds__(64 * kFewWaves) mx4_few_rows_kernel(Source<T> s, FewArgs p) {
+    constexpr int ROWS = 16 * MT, CHUNK = kFewUnits / ROWS, STEPS = CHUNK / 4 / kFewWaves;  // blocks, a wave's steps
+    __shared__ intx4 xc[kFewUnits];  // [block][row]
+    __shared__ uint8_t xs[kFewUnits];
+    const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * 16, row = min(n0 + c, p.N - 1) * p.blocks;
+    floatx4 acc[MT] = {};
+    for (int64_t b0 = 0; b0 < p.blocks; b0 += CHUNK) {
+        intx4 wc[STEPS];
+        int wb[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int64_t b = b0 + 4 * (kFewWaves * i + wave) + q;
+            const int64_t at = row + min(b, p.blocks - 1);
+            wc[i] = *reinterpret_cast<const intx4*>(p.w + at * 16);
+            wb[i] = b < p.blocks ? (int)p.ws[at] : 0;
+        }
+        // whole steps: blocks past the end are zero
+        const int here = (int)min((int64_t)CHUNK, (p.blocks - b0 + 3) / 4 * 4);
+        __syncthreads();  // the last chunk has been read
+        for (int i = threadIdx.x; i < here * (int)s.rows; i += 64 * kFewWaves) {
+            const int m = i / here, b = i - m * here;
+            uint32_t byte;
+            xc[b * ROWS + m] = quantize(load_values(s.x + m * s.ldx, (b0 + b) * kBlock, s.cols), byte);
+            xs[b * ROWS + m] = (uint8_t)byte;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int b = 4 * (kFewWaves * i + wave);
+            if (b < here) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const int at = (b + q) * ROWS + 16 * t + c;
+                    acc[t] = mfma16<0>(wc[i], wb[i], xc[at], (int)xs[at], acc[t]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    float* sum = reinterpret_cast<float*>(xc);  // [wave][row][16 outputs]
+    static_assert(kFewWaves * kFewRows * 16 * sizeof(float) <= sizeof(xc), "the sums fit");
+#pragma unroll
+    for (int t = 0; t < MT; ++t) *reinterpret_cast<floatx4*>(sum + (wave * ROWS + 16 * t + c) * 16 + 4 * q) = acc[t];
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * 16; i += 64 * kFewWaves) {
+        const int64_t m = i >> 4, n = n0 + (i & 15);
+        if (m >= s.rows || n >= p.N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) v += sum[w * ROWS * 16 + i];
+        reinterpret_cast<T*>(p.y)[m * p.ldy + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
+    }
+}
+
 // The mask words alone, for a backward that needs no input gradient.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_mask_kernel(Source<T> s, int steps, uint16_t* bits) {
@@ -813,6 +892,19 @@ hipError_t narrow_linear_t(const Mx4Source& x, const NarrowArgs& p, hipStream_t 
     return x.y ? narrow_linear_masked<T, true>(src, p, s) : narrow_linear_masked<T, false>(src, p, s);
 }
 
+template <typename T>
+hipError_t few_rows_t(const Mx4Source& x, const FewArgs& p, hipStream_t s) {
+    const Source<T> src{(const T*)x.x, nullptr, x.rows, x.cols, x.ldx, 0};
+    const dim3 grid((unsigned)ceil_div(p.N, 16)), block(64 * kFewWaves);
+    if (x.rows <= 16)
+        IA_LAUNCH("mx4_few_rows_kernel", (mx4_few_rows_kernel<T, 1>), grid, block, 0, s, src, p);
+    else if (x.rows <= 32)
+        IA_LAUNCH("mx4_few_rows_kernel", (mx4_few_rows_kernel<T, 2>), grid, block, 0, s, src, p);
+    else
+        IA_LAUNCH("mx4_few_rows_kernel", (mx4_few_rows_kernel<T, 4>), grid, block, 0, s, src, p);
+    return hipGetLastError();
+}
+
 // Blocks and rows a block takes of a narrow gradient: one block a CU, whole
 // blocks of 32 rows.
 constexpr int64_t kGradBlocks = 256;
@@ -906,7 +998,7 @@ bool is_narrow(int64_t K, int64_t N) {
 }
 
 size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) {
-    return is_narrow(K, N) ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+    return is_narrow(K, N) || M <= kFewRows ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
 }
 
 hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
@@ -917,6 +1009,10 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
         const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy,
                            nullptr};
         return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
+    }
+    if (x.rows <= kFewRows) {
+        const FewArgs p{w.codes, w.scales, w.rows, mx4_blocks(x.cols), bias, act, y, ldy};
+        return IA_BY_DTYPE(x.dtype, few_rows_t, x, p, s);
     }
     const Mx4View q = scratch_view(ws, x.rows, x.cols);
     hipError_t e = launch_mx4_quantize(x, false, q, s);

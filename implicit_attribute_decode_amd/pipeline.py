@@ -657,10 +657,12 @@ _ACTS = {"none": ia.IA_ACT_NONE, "relu": ia.IA_ACT_RELU}
 
 def _matrix(t: torch.Tensor, name: str):
     """(dtype, rows, cols, row stride) of a 2-D tensor with unit column stride; a row stride of 0 repeats one row."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, cols] with unit column stride")
-    rows, cols = t.shape
-    return _dtype(t), rows, cols, (t.stride(0) if rows > 1 else cols)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return _dtype(t), rows, cols, (ld if rows > 1 else cols)
 
 
 def _bytes(n: int, device):
@@ -670,22 +672,24 @@ def _bytes(n: int, device):
 class Mx4Tensor:
     """A [rows, cols] matrix in MXFP4: codes uint8 [rows, 16 ceil(cols / 32)]
     (two E2M1 codes a byte, the earlier value in the low half), scales uint8
-    [rows, ceil(cols / 32)] (2^(byte - 127), 255 = NaN)."""
+    [rows, ceil(cols / 32)] (2^(byte - 127), 255 = NaN).  The tensors are not
+    replaced; their values may change (quantised anew)."""
+
+    __slots__ = ("_codes", "_scales", "rows", "cols", "c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         blocks = (cols + 31) // 32
         rows = codes.shape[0]
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda or not scales.is_cuda:
             raise ValueError("codes and scales must be uint8 tensors on the GPU")
-        if (tuple(codes.shape) != (rows, 16 * blocks) or tuple(scales.shape) != (rows, blocks)
+        if (codes.shape != (rows, 16 * blocks) or scales.shape != (rows, blocks)
                 or not codes.is_contiguous() or not scales.is_contiguous()):
             raise ValueError(f"codes [{rows}, {16 * blocks}] and scales [{rows}, {blocks}] expected, contiguous")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
+        self.c = ia.mx4(codes, scales, rows, cols)
 
-    @property
-    def c(self):
-        """The ia_mx4 that describes this matrix."""
-        return ia.mx4(self.codes, self.scales, self.rows, self.cols)
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
@@ -696,7 +700,7 @@ class Mx4Tensor:
     def dequantize(self, dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
         """The values, rounded once to dtype (float32, float16 or bfloat16)."""
         if out is None:
-            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
+            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self._codes.device)
         d, rows, cols, ld = _matrix(out, "out")
         if (rows, cols) != (self.rows, self.cols):
             raise ValueError("out has another shape")
@@ -715,7 +719,7 @@ def mx4_quantize(x: torch.Tensor, transpose: bool = False, out: Mx4Tensor | None
 
 
 def _bias(bias, n: int):
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (n,) or not bias.is_contiguous()
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (n,) or not bias.is_contiguous()
                              or not bias.is_cuda):
         raise ValueError(f"bias must be a contiguous float32 [{n}] on the GPU")
     return bias
@@ -742,10 +746,11 @@ def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: torch.Tensor | None = None, 
     if K != w.cols:
         raise ValueError(f"x has {K} columns, the weights {w.cols}")
     if out is None:
-        out = torch.empty((M, w.rows), dtype=x.dtype, device=x.device)
-    do, rows, cols, ldy = _matrix(out, "out")
-    if (do, rows, cols) != (d, M, w.rows):
-        raise ValueError("out has another shape or type")
+        out, ldy = torch.empty((M, w.rows), dtype=x.dtype, device=x.device), w.rows
+    else:
+        do, rows, cols, ldy = _matrix(out, "out")
+        if (do, rows, cols) != (d, M, w.rows):
+            raise ValueError("out has another shape or type")
     ws = _bytes(ia.ia_mx4_linear_workspace_size(M, K, w.rows), x.device)
     ia.ia_mx4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
     return out
