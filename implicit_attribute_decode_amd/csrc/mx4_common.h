@@ -12,6 +12,8 @@ typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t loose_uintx4 __attribute__((ext_vector_type(4), aligned(2)));  // at any element
 typedef unsigned short ushortx2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 32;  // values per scale
