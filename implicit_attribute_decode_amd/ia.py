@@ -202,7 +202,8 @@ def _stream(stream=None) -> int:
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream(torch.cuda.current_device())
+        # torch.cuda.current_stream().cuda_stream without the Stream object (1.4 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
