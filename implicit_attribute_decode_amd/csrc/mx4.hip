@@ -564,13 +564,14 @@ __global__ void __launch_bounds__(256) mx4_mask_kernel(Source<T> s, int steps, u
 // dw = Qc(d)^T Qc(x) and db = column sums of d for up to 256 x 256 weights:
 // both matrices are read once and quantised along their rows m in registers.
 // A block of 8 waves takes a run of rows in steps of 128.  The columns are cut
-// into panels of 16 lanes x 8 bytes (64 columns, 32 in fp32); in a step each
-// wave loads its panels, lane (q, c) the rows 32 q .. 32 q + 31 of its 8
-// bytes, which hold 4 (2) whole blocks, one for each of 4 (2) MFMA tiles whose
+// into panels of 16 lanes x 4 bytes (32 columns, 16 in fp32); in a step each
+// wave takes every eighth of them, lane (q, c) the rows 32 q .. 32 q + 31 of its 4
+// bytes, which hold 2 (1) whole blocks, one for each of 2 (1) MFMA tiles whose
 // row c is the lane's column.  The codes meet in LDS (two buffers, one barrier
-// a step); wave w multiplies the n tiles 2 w, 2 w + 1 with every k tile.  The
-// next step's loads are in flight meanwhile.  The blocks' sums go to `part` in
-// register order and are added in a fixed order by mx4_narrow_join_kernel.
+// a step); wave w multiplies the n tiles 2 w, 2 w + 1 with every k tile.  Two
+// panels' loads are in flight but for the one being quantised.  The blocks' sums
+// go to `part` in register order and are added in a fixed order by
+// mx4_narrow_join_kernel.
 // Bound by the bytes of d and x.
 template <typename T>
 struct NarrowGradArgs {
@@ -589,18 +590,18 @@ struct NarrowGradArgs {
 constexpr int kGradRows = 128;
 constexpr int kGradTiles = 32;  // n and k tiles of 16 columns
 
-// A lane's share of a panel: 32 rows of 8 bytes, as words.
+// A lane's share of a panel: 32 rows of 4 bytes, as words.
 template <typename T>
 struct Panel {
-    static constexpr int E = 8 / (int)sizeof(T), COLS = 16 * E;
-    uint32_t w[kBlock][2];
-    uint32_t bits[2][E / 2];  // mask words of rows 0..15 and 16..31
+    static constexpr int E = 4 / (int)sizeof(T), COLS = 16 * E;
+    uint32_t w[kBlock];
+    uint16_t bits[2][E];  // mask words of rows 0..15 and 16..31
 };
 
-// Rows row0 + 32 q + k of the lane's columns, zero from row `end` and column
-// `cols` on.  The rows' addresses are uniform, the lane adds 32 bits: `ld` is
-// below kMaxGradStride.  A piece that crosses the last column is read from 8
-// bytes before the row's end and shifted (cols is at least 8 bytes' worth).
+// Rows row0 + 32 q + k of the lane's columns, zero from row `end` on.  The rows'
+// addresses are uniform, the lane adds 32 bits: `ld` is below kMaxGradStride.  A
+// piece that crosses the last column is read from before its place (cols is at
+// least E); shift_panel puts it right.
 constexpr int64_t kMaxGradStride = 1 << 22;
 
 template <typename T>
@@ -615,7 +616,7 @@ __device__ __forceinline__ void load_panel(Panel<T>& v, const T* m, int64_t ld, 
         uint32_t off = (uint32_t)((32 * q * (int)ld + from) * (int)sizeof(T));
         asm volatile("" : "+v"(off));
 #pragma unroll
-        for (int k = 0; k < kBlock; ++k) __builtin_memcpy(v.w[k], base + k * pitch + off, 8);
+        for (int k = 0; k < kBlock; ++k) __builtin_memcpy(&v.w[k], base + k * pitch + off, 4);
     } else {
         const int last = (int)(end - row0) - 1;
         int r = 32 * q;
@@ -623,11 +624,9 @@ __device__ __forceinline__ void load_panel(Panel<T>& v, const T* m, int64_t ld, 
 #pragma unroll
         for (int k = 0; k < kBlock; ++k) {
             const uint32_t off = (uint32_t)((min(r + k, last) * (int)ld + from) * (int)sizeof(T));
-            uint32_t w[2];
-            __builtin_memcpy(w, base + off, 8);
-            const uint32_t keep = (uint32_t)((r + k - last - 1) >> 31);
-            v.w[k][0] = w[0] & keep;
-            v.w[k][1] = w[1] & keep;
+            uint32_t w;
+            __builtin_memcpy(&w, base + off, 4);
+            v.w[k] = w & (uint32_t)((r + k - last - 1) >> 31);
         }
     }
 }
@@ -639,11 +638,7 @@ __device__ __forceinline__ void shift_panel(Panel<T>& v, int cols, int panel, in
     if ((panel + 1) * COLS <= cols) return;
     const int col = panel * COLS + E * c, shift = (col - min(col, cols - E)) * 8 * (int)sizeof(T);
 #pragma unroll
-    for (int k = 0; k < kBlock; ++k) {
-        const uint64_t w = ((uint64_t)v.w[k][1] << 32 | v.w[k][0]) >> (shift & 63);
-        v.w[k][0] = shift < 64 ? (uint32_t)w : 0u;
-        v.w[k][1] = shift < 64 ? (uint32_t)(w >> 32) : 0u;
-    }
+    for (int k = 0; k < kBlock; ++k) v.w[k] = shift < 32 ? v.w[k] >> (shift & 31) : 0u;
 }
 
 // The mask words of the lane's columns (`words` to a group of 16 rows; a
@@ -660,17 +655,17 @@ __device__ __forceinline__ void load_bits(Panel<T>& v, const uint16_t* bits, int
 }
 template <typename T>
 __device__ __forceinline__ uint32_t mask_bits(const Panel<T>& v, int e) {
-    return __builtin_amdgcn_perm(v.bits[1][e >> 1], v.bits[0][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+    return (uint32_t)v.bits[0][e] | (uint32_t)v.bits[1][e] << 16;
 }
 
 // Rows 2 i, 2 i + 1 of column e.
-__device__ __forceinline__ pair_t<float> panel_pair(const Panel<float>& v, int i, int e) {
-    return pair_t<float>{__builtin_bit_cast(float, v.w[2 * i][e]), __builtin_bit_cast(float, v.w[2 * i + 1][e])};
+__device__ __forceinline__ pair_t<float> panel_pair(const Panel<float>& v, int i, int) {
+    return pair_t<float>{__builtin_bit_cast(float, v.w[2 * i]), __builtin_bit_cast(float, v.w[2 * i + 1])};
 }
 template <typename T>
 __device__ __forceinline__ pair_t<T> panel_pair(const Panel<T>& v, int i, int e) {
-    return __builtin_bit_cast(pair_t<T>, __builtin_amdgcn_perm(v.w[2 * i + 1][e >> 1], v.w[2 * i][e >> 1],
-                                                               e & 1 ? 0x07060302u : 0x05040100u));
+    return __builtin_bit_cast(pair_t<T>,
+                              __builtin_amdgcn_perm(v.w[2 * i + 1], v.w[2 * i], e & 1 ? 0x07060302u : 0x05040100u));
 }
 // The pair where its bits 2 i, 2 i + 1 of m are set, else zero.
 __device__ __forceinline__ pair_t<float> keep_pair(pair_t<float> v, uint32_t m, int i) {
@@ -693,34 +688,41 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
     const int64_t begin = (int64_t)blockIdx.x * p.run, end = min(begin + p.run, p.M);
     floatx4 acc[2][16] = {};
     float sum[SUBS][E] = {};
-    Panel<T> v;
+    // panels in turn: one on its way while the other is quantised (in fp32, which
+    // has no registers for it, one)
+    constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;
+    Panel<T> v[AHEAD];
     const int64_t steps = (end - begin + kGradRows - 1) / kGradRows;
-    auto load = [&](int64_t step, int sub) {  // panels from np on are x's
-        const int all = wave * SUBS + sub;
+    auto load = [&](Panel<T>& to, int64_t step, int sub) {  // panels from np on are x's
+        const int all = 8 * sub + wave;
         if (all >= np + kp) return;
         const bool of_d = all < np;
         const int panel = of_d ? all : all - np;
         const int64_t row0 = begin + step * kGradRows;
-        load_panel(v, of_d ? p.d : p.x, of_d ? p.ldd : p.ldx, of_d ? p.N : p.K, panel, q, c, row0, end);
-        if (of_d && p.bits) load_bits(v, p.bits, p.words, panel * COLS + E * c, row0 + 32 * q, end);
+        if (of_d && p.bits) load_bits(to, p.bits, p.words, panel * COLS + E * c, row0 + 32 * q, end);
+        load_panel(to, of_d ? p.d : p.x, of_d ? p.ldd : p.ldx, of_d ? p.N : p.K, panel, q, c, row0, end);
     };
-    if (steps > 0) load(0, 0);
+    if (steps > 0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load(v[i], 0, i);
+    }
     for (int64_t step = 0; step < steps; ++step) {
         const int buf = (int)(step & 1);
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const int panel = wave * SUBS + sub;
+            const int panel = 8 * sub + wave;
+            Panel<T>& from = v[sub % AHEAD];
             if (panel < np + kp) {
                 uint32_t bytes = 0;
-                shift_panel(v, panel < np ? p.N : p.K, panel < np ? panel : panel - np, c);
+                shift_panel(from, panel < np ? p.N : p.K, panel < np ? panel : panel - np, c);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     Values<T> b;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) b.p[i] = panel_pair(v, i, e);
+                    for (int i = 0; i < 16; ++i) b.p[i] = panel_pair(from, i, e);
                     if (panel < np) {
                         if (p.bits) {
-                            const uint32_t m = mask_bits(v, e);
+                            const uint32_t m = mask_bits(from, e);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) b.p[i] = keep_pair(b.p[i], m, i);
                         }
@@ -734,15 +736,17 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
                 }
                 __builtin_memcpy(&scales[buf][lane][panel * E], &bytes, E);
             }
-            if (sub + 1 < SUBS)
-                load(step, sub + 1);
+            if (sub + AHEAD < SUBS)
+                load(from, step, sub + AHEAD);
             else if (step + 1 < steps)
-                load(step + 1, 0);
+                load(from, step + 1, sub + AHEAD - SUBS);
         }
         __syncthreads();
         if (2 * wave < tn) {
-            const intx4 d0 = codes[buf][2 * wave][lane], d1 = codes[buf][2 * wave + 1][lane];
-            const int s0 = scales[buf][lane][2 * wave], s1 = scales[buf][lane][2 * wave + 1];
+            const bool two = 2 * wave + 1 < tn;
+            const int second = two ? 2 * wave + 1 : 2 * wave;
+            const intx4 d0 = codes[buf][2 * wave][lane], d1 = codes[buf][second][lane];
+            const int s0 = scales[buf][lane][2 * wave], s1 = scales[buf][lane][second];
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 if (k < tk) {
@@ -753,13 +757,13 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
                 }
         }
     }
-    if (2 * wave < tn) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h)
+        if (2 * wave + h < tn) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 if (k < tk) p.part[(((int64_t)blockIdx.x * tn + 2 * wave + h) * tk + k) * 64 + lane] = acc[h][k];
-    }
+        }
     if (!p.sums) return;
 #pragma unroll
     for (int sub = 0; sub < SUBS; ++sub)
@@ -768,8 +772,8 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
             float a = sum[sub][e];
             a += __shfl_xor(a, 16, 64);
             a += __shfl_xor(a, 32, 64);
-            const int n = (wave * SUBS + sub) * COLS + E * c + e;
-            if (q == 0 && wave * SUBS + sub < np && n < p.N) p.sums[(int64_t)blockIdx.x * p.N + n] = a;
+            const int n = (8 * sub + wave) * COLS + E * c + e;
+            if (q == 0 && 8 * sub + wave < np && n < p.N) p.sums[(int64_t)blockIdx.x * p.N + n] = a;
         }
 }
 
@@ -921,7 +925,7 @@ GradPlan grad_plan(int64_t M, int64_t N, int64_t K, size_t es) {
     g.run = ceil_div(ceil_div(M, kGradBlocks), kBlock) * kBlock;
     if (g.run < kGradRows) g.run = kGradRows;
     g.blocks = ceil_div(M, g.run);
-    const int64_t e = 8 / (int64_t)es, cols = 16 * e;
+    const int64_t e = 4 / (int64_t)es, cols = 16 * e;
     g.tn = (int)(ceil_div(N, cols) * e);
     g.tk = (int)(ceil_div(K, cols) * e);
     return g;
