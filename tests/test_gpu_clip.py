@@ -93,6 +93,27 @@ def test_rows_of_a_wider_array():
     assert host(empty.norm(1.0)).tolist() == [0.0, 1.0, 1.0]
 
 
+def test_many_dense_and_strided_tensors_of_every_type():
+    """Several launches of either kind, more block sums than one pass adds by itself."""
+    rng = np.random.default_rng(31)
+    g, out, hold = [], [], []
+    for k in range(640):
+        dt = TYPES[k % 3]
+        if k % 7 == 0:
+            wide = _tensors(rng, [5 * (50 + k % 13)], [dt])[0].view(-1, 5)
+            hold.append(wide)
+            g.append(wide[:, 1:4])
+            out.append(torch.empty((wide.shape[0], 3), dtype=dt, device="cuda"))
+        else:
+            g.append(_tensors(rng, [17_000 + 61 * (k % 97)], [dt])[0])
+            out.append(torch.empty_like(g[-1]))
+    before = [_f64(t) for t in g]
+    stats = clip_grad_norm(g, 0.25, out)
+    _check_clip(before, out, stats, 0.25)
+    clip_grad_norm(g, 0.25)
+    assert all(torch.equal(a, o) for a, o in zip(g, out))
+
+
 def test_large_and_small_magnitudes_do_not_overflow():
     """Squares beyond fp32's range, and below it."""
     a = torch.full((5000,), 1e30, device="cuda")

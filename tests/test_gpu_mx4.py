@@ -295,6 +295,51 @@ def test_offsets_past_32_bits():
     assert torch.equal(v[at:], Mx4Tensor(codes[at:].clone(), scales[at:].clone(), K).dequantize(torch.float16))
 
 
+def test_sums_longer_than_32_bit_offsets_reach():
+    """33.5M terms over 130 rows (2.2 GB of codes in one tile's rows): values of
+    0.5 and 1 of either sign, so that every partial sum is exact in fp32."""
+    rows, K = 130, (1 << 25) + 96
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def codes(n):
+        pick = torch.tensor([0x11, 0x12, 0x21, 0x22, 0x91, 0x19, 0xa1, 0x1a, 0xaa, 0x99, 0x9a, 0xa9], device="cuda",
+                            dtype=torch.uint8)
+        # as many of either sign on average: the sums stay small
+        return pick[torch.randint(0, 12, (n, K // 2), generator=gen, device="cuda", dtype=torch.int32)]
+
+    a = torch.cat([codes(26) for _ in range(rows // 26)])
+    b = codes(3)
+    one = lambda n: torch.full((n, K // 32), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    got = mx4_matmul(Mx4Tensor(a, one(rows), K), Mx4Tensor(b, one(3), K))
+    want = torch.zeros((rows, 3), dtype=torch.float64, device="cuda")
+    step = 1 << 22
+    for k in range(0, K, step):
+        n = min(step, K - k)
+        part = lambda c, r: Mx4Tensor(c[:, k // 2:(k + n) // 2].contiguous(),  # noqa: E731
+                                      torch.full((r, n // 32), 127, dtype=torch.uint8, device="cuda"), n).dequantize()
+        want += part(a, rows).double() @ part(b, 3).double().t()
+    assert torch.equal(got.double(), want)
+
+
+def test_backward_of_rows_far_apart():
+    """Row strides beyond what the narrow kernels address."""
+    rng = np.random.default_rng(12)
+    M, N, K, far = 40, 58, 70, (1 << 22) + 8
+    dy, x, y = (_matrix(rng, M, c, torch.float16) for c in (N, K, N))
+    wt = mx4_quantize(_matrix(rng, N, K), transpose=True)
+    want = mx4_linear_backward(dy, x, wt, y)
+
+    def apart(t):
+        return torch.empty(M * far, dtype=torch.float16, device="cuda").as_strided(tuple(t.shape), (far, 1)).copy_(t)
+
+    for args in ((apart(dy), x, y), (dy, apart(x), y), (dy, x, apart(y))):
+        got = mx4_linear_backward(args[0], args[1], wt, args[2])
+        assert torch.equal(got["x"], want["x"])
+        for k in ("weight", "bias"):  # another order of summation
+            ref, scale = O.linear_backward(_f64(dy), _f64(x), np.zeros((N, K)), _f64(y))[k]
+            _assert_near(got[k], ref, scale, M, torch.float32)
+
+
 def test_side_stream_and_graph_replays():
     """The layer's forward and backward on another stream, and replayed from a graph with eager work between."""
     rng = np.random.default_rng(11)
