@@ -368,10 +368,11 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* code
 
 // ------------------------------------------------------- narrow layers, fused
 
-// act(Q(x) w^T + bias) for layers of up to 256 outputs whose weights fit LDS.
-// A lane's share of the MFMA operand is one block of one row, so a wave
-// quantises 16 rows of x in its registers on the way to the matrix cores: x is
-// read once and only y is written.  Bound by those bytes.
+// act(Q(x) w^T + bias) for layers whose weights for up to 256 outputs (64 G) fit
+// LDS; wider layers are taken 256 outputs at a time (blockIdx.y).  A lane's share
+// of the MFMA operand is one block of one row, so a wave quantises 16 rows of x
+// in its registers on the way to the matrix cores: x is read once (once for 256
+// outputs) and only y is written.  Bound by those bytes.
 struct NarrowArgs {
     const uint8_t* w;   // [N][blocks]
     const uint8_t* ws;
@@ -381,9 +382,18 @@ struct NarrowArgs {
     void* y;
     int64_t ldy;
     uint16_t* bits;     // with a mask: [rows / 16][128 steps] words of store_mask, or null
+    bool lines;         // y's rows are whole lines (writes_lines)
 };
 
 constexpr int kNarrowUnits = 14;  // 64 outputs x 128 inputs: 4 KiB of codes, 256 B of scales; within 64 KiB
+
+// Output rows that are whole 128-byte lines, and long, are written past the
+// memory-side cache: 300,000 x 256 -> 256 in fp16 69 -> 64 us.  Rows that share
+// lines must not be: 100,000 x 64 -> 250 in fp32 would take 88 us instead of 29,
+// 300,000 x 192 -> 201 in bf16 130 instead of 58.
+bool writes_lines(const void* y, int64_t ldy, int64_t N, size_t es) {
+    return (uintptr_t)y % 128 == 0 && (size_t)ldy * es % 128 == 0 && (size_t)N * es >= 512;
+}
 
 size_t narrow_lds(int groups, int steps) {
     return (size_t)groups * steps * (4096 + 256) + (size_t)groups * 64 * sizeof(float);
@@ -406,15 +416,16 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
     uint8_t* wsc = reinterpret_cast<uint8_t*>(shared + (size_t)p.steps * NT * 64);  // [step][lane][tile]
     float* sbias = reinterpret_cast<float*>(wsc + (size_t)p.steps * 64 * NT);       // [group][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4, c = lane & 15;
+    const int n0 = (int)blockIdx.y * 64 * G;
     for (int i = threadIdx.x; i < p.steps * NT * 64; i += 256) {
         const int l = i & 63, j = (i >> 6) % NT, step = (i >> 6) / NT;
-        const int n = 64 * (j >> 2) + narrow_column<T>(j & 3, (l & 15) >> 2, l & 3), b = 4 * step + (l >> 4);
+        const int n = n0 + 64 * (j >> 2) + narrow_column<T>(j & 3, (l & 15) >> 2, l & 3), b = 4 * step + (l >> 4);
         const bool in = n < p.N && b < p.blocks;
         const int64_t at = (int64_t)n * p.blocks + b;
         wc[i] = in ? *reinterpret_cast<const intx4*>(p.w + at * 16) : intx4{0, 0, 0, 0};
         wsc[(step * 64 + l) * NT + j] = in ? p.ws[at] : (uint8_t)0;
     }
-    for (int n = threadIdx.x; n < 64 * G; n += 256) sbias[n] = p.bias && n < p.N ? p.bias[n] : 0.0f;
+    for (int n = threadIdx.x; n < 64 * G; n += 256) sbias[n] = p.bias && n0 + n < p.N ? p.bias[n0 + n] : 0.0f;
     __syncthreads();
     T* out = reinterpret_cast<T*>(p.y);
     for (int64_t m0 = ((int64_t)blockIdx.x * 4 + wave) * 16; m0 < s.rows; m0 += (int64_t)gridDim.x * 64) {
@@ -444,7 +455,8 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
             }
         }
         if (m0 + c >= s.rows) continue;
-        T* to = out + (m0 + c) * p.ldy;
+        T* to = out + (m0 + c) * p.ldy + n0;
+        const int N = p.N - n0;
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -454,16 +466,18 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     o[e] = (T)activate(acc[4 * g + (E * h + e) / 4][(E * h + e) % 4] + sbias[n + e], p.act);
-                if (n + E <= p.N) {
-                    // written once, not read here: past the memory-side cache
-                    // (300,000 x 256 -> 256 in fp16 69 -> 64 us)
-                    uintx4 w;
-                    __builtin_memcpy(&w, o, sizeof(w));
-                    __builtin_nontemporal_store(w, reinterpret_cast<loose_uintx4*>(to + n));
+                if (n + E <= N) {
+                    if (p.lines) {
+                        uintx4 w;
+                        __builtin_memcpy(&w, o, sizeof(w));
+                        __builtin_nontemporal_store(w, reinterpret_cast<loose_uintx4*>(to + n));
+                    } else {
+                        __builtin_memcpy(to + n, o, sizeof(o));
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        if (n + e < p.N) to[n + e] = o[e];
+                        if (n + e < N) to[n + e] = o[e];
                 }
             }
     }
@@ -872,11 +886,11 @@ hipError_t dequantize_t(const Mx4View& q, void* x, int64_t ldx, hipStream_t s) {
 
 template <typename T, bool MASK>
 hipError_t narrow_linear_masked(const Source<T>& src, const NarrowArgs& p, hipStream_t s) {
-    const int groups = (p.N + 63) / 64;
+    const int groups = p.N < 256 ? (p.N + 63) / 64 : 4;
     const size_t lds = narrow_lds(groups, p.steps);
     // each block reads the weights once; as many blocks as fit the CUs
     const int64_t tiles = ceil_div(src.rows, 64), most = 256 * (int64_t)(163840 / lds < 8 ? 163840 / lds : 8);
-    const dim3 grid((unsigned)(tiles < most ? tiles : most));
+    const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)((p.N + 255) / 256));
     switch (groups) {
         case 1:
             IA_LAUNCH("mx4_narrow_linear_kernel", (mx4_narrow_linear_kernel<T, 1, MASK>), grid, dim3(256), lds, s, src, p);
@@ -955,7 +969,8 @@ hipError_t narrow_grad_t(const Mx4Source& dy, const Mx4Source& x, const Mx4View&
     uint16_t* bits = dy.y && (dw || db) ? (uint16_t*)((char*)ws + at.bits) : nullptr;
     hipError_t e = hipSuccess;
     if (dx) {
-        const NarrowArgs p{wt.codes, wt.scales, (int)K, (int)blocks, steps, nullptr, IA_ACT_NONE, dx, lddx, bits};
+        const NarrowArgs p{wt.codes, wt.scales, (int)K, (int)blocks, steps, nullptr, IA_ACT_NONE, dx, lddx, bits,
+                           writes_lines(dx, lddx, K, sizeof(T))};
         e = narrow_linear_t<T>(dy, p, s);
     } else if (bits) {
         IA_LAUNCH("mx4_mask_kernel", mx4_mask_kernel<T>, dim3(grid_for(ceil_div(M, 16) * steps * 64)), dim3(256), 0, s,
@@ -1000,22 +1015,30 @@ hipError_t launch_mx4_dequantize(const Mx4View& q, int32_t dtype, void* x, int64
     return IA_BY_DTYPE(dtype, dequantize_t, q, x, ldx, s);
 }
 
-// Whether a layer of K inputs and N outputs goes through the fused kernel.
-bool is_narrow(int64_t K, int64_t N) {
-    return N <= 256 && K > 0 && ceil_div(N, 64) * ceil_div(mx4_blocks(K), 4) <= kNarrowUnits;
+// Whether a layer of M rows, K inputs and N outputs goes through the narrow
+// kernel: where 256 outputs' weights fit LDS, and with more outputs where a row has
+// at most 256 inputs, so that taking it again for each 256 outputs costs little.
+// Against quantising and the tiled product: 150,000 x 32 -> 512 in fp16 81 -> 50 us,
+// 50,000 x 200 -> 2,000 in fp16 133 -> 83, 1,000 x 256 -> 10,000 in fp32 25 -> 20;
+// 200,000 x 380 -> 1,000 in fp32 would be 386 -> 529.
+bool is_narrow(int64_t M, int64_t K, int64_t N) {
+    const int64_t steps = ceil_div(mx4_blocks(K), 4);
+    if (K == 0) return false;
+    if (N <= 256) return ceil_div(N, 64) * steps <= kNarrowUnits;
+    return M > kFewRows && steps <= 2 && N <= 16384;
 }
 
 size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) {
-    return is_narrow(K, N) || M <= kFewRows ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+    return is_narrow(M, K, N) || M <= kFewRows ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
 }
 
 hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
                              int64_t ldy, void* ws, hipStream_t s) {
     if (x.rows == 0 || w.rows == 0) return hipSuccess;
-    if (is_narrow(x.cols, w.rows)) {
+    if (is_narrow(x.rows, x.cols, w.rows)) {
         const int64_t blocks = mx4_blocks(x.cols);
         const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy,
-                           nullptr};
+                           nullptr, writes_lines(y, ldy, w.rows, x.dtype == IA_DTYPE_F32 ? 4 : 2)};
         return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
     }
     if (x.rows <= kFewRows) {
@@ -1055,7 +1078,7 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     float* part = (float*)(at += scratch_bytes(K, M));
     void* mat = at + round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float));
     ColumnOut o{};
-    const bool narrow = dx && M > 0 && is_narrow(N, K);  // dx is a layer of N inputs and K outputs on d
+    const bool narrow = dx && M > 0 && is_narrow(M, N, K);  // dx is a layer of N inputs and K outputs on d
     if (dx && !narrow) {
         o.rcodes = dr.codes;
         o.rscales = dr.scales;
@@ -1067,7 +1090,8 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
         o.blocks = mx4_blocks(M);
     }
     if (db) o.sums = part;
-    hipError_t e = IA_BY_DTYPE(dy.dtype, quantize_tile_t, dy, o, s);
+    hipError_t e = hipSuccess;
+    if (o.rcodes || o.codes || o.sums) e = IA_BY_DTYPE(dy.dtype, quantize_tile_t, dy, o, s);
     if (e == hipSuccess && narrow) e = launch_mx4_linear(dy, wt, nullptr, kMx4NoAct, dx, lddx, nullptr, s);
     if (e == hipSuccess && dx && !narrow) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
     if (e == hipSuccess && dw) {

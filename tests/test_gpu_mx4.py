@@ -181,6 +181,24 @@ def test_linear_strided_repeated_and_into_wider_outputs(dtype):
             assert torch.equal(out[:, 4:4 + N], want) and (out[:, :4] == 3).all() and (out[:, 4 + N:] == 3).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N,K", [(65, 513, 256), (300, 1100, 31), (1000, 2304, 200)])
+def test_linear_of_few_inputs_and_many_outputs(M, N, K, dtype):
+    rng = np.random.default_rng(M + N * K)
+    x, w, bias = _matrix(rng, M, K, dtype), _matrix(rng, N, K), _matrix(rng, 1, N)[0]
+    want, scale = O.linear(_f64(x), _f64(w), _f64(bias), True)
+    wide = torch.full((M, N + 24), 3.0, device="cuda", dtype=dtype)
+    for first in (0, 8, 11):
+        out = wide[:, first:first + N]
+        mx4_linear(x, mx4_quantize(w), bias, "relu", out=out)
+        _assert_near(out, want, scale, K, dtype)
+        assert (wide[:, :first] == 3).all() and (wide[:, first + N:] == 3).all()
+        wide.fill_(3.0)
+    dy = _matrix(rng, M, K, dtype, 1e-2)  # the layer back: K outputs of N inputs
+    back = mx4_linear_backward(dy, wide[:, :N], mx4_quantize(w))["x"]
+    _assert_near(back, *O.linear_backward(_f64(dy), _f64(wide[:, :N]), _f64(w).T)["x"], K, dtype)
+
+
 BACKWARD = [(1, 1, 1), (3, 5, 7), (31, 32, 33), (64, 58, 192), (200, 256, 192), (129, 11, 64), (1000, 56, 32),
             (4099, 58, 250), (33, 300, 70), (260, 515, 300), (20_003, 64, 64)]
 
