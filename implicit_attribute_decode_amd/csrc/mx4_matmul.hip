@@ -153,8 +153,7 @@ struct ScaleRow {
 
 // 32 rows by C columns of sums, which a wave keeps in LDS (16-byte units, unit u
 // of row r in place u ^ r), to the output: a lane takes runs of 16 bytes, so
-// that an instruction writes whole lines.  Written once and not read here: past
-// the memory-side cache.
+// that an instruction writes whole lines.
 template <typename T, int C>
 __device__ __forceinline__ void store_rows(const floatx4* sums, const MatArgs& p, T* out, int64_t m, int64_t n, int lane) {
     constexpr int E = 16 / (int)sizeof(T), L = C / E, UNITS = C / 4;  // values a run, lanes a row
@@ -377,9 +376,18 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* p
     }
 }
 
-// How a product is cut: tiles of 256 x 256 where they fill the 256 CUs, else
-// of 128 x 128, and when those are few the sum over k in up to `splits` parts
-// of at least 4 stages (1,024 values) each, joined in order.
+// How a product is cut.  A CU holds one block of 256 x 256 (half the bytes to
+// copy) or two of 128 x 128, one of which multiplies while the other starts or
+// stores.  Measured, a round of 256 of the former takes 16 + 2.4 stages us, of
+// 512 of the latter 3.5 + 1.7 stages; the larger tiles leave CUs idle in their
+// last round, the smaller ones hardly.  Us with tiles of 256 and of 128:
+//   8,192^3 bf16 369, 452           4,096^3 bf16 54, 60
+//   4,096 x 4,096 -> 4,400 bf16 88, 74       3,328 x 16,384 -> 4,096 bf16 154, 185
+//   20,000 x 1,438 -> 1,548 bf16 79, 67      100,000 x 512 -> 512 f16 72, 61
+//   6,000^3 f16 207, 213            200,000 x 380 -> 1,000 f32 273, 293
+// (in the last line the rule takes tiles of 128).
+// Where blocks of 128 are few, the sum over k goes in up to `splits` parts of
+// at least 4 stages (1,024 values), joined in order.
 struct MatPlan {
     int tile;
     bool wide;  // 64-bit offsets
@@ -389,11 +397,15 @@ struct MatPlan {
 MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
     MatPlan p{};
     p.wide = blocks >= (int64_t)1 << 20;  // 128 rows of 2^25 values: 2^31 bytes
-    p.tile = ceil_div(M, 256) * ceil_div(N, 256) >= 192 && !p.wide ? 256 : 128;
+    const int64_t all = ceil_div(blocks, kStageBlocks);
+    const int64_t large = ceil_div(M, 256) * ceil_div(N, 256), small = ceil_div(M, 128) * ceil_div(N, 128);
+    const double large_us = (double)ceil_div(large, 256) * (16.0 + 2.4 * (double)all);
+    const double small_us = (small > 512 ? (double)small / 512 : 1.0) * (3.5 + 1.7 * (double)all);
+    p.tile = large_us < small_us && !p.wide ? 256 : 128;
     p.tiles_m = ceil_div(M, p.tile);
     p.tiles_n = ceil_div(N, p.tile);
-    const int64_t all = ceil_div(blocks, kStageBlocks), tiles = p.tiles_m * p.tiles_n;
-    int64_t splits = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    int64_t splits = p.tile == 128 && tiles > 0 && tiles < 256 ? 512 / tiles : 1;
     if (splits > all / 4) splits = all / 4;
     if (splits < 1) splits = 1;
     p.stages = ceil_div(ceil_div(all, splits), 2) * 2;  // whole groups of 16 scales

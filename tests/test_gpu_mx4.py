@@ -155,6 +155,15 @@ def test_matmul(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N,K", [(3900, 4087, 2999), (4090, 3850, 4800)])
+def test_matmul_of_many_long_rows(M, N, K, dtype):
+    rng = np.random.default_rng(M + N + K)
+    a, b, bias = _matrix(rng, M, K), _matrix(rng, N, K), _matrix(rng, 1, N)[0]
+    want, scale = O.product(O.values(_f64(a)), O.values(_f64(b)), _f64(bias), True)
+    _assert_near(mx4_matmul(mx4_quantize(a), mx4_quantize(b), bias, "relu", dtype), want, scale, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
 def test_linear(M, N, K, dtype):
     rng = np.random.default_rng(M * N + K)
