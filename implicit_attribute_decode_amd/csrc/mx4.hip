@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(256) mx4_narrow_linear_kernel(Source<T> s, Nar
 // ------------------------------------------------------------ few rows
 
 // act(Q(x) w^T + bias) for up to 64 rows (16 MT), where the weights are what
-// there is to read: a block of 8 waves takes 16 outputs, each wave every eighth
+// there is to read (1 x 4,096 -> 4,096 in fp16: 8.9 MB in 5.2 us, most of it the
+// launch and one round of loads): a block of 8 waves takes 16 outputs, each wave every eighth
 // step of 128 inputs.  The weights of a chunk are loaded first; while they come,
 // the block quantises the chunk of x once, one block of 32 a thread, into LDS,
 // where every wave takes it as its operand.  The waves' sums meet in LDS and
@@ -1028,23 +1029,40 @@ bool is_narrow(int64_t M, int64_t K, int64_t N) {
     return M > kFewRows && steps <= 2 && N <= 16384;
 }
 
+// Whether a layer goes through the few rows' kernel.  Each block quantises all of
+// x, a chunk of kFewUnits blocks at a time, so chunks have to be few, and blocks
+// not more than run at once.  fp16, us against quantising and the tiled product:
+//   1 x 256 -> 256 4, 8                  64 x 1,024 -> 4,096 7, 13
+//   1 x 4,096 -> 4,096 5, 15             64 x 4,096 -> 64 (fp32) 34, 18
+//   7 x 16,384 -> 256 15, 15             32 x 8,192 -> 2,048 17, 17
+//   1 x 32,768 -> 16 20, 13              4 x 8,192 -> 32,768 48, 40
+bool is_few(int64_t M, int64_t K, int64_t N) {
+    if (M > kFewRows) return false;
+    const int64_t chunk = kFewUnits / (M <= 16 ? 16 : M <= 32 ? 32 : 64);
+    const int64_t chunks = ceil_div(mx4_blocks(K), chunk);
+    return chunks <= (M <= 16 ? 4 : 2) && chunks * ceil_div(N, 16) <= 1024;
+}
+
 size_t mx4_linear_workspace(int64_t M, int64_t K, int64_t N) {
-    return is_narrow(M, K, N) || M <= kFewRows ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+    return is_few(M, K, N) || is_narrow(M, K, N) ? 0 : scratch_bytes(M, K) + mx4_matmul_workspace(M, N, K);
+}
+
+hipError_t launch_narrow_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y, int64_t ldy,
+                                hipStream_t s) {
+    const int64_t blocks = mx4_blocks(x.cols);
+    const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy,
+                       nullptr, writes_lines(y, ldy, w.rows, x.dtype == IA_DTYPE_F32 ? 4 : 2)};
+    return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
 }
 
 hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* bias, int32_t act, void* y,
                              int64_t ldy, void* ws, hipStream_t s) {
     if (x.rows == 0 || w.rows == 0) return hipSuccess;
-    if (is_narrow(x.rows, x.cols, w.rows)) {
-        const int64_t blocks = mx4_blocks(x.cols);
-        const NarrowArgs p{w.codes, w.scales, (int)w.rows, (int)blocks, (int)ceil_div(blocks, 4), bias, act, y, ldy,
-                           nullptr, writes_lines(y, ldy, w.rows, x.dtype == IA_DTYPE_F32 ? 4 : 2)};
-        return IA_BY_DTYPE(x.dtype, narrow_linear_t, x, p, s);
-    }
-    if (x.rows <= kFewRows) {
+    if (is_few(x.rows, x.cols, w.rows)) {
         const FewArgs p{w.codes, w.scales, w.rows, mx4_blocks(x.cols), bias, act, y, ldy};
         return IA_BY_DTYPE(x.dtype, few_rows_t, x, p, s);
     }
+    if (is_narrow(x.rows, x.cols, w.rows)) return launch_narrow_linear(x, w, bias, act, y, ldy, s);
     const Mx4View q = scratch_view(ws, x.rows, x.cols);
     hipError_t e = launch_mx4_quantize(x, false, q, s);
     if (e != hipSuccess) return e;
@@ -1092,7 +1110,7 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     if (db) o.sums = part;
     hipError_t e = hipSuccess;
     if (o.rcodes || o.codes || o.sums) e = IA_BY_DTYPE(dy.dtype, quantize_tile_t, dy, o, s);
-    if (e == hipSuccess && narrow) e = launch_mx4_linear(dy, wt, nullptr, kMx4NoAct, dx, lddx, nullptr, s);
+    if (e == hipSuccess && narrow) e = launch_narrow_linear(dy, wt, nullptr, kMx4NoAct, dx, lddx, s);
     if (e == hipSuccess && dx && !narrow) e = launch_mx4_matmul(dr, wt, nullptr, kMx4NoAct, dy.dtype, dx, lddx, mat, s);
     if (e == hipSuccess && dw) {
         e = launch_mx4_quantize(x, true, xc, s);

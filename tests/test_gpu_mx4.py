@@ -191,6 +191,16 @@ def test_linear_strided_repeated_and_into_wider_outputs(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N,K", [(1, 50, 16_000), (4, 2100, 8192), (20, 33, 3999), (64, 40, 2017), (64, 256, 8190),
+                                   (1, 16, 30_001), (3, 20_000, 100)])
+def test_linear_of_few_rows(M, N, K, dtype):
+    rng = np.random.default_rng(M + N + K)
+    x, w, bias = _matrix(rng, M, K + 3, dtype)[:, 3:], _matrix(rng, N, K), _matrix(rng, 1, N)[0]
+    want, scale = O.linear(_f64(x), _f64(w), _f64(bias), True)
+    _assert_near(mx4_linear(x, mx4_quantize(w), bias, "relu"), want, scale, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("M,N,K", [(65, 513, 256), (300, 1100, 31), (1000, 2304, 200)])
 def test_linear_of_few_inputs_and_many_outputs(M, N, K, dtype):
     rng = np.random.default_rng(M + N * K)
