@@ -352,27 +352,45 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) mx4_matmul_kernel(MatA
 }
 
 // The splits of a long sum added in a fixed order: c = act(sum of part[s] +
-// bias).  A wave takes every fourth split of 64 neighbouring outputs.
-template <typename T>
+// bias).  A thread adds four neighbouring outputs over every WAYS-th split, and
+// the WAYS waves' sums meet in LDS.
+template <typename T, int WAYS>
 __global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* part, int splits) {
-    __shared__ float sum[4][64];
+    __shared__ floatx4 sum[WAYS][256 / WAYS];
     const int64_t total = p.M * p.N;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t base = (int64_t)blockIdx.x * 64; base < total; base += (int64_t)gridDim.x * 64) {
-        const int64_t i = base + lane;
-        float v = 0.0f;
-        if (i < total) {
+    const int way = threadIdx.x / (256 / WAYS), u = threadIdx.x % (256 / WAYS);
+    const int64_t i = ((int64_t)blockIdx.x * (256 / WAYS) + u) * 4;
+    floatx4 v = {};
+    if (i + 4 <= total) {
 #pragma unroll 8
-            for (int s = wave; s < splits; s += 4) v += part[s * total + i];
+        for (int s = way; s < splits; s += WAYS) {
+            floatx4 w;
+            __builtin_memcpy(&w, part + s * total + i, sizeof(w));
+            v += w;
         }
-        sum[wave][lane] = v;
+    } else {
+        for (int s = way; s < splits; s += WAYS)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < total) v[e] += part[s * total + i + e];
+    }
+    if (WAYS > 1) {
+        sum[way][u] = v;
         __syncthreads();
-        if (wave == 0 && i < total) {
-            const int64_t m = i / p.N, n = i - m * p.N;
-            v = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
-            reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v + (p.bias ? p.bias[n] : 0.0f), p.act);
+        if (way != 0) return;
+#pragma unroll
+        for (int w = 1; w < WAYS; ++w) v += sum[w][u];
+    }
+    if (i >= total) return;
+    int64_t m = i / p.N, n = i - m * p.N;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (i + e >= total) return;
+        reinterpret_cast<T*>(p.c)[m * p.ldc + n] = (T)activate(v[e] + (p.bias ? p.bias[n] : 0.0f), p.act);
+        if (++n == p.N) {
+            n = 0;
+            ++m;
         }
-        __syncthreads();
     }
 }
 
@@ -387,7 +405,8 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* p
 //   6,000^3 f16 207, 213            200,000 x 380 -> 1,000 f32 273, 293
 // (in the last line the rule takes tiles of 128).
 // Where blocks of 128 are few, the sum over k goes in up to `splits` parts of
-// at least 4 stages (1,024 values), joined in order.
+// at least 4 stages (1,024 values), joined in order: 130 tiles of 68 stages so
+// 60 us, whole 85; but 225 tiles of 10 stages would take 29 instead of 20.
 struct MatPlan {
     int tile;
     bool wide;  // 64-bit offsets
@@ -405,7 +424,8 @@ MatPlan mat_plan(int64_t M, int64_t N, int64_t blocks) {
     p.tiles_m = ceil_div(M, p.tile);
     p.tiles_n = ceil_div(N, p.tile);
     const int64_t tiles = p.tiles_m * p.tiles_n;
-    int64_t splits = p.tile == 128 && tiles > 0 && tiles < 256 ? 512 / tiles : 1;
+    const bool few = tiles <= 128 || (tiles < 256 && all >= 32);
+    int64_t splits = p.tile == 128 && tiles > 0 && few ? 512 / tiles : 1;
     if (splits > all / 4) splits = all / 4;
     if (splits < 1) splits = 1;
     p.stages = ceil_div(ceil_div(all, splits), 2) * 2;  // whole groups of 16 scales
@@ -441,8 +461,13 @@ hipError_t matmul_t(MatArgs p, void* ws, hipStream_t s) {
     part.ldc = p.N;
     hipError_t e = launch_tiles<float>(part, plan, s);
     if (e != hipSuccess) return e;
-    IA_LAUNCH("mx4_join_kernel", mx4_join_kernel<T>, dim3(grid_for(p.M * p.N * 4)), dim3(256), 0, s, p, (const float*)ws,
-              plan.splits);
+    const int64_t quads = ceil_div(p.M * p.N, 4);
+    if (plan.splits >= 8)
+        IA_LAUNCH("mx4_join_kernel", (mx4_join_kernel<T, 4>), dim3((unsigned)ceil_div(quads, 64)), dim3(256), 0, s, p,
+                  (const float*)ws, plan.splits);
+    else
+        IA_LAUNCH("mx4_join_kernel", (mx4_join_kernel<T, 1>), dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, p,
+                  (const float*)ws, plan.splits);
     return hipGetLastError();
 }
 
