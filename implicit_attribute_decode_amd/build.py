@@ -24,8 +24,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 
-# Per-source flags.  The decoder MLP and MXFP4 product kernels need
-# far fewer than 256 registers per lane, so their MFMA accumulators stay in
+# Per-source flags.  The decoder MLP and MXFP4 product kernels fit 256
+# registers per lane, so their MFMA accumulators stay in
 # ordinary VGPRs: with accumulation registers the compiler moves every result
 # out with one v_accvgpr_read before its activation (about a tenth of the
 # backward's VALU instructions).

