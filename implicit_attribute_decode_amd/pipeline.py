@@ -74,12 +74,13 @@ class Decoder:
 
     def _out(self, N, out):
         if out is None:
-            out = dict(scales=torch.empty((N, 3), device=self.device), quats=torch.empty((N, 4), device=self.device),
-                       opacity=torch.empty((N,), device=self.device))
+            out = dict(scales=torch.empty((N, 3), dtype=torch.float32, device=self.device),
+                       quats=torch.empty((N, 4), dtype=torch.float32, device=self.device),
+                       opacity=torch.empty((N,), dtype=torch.float32, device=self.device))
             if self.sh:
-                out["sh"] = torch.empty((N, 16, 3), device=self.device)
+                out["sh"] = torch.empty((N, 16, 3), dtype=torch.float32, device=self.device)
             else:
-                out["colors"] = torch.empty((N, 3), device=self.device)
+                out["colors"] = torch.empty((N, 3), dtype=torch.float32, device=self.device)
         return out
 
     def _gaussians(self, out):
@@ -128,7 +129,7 @@ class Decoder:
         out = dict(tables=torch.empty(self._tables.shape, dtype=torch.float32, device=self.device),
                    weights=[torch.empty(w.shape, dtype=torch.float32, device=self.device) for w in self._W],
                    biases=[torch.empty(b.shape, dtype=torch.float32, device=self.device) for b in self._b])
-        out["pos"] = torch.empty((N, 3), device=self.device) if want_pos else None
+        out["pos"] = torch.empty((N, 3), dtype=torch.float32, device=self.device) if want_pos else None
         wp = [ia._ptr(w) for w in out["weights"]] + [None] * (12 - len(out["weights"]))
         bp = [ia._ptr(b) for b in out["biases"]] + [None] * (12 - len(out["biases"]))
         G = ia.DecoderGrads(ia._ptr(out["tables"]), (ia.C.c_void_p * 12)(*wp), (ia.C.c_void_p * 12)(*bp))
@@ -265,7 +266,7 @@ class Renderer:
         out = out or {}
         image = out.get("image")
         if image is None:
-            image = torch.empty((F, 3, H, W), device=self.device)
+            image = torch.empty((F, 3, H, W), dtype=torch.float32, device=self.device)
         means = g["means"]
         stride = int(means.stride(0)) if means.dim() == 2 else 3
         sh = g.get("sh")
@@ -277,7 +278,7 @@ class Renderer:
             A = ia.RenderAux()
             A.binning = int(binning)
         if aux:
-            res["T_final"] = torch.empty((F, H, W), device=self.device)
+            res["T_final"] = torch.empty((F, H, W), dtype=torch.float32, device=self.device)
             res["n_contrib"] = torch.empty((F, H, W), dtype=torch.int32, device=self.device)
             res["n_entries"] = torch.zeros(1, dtype=torch.int64, device=self.device)
             res["overflow"] = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -309,11 +310,11 @@ class Renderer:
         stride = int(means.stride(0)) if means.dim() == 2 else 3
         G = ia.gaussians(means=means, scales=g["scales"], quats=g["quats"], colors=g.get("colors"), sh=g.get("sh"),
                          opacity=g["opacity"], means_stride=stride, sh_degree=3 if g.get("sh") is not None else -1)
-        out = {k: torch.empty(shape, device=self.device)
+        out = {k: torch.empty(shape, dtype=torch.float32, device=self.device)
                for k, shape in (("means", (N, 3)), ("scales", (N, 3)), ("quats", (N, 4)), ("opacity", (N,)),
                                 ("colors", (N, 3)))}
         if g.get("sh") is not None:
-            out["sh"] = torch.empty((N, 16, 3), device=self.device)
+            out["sh"] = torch.empty((N, 16, 3), dtype=torch.float32, device=self.device)
         GG = ia.GaussianGrads(*[ia._ptr(out.get(k)) for k in ("means", "scales", "quats", "opacity", "colors", "sh")])
         ia.ia_render_backward(G, fo, cams, ws, max_entries, grad_image.contiguous(), res["T_final"],
                               res["n_contrib"], GG)
@@ -385,8 +386,8 @@ class Adam:
     def __init__(self, groups: dict, warmup: int, total: int, beta1: float = 0.9, beta2: float = 0.999,
                  eps: float = 1e-15):
         self.groups = groups  # name -> {"param": fp32 tensor, "lr": base, optional "f16": tensor}
-        self.state = {k: (torch.zeros(g["param"].shape, device=g["param"].device),
-                          torch.zeros(g["param"].shape, device=g["param"].device)) for k, g in groups.items()}
+        self.state = {k: tuple(torch.zeros(g["param"].shape, dtype=torch.float32, device=g["param"].device)
+                               for _ in range(2)) for k, g in groups.items()}
         self.warmup, self.total = warmup, total
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
         self.t = 0
@@ -444,7 +445,7 @@ class Adam:
                            0 if f16 is None else f16.data_ptr(), rows, dim, stride, rate)
             at += pack.size
         device = p.device if names else "cuda"
-        stats = torch.empty(3, device=device)
+        stats = torch.empty(3, dtype=torch.float32, device=device)
         ws = torch.empty(ia.ia_clip_workspace_size(len(names)), dtype=torch.uint8, device=device)
         ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t, ws, stats)
         return stats
@@ -498,7 +499,7 @@ class GradClip:
         self._ws_bytes = ia.ia_clip_workspace_size(len(self.grads))
 
     def _call(self, fn, max_norm):
-        stats = torch.empty(3, device=self.device)
+        stats = torch.empty(3, dtype=torch.float32, device=self.device)
         fn(self._arr, max_norm, torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device), stats)
         return stats
 
@@ -522,9 +523,9 @@ def densify_positions(xyzt, grad_acc, grad_count, attrs: dict, m, v, noise, grad
     one host synchronisation."""
     N = int(xyzt.shape[0])
     dev = xyzt.device
-    out_x = torch.empty((2 * N, 4), device=dev)
-    out_m = torch.empty((2 * N, 3), device=dev)
-    out_v = torch.empty((2 * N, 3), device=dev)
+    out_x = torch.empty((2 * N, 4), dtype=torch.float32, device=dev)
+    out_m = torch.empty((2 * N, 3), dtype=torch.float32, device=dev)
+    out_v = torch.empty((2 * N, 3), dtype=torch.float32, device=dev)
     out_n = torch.zeros(1, dtype=torch.int64, device=dev)
     ws = torch.empty(max(ia.ia_densify_workspace_size(N), 256), dtype=torch.uint8, device=dev)
     p = ia.DensifyParams(grad_threshold, scale_threshold, min_opacity)
@@ -774,8 +775,8 @@ def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, wt: Mx4Tensor | None,
     if want_x and (wt is None or (wt.rows, wt.cols) != (K, N)):
         raise ValueError(f"wt must be [{K}, {N}]")
     dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
-    dw = torch.empty((N, K), device=x.device)
-    db = torch.empty(N, device=x.device)
+    dw = torch.empty((N, K), dtype=torch.float32, device=x.device)
+    db = torch.empty(N, dtype=torch.float32, device=x.device)
     ws = _bytes(ia.ia_mx4_linear_backward_workspace_size(M, N, K), x.device)
     ia.ia_mx4_linear_backward(dy, lddy, y, ldy, x, ldx, d, M, N, K, wt.c if want_x else None, dx, K, dw, db, ws)
     return {"x": dx, "weight": dw, "bias": db}
