@@ -423,6 +423,8 @@ def ia_adam_step_strided(param, grad, m, v, lr: float, beta1: float, beta2: floa
     rows, dim = (int(d) for d in param.shape)
     if param.stride(1) != 1 or tuple(grad.shape) != (rows, dim) or not grad.is_contiguous():
         raise ValueError("param must be [rows, dim] with unit column stride; grad, m, v dense [rows, dim]")
+    if max(dim, param.stride(0)) > 2 ** 31 - 1:  # the arguments would keep the low bits
+        raise ValueError("param's rows are more than 2^31 - 1 floats apart")
     _check(load().ia_adam_step_strided(_ptr(param), int(param.stride(0)), dim, _ptr(grad), _ptr(m), _ptr(v), rows,
                                        float(lr), float(beta1), float(beta2), float(eps), int(step),
                                        _stream(stream)))

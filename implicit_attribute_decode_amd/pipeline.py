@@ -451,6 +451,7 @@ class Adam:
         return stats
 
 
+_INT32_MAX = 2 ** 31 - 1
 _DTYPES = {torch.float32: ia.IA_DTYPE_F32, torch.float16: ia.IA_DTYPE_F16, torch.bfloat16: ia.IA_DTYPE_BF16}
 
 
@@ -489,6 +490,8 @@ class GradClip:
             if g.is_contiguous() and o.is_contiguous():
                 d.rows, d.dim, d.stride, d.out_stride = g.numel(), 1, 1, 1
             elif g.dim() == 2 and all(t.shape[1] <= 1 or t.stride(1) == 1 for t in (g, o)):
+                if max(g.shape[1], g.stride(0), o.stride(0)) > _INT32_MAX:  # the fields would keep the low bits
+                    raise ValueError(f"gradient {k}: rows of more than 2^31 - 1 elements, or as far apart")
                 d.rows, d.dim, d.stride, d.out_stride = g.shape[0], max(g.shape[1], 1), g.stride(0), o.stride(0)
                 if g.shape[1] == 0:
                     d.rows, d.stride, d.out_stride = 0, 1, 1
