@@ -12,6 +12,7 @@
 #include <string>
 
 #include "ia_internal.h"
+#include "ranges.h"
 
 namespace {
 
@@ -1020,16 +1021,10 @@ constexpr int64_t kMaxElements = int64_t(1) << 40;
 // rows x dim is within [0, 2^40] (dim >= 1)
 bool size_ok(int64_t rows, int64_t dim) { return rows >= 0 && dim >= 1 && rows <= kMaxElements / dim; }
 
-// Byte ranges [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
+// rows `stride` elements apart stay within 2^56 bytes
+bool extent_ok(int64_t rows, int64_t stride) { return stride <= (int64_t(1) << 54) / rows; }
 
-// Bytes from the first to the last element of rows of `cols` elements `ld` apart.
-size_t extent(int64_t rows, int64_t cols, int64_t ld, size_t es) {
-    return rows == 0 || cols == 0 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * es;
-}
+constexpr char kClash[] = "memory that the call writes overlaps other memory of the call";
 
 ia_status check_clip(int32_t count, float max_norm, const void* ws, size_t ws_bytes, const float* stats) {
     if (count < 0) return fail(IA_ERR_INVALID_ARG, "count must be >= 0");
@@ -1038,7 +1033,29 @@ ia_status check_clip(int32_t count, float max_norm, const void* ws, size_t ws_by
     return check_ws(ws, ws_bytes, ia::clip_workspace(count));
 }
 
-ia_status check_grads(const ia_grad* grads, int32_t count, bool outputs) {
+// Nothing that a norm (a clipping, with `outputs`) writes overlaps anything else.
+ia_status check_grad_ranges(const ia_grad* grads, int32_t count, bool outputs, const void* ws, const float* stats) {
+    ia::Ranges r;
+    if (!r.reserve(2 * (size_t)count + 2)) return fail(IA_ERR_OUT_OF_MEMORY, "no host memory to check the tensors");
+    const auto in_place = [&](const ia_grad& g) {
+        return outputs && (!g.out || (g.out == g.data && g.out_stride == g.stride));
+    };
+    for (int32_t k = 0; k < count; ++k)
+        r.add(ia::rows_of(grads[k].data, grads[k].rows, grads[k].dim, grads[k].stride, dtype_size(grads[k].dtype),
+                          in_place(grads[k])));
+    r.run_done();
+    for (int32_t k = 0; k < (outputs ? count : 0); ++k)
+        if (!in_place(grads[k]))
+            r.add(ia::rows_of(grads[k].out, grads[k].rows, grads[k].dim, grads[k].out_stride,
+                              dtype_size(grads[k].dtype), true));
+    r.run_done();
+    r.add(ia::bytes_of(ws, ia::clip_workspace(count), true));
+    r.add(ia::bytes_of(stats, 3 * sizeof(float), true));
+    r.run_done();
+    return r.clash() ? fail(IA_ERR_INVALID_ARG, kClash) : IA_OK;
+}
+
+ia_status check_grads(const ia_grad* grads, int32_t count) {
     if (count > 0 && !grads) return fail(IA_ERR_INVALID_ARG, "grads is null");
     int64_t total = 0;
     for (int32_t k = 0; k < count; ++k) {
@@ -1050,13 +1067,33 @@ ia_status check_grads(const ia_grad* grads, int32_t count, bool outputs) {
         if (g.stride < g.dim || (g.out && g.out_stride < g.dim))
             return fail(IA_ERR_INVALID_ARG, "a stride is below dim");
         if (g.rows == 0) continue;
+        if (!extent_ok(g.rows, g.stride) || (g.out && !extent_ok(g.rows, g.out_stride)))
+            return fail(IA_ERR_INVALID_ARG, "rows too far apart");
         if (!g.data || !aligned(g.data, es) || !aligned(g.out, es))
             return fail(IA_ERR_INVALID_ARG, "a gradient is null or misaligned");
-        if (outputs && g.out && !(g.out == g.data && g.out_stride == g.stride) &&
-            overlap(g.data, extent(g.rows, g.dim, g.stride, es), g.out, extent(g.rows, g.dim, g.out_stride, es)))
-            return fail(IA_ERR_INVALID_ARG, "out overlaps data");
     }
     return IA_OK;
+}
+
+ia_status check_group_ranges(const ia_adam_group* groups, int32_t count, const void* ws, const float* stats) {
+    ia::Ranges r;
+    if (!r.reserve(5 * (size_t)count + 2)) return fail(IA_ERR_OUT_OF_MEMORY, "no host memory to check the groups");
+    const auto dense = [&](auto member, size_t es, bool written) {
+        for (int32_t k = 0; k < count; ++k)
+            r.add(ia::rows_of(groups[k].*member, groups[k].rows, groups[k].dim, groups[k].dim, es, written));
+        r.run_done();
+    };
+    for (int32_t k = 0; k < count; ++k)
+        r.add(ia::rows_of(groups[k].param, groups[k].rows, groups[k].dim, groups[k].param_stride, 4, true));
+    r.run_done();
+    dense(&ia_adam_group::grad, 4, false);
+    dense(&ia_adam_group::m, 4, true);
+    dense(&ia_adam_group::v, 4, true);
+    dense(&ia_adam_group::param_f16, 2, true);
+    r.add(ia::bytes_of(ws, ia::clip_workspace(count), true));
+    r.add(ia::bytes_of(stats, 3 * sizeof(float), true));
+    r.run_done();
+    return r.clash() ? fail(IA_ERR_INVALID_ARG, kClash) : IA_OK;
 }
 
 }  // namespace
@@ -1073,7 +1110,8 @@ ia_status ia_clip_workspace_size(int32_t count, size_t* bytes) {
 ia_status ia_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes, float* stats,
                        void* stream) {
     ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
-    if (st == IA_OK) st = check_grads(grads, count, false);
+    if (st == IA_OK) st = check_grads(grads, count);
+    if (st == IA_OK) st = check_grad_ranges(grads, count, false, ws, stats);
     if (st != IA_OK) return st;
     hipError_t e = ia::launch_grad_norm(grads, count, max_norm, ws, stats, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "gradient norm launch");
@@ -1083,7 +1121,8 @@ ia_status ia_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void
 ia_status ia_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes,
                             float* stats, void* stream) {
     ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
-    if (st == IA_OK) st = check_grads(grads, count, true);
+    if (st == IA_OK) st = check_grads(grads, count);
+    if (st == IA_OK) st = check_grad_ranges(grads, count, true, ws, stats);
     if (st != IA_OK) return st;
     hipError_t e = ia::launch_clip_grad_norm(grads, count, max_norm, ws, stats, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "gradient clipping launch");
@@ -1110,7 +1149,10 @@ ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float ma
         if (!aligned(g.param, 4) || !aligned(g.grad, 4) || !aligned(g.m, 4) || !aligned(g.v, 4) ||
             !aligned(g.param_f16, 2))
             return fail(IA_ERR_INVALID_ARG, "a group's array is misaligned");
+        if (!extent_ok(g.rows, g.param_stride)) return fail(IA_ERR_INVALID_ARG, "rows too far apart");
     }
+    st = check_group_ranges(groups, count, ws, stats);
+    if (st != IA_OK) return st;
     hipError_t e = ia::launch_adam_clip(groups, count, max_norm, beta1, beta2, eps, step, ws, stats,
                                         (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "clipped adam launch");

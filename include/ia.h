@@ -591,8 +591,9 @@ IA_API ia_status ia_densify(const float* xyzt, const float* grad_acc, const int3
 typedef struct {
     void* data;         /* device, dtype (written only where out is NULL)      */
     void* out;          /* device, dtype: where ia_clip_grad_norm writes; NULL:
-                           in place.  Must not overlap data unless equal to it
-                           with the same stride                                */
+                           in place.  Must not overlap the data or out of any
+                           tensor of the call, its own data excepted where it
+                           is equal to it with the same stride                 */
     int64_t rows;
     int32_t dim;
     int32_t stride;     /* >= dim                                              */
@@ -621,8 +622,9 @@ IA_API ia_status ia_clip_workspace_size(int32_t count, size_t* bytes);
  *          256-byte aligned.
  * Asynchronous on stream; no host synchronisation.
  * Errors: INVALID_ARG (null, negative sizes, stride < dim, misalignment, over
- * 2^40 elements, max_norm negative or NaN), UNSUPPORTED (dtype),
- * WORKSPACE_TOO_SMALL, DEVICE. */
+ * 2^40 elements, max_norm negative or NaN, memory that is written - stats, ws,
+ * outputs - shared with other memory of the call), UNSUPPORTED (dtype),
+ * WORKSPACE_TOO_SMALL, DEVICE, OUT_OF_MEMORY (host). */
 IA_API ia_status ia_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, size_t ws_bytes,
                               float* stats, void* stream);
 
@@ -656,7 +658,9 @@ typedef struct {
  * mirror changes (stats tells).  groups: host [count], read before the call
  * returns; stats, ws as ia_grad_norm.
  * Errors: INVALID_ARG (also step < 1, betas outside [0, 1), negative or NaN
- * eps or lr, dim < 1, param_stride < dim), WORKSPACE_TOO_SMALL, DEVICE. */
+ * eps or lr, dim < 1, param_stride < dim, a parameter, moment or mirror that
+ * shares memory with another array of the call), WORKSPACE_TOO_SMALL, DEVICE,
+ * OUT_OF_MEMORY (host). */
 IA_API ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
                                    float eps, int32_t step, void* ws, size_t ws_bytes, float* stats, void* stream);
 

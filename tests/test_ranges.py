@@ -1,0 +1,167 @@
+"""The host's overlap check (csrc/ranges.h) against a byte-by-byte count, and the
+calls that it refuses.  The refusals pass addresses that nothing dereferences:
+every one of them returns before anything is enqueued."""
+import ctypes as C
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+from implicit_attribute_decode_amd import ia
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SOURCE = """
+#include "ranges.h"
+// ranges: n x {at, rows, cols, ld, element size, written}, in `runs` runs of equal length
+extern "C" int clash_few(const int64_t* v, int n) {
+    ia::Rows r[64];
+    for (int i = 0; i < n; ++i)
+        r[i] = ia::rows_of((const void*)v[6 * i], v[6 * i + 1], v[6 * i + 2], v[6 * i + 3], v[6 * i + 4], v[6 * i + 5]);
+    return ia::clash(r, n);
+}
+extern "C" int clash_many(const int64_t* v, int n, int runs) {
+    ia::Ranges r;
+    if (!r.reserve(n)) return -1;
+    for (int i = 0; i < n; ++i) {
+        r.add(ia::rows_of((const void*)v[6 * i], v[6 * i + 1], v[6 * i + 2], v[6 * i + 3], v[6 * i + 4], v[6 * i + 5]));
+        if ((i + 1) % (n / runs) == 0) r.run_done();
+    }
+    r.run_done();
+    return r.clash();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    d = tmp_path_factory.mktemp("ranges")
+    (d / "ranges.cpp").write_text(SOURCE)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "implicit_attribute_decode_amd", "csrc"), str(d / "ranges.cpp"), "-o",
+                    str(d / "ranges.so")], check=True)
+    return C.CDLL(str(d / "ranges.so"))
+
+
+def _bytes(at, rows, cols, ld, es):
+    return {at + (r * ld + c) * es + b for r in range(rows) for c in range(cols) for b in range(es)}
+
+
+def _clash(ranges):
+    b = [_bytes(*r[:5]) for r in ranges]
+    return any((ranges[i][5] or ranges[j][5]) and b[i] & b[j] for i in range(len(b)) for j in range(i))
+
+
+def _check(lib, ranges):
+    v = np.array(ranges, np.int64)
+    ptr = v.ctypes.data_as(C.c_void_p)
+    want = int(_clash(ranges))
+    assert lib.clash_few(ptr, len(ranges)) == want, ranges
+    for runs in (1, 2, len(ranges)):
+        assert lib.clash_many(ptr, len(ranges), runs) == want, ranges
+    return want
+
+
+def test_pairs_agree_with_a_count_of_bytes(lib):
+    rng = np.random.default_rng(1)
+    seen = [0, 0]
+    for _ in range(6000):
+        pair = []
+        for _ in range(2):
+            es, cols = int(rng.choice([1, 2, 4])), int(rng.integers(0, 5))
+            pair.append((int(rng.integers(1000, 1090)) // es * es, int(rng.integers(0, 9)), cols,
+                         int(rng.choice([0, cols + rng.integers(0, 9)])), es, int(rng.integers(0, 2))))
+        seen[_check(lib, pair)] += 1
+    assert min(seen) > 500
+
+
+def test_lists_agree_with_a_count_of_bytes(lib):
+    rng = np.random.default_rng(2)
+    seen = [0, 0]
+    for n in rng.integers(3, 13, 1500):
+        at, ranges = 1000, []
+        for _ in range(n):  # mostly apart, in order or not
+            cols, rows = int(rng.integers(1, 4)), int(rng.integers(0, 4))
+            ld = cols + int(rng.integers(0, 3))
+            ranges.append((at, rows, cols, ld, 4, int(rng.integers(0, 2))))
+            at += 4 * rows * ld - (4 if rng.random() < 0.2 else 0)
+        if rng.random() < 0.5:
+            rng.shuffle(ranges)
+        seen[_check(lib, [tuple(int(x) for x in r) for r in ranges])] += 1
+    assert min(seen) > 200
+
+
+def test_columns_of_one_array(lib):
+    """Column slices interleave without sharing a byte; slices that share a column do not pass."""
+    apart = [(4000, 50, 3, 16, 4, 1), (4012, 50, 1, 16, 4, 1), (4016, 50, 8, 16, 4, 0), (4048, 50, 4, 16, 4, 1)]
+    assert not _check(lib, apart)
+    assert _check(lib, apart[:3] + [(4044, 50, 4, 16, 4, 1)])
+    assert not _check(lib, [(4000, 25, 3, 32, 4, 1), (4012, 50, 1, 16, 4, 1)])  # other strides, still apart
+    assert _check(lib, [(4000, 25, 4, 32, 4, 1), (4012, 50, 1, 16, 4, 1)])
+    assert _check(lib, [(4000, 40, 1, 7, 4, 1), (4004, 40, 1, 5, 4, 1)])  # strides without a common factor meet
+    assert not _check(lib, [(4000, 3, 1, 7, 4, 1), (4004, 3, 1, 5, 4, 1)])  # ... but not in these rows
+
+
+def test_long_rows_are_checked_at_once(lib):
+    """2^31 rows of two arrays: a period of their places decides."""
+    big = 1 << 31
+    far = np.array([(1 << 40, big, 1, 7, 4, 1), ((1 << 40) + 4, big, 1, 14, 4, 1)], np.int64)
+    assert lib.clash_few(far.ctypes.data_as(C.c_void_p), 2) == 0
+    far[1, 3] = 15
+    assert lib.clash_few(far.ctypes.data_as(C.c_void_p), 2) == 1
+
+
+# ------------------------------------------------------------- refused calls
+
+P = 1 << 20
+WS, STATS = 1 << 30, 1 << 29
+BAD = ia.IA_ERR_INVALID_ARG
+
+
+def _grad(data, out=None, rows=10, dim=1, stride=1, out_stride=1):
+    return ia.Grad(data=data, out=out, rows=rows, dim=dim, stride=stride, out_stride=out_stride, dtype=ia.IA_DTYPE_F32)
+
+
+@pytest.mark.parametrize("grads", [
+    [_grad(P), _grad(P)],  # one tensor twice, in place
+    [_grad(P), _grad(P + 36)],  # two that overlap, in place
+    [_grad(P, P + 4096), _grad(P + 8192, P + 4096)],  # one output for two
+    [_grad(P, P + 4096), _grad(P + 8192, P + 4096 + 36)],
+    [_grad(P, P + 4096), _grad(P + 4096, P + 8192)],  # an output over another's gradient
+    [_grad(P, P + 4096), _grad(P + 4096)],
+    [_grad(P + 8192, P + 16), _grad(P, P + 4096)],
+    [_grad(P, dim=3, stride=4), _grad(P + 8, dim=2, stride=4)],  # column slices that share a column
+    [_grad(WS + 256)], [_grad(P, WS)], [_grad(STATS + 8)], [_grad(P, STATS - 36)],  # the workspace, the statistics
+])
+def test_clipping_over_shared_memory_is_refused(grads):
+    arr = (ia.Grad * len(grads))(*grads)
+    assert ia.load().ia_clip_grad_norm(arr, len(grads), 1.0, WS, 1 << 20, STATS, None) == BAD
+    assert "overlap" in ia.ia_last_error()
+
+
+def test_a_norm_that_would_be_written_over_its_gradients_is_refused():
+    for at in (STATS, STATS - 36, WS, WS + 1024):
+        arr = (ia.Grad * 1)(_grad(at))
+        assert ia.load().ia_grad_norm(arr, 1, 1.0, WS, 1 << 20, STATS, None) == BAD
+
+
+def test_rows_too_far_apart_are_refused():
+    arr = (ia.Grad * 1)(_grad(P, rows=1 << 30, dim=2, stride=(1 << 31) - 1))
+    assert ia.load().ia_clip_grad_norm(arr, 1, 1.0, WS, 1 << 20, STATS, None) == BAD
+
+
+FREE = dict(param=P, grad=P + 4096, m=P + 8192, v=P + 12288, param_f16=P + 16384, rows=10, dim=1, param_stride=1, lr=1e-3)
+
+
+@pytest.mark.parametrize("first,second", [
+    (dict(m=P), {}), (dict(v=P + 8192), {}), (dict(grad=P + 36), {}), (dict(param_f16=P + 36), {}),
+    ({}, dict(param=P)), ({}, dict(param=P + 39 // 4 * 4)), ({}, dict(m=P + 8192)), ({}, dict(grad=P + 12288)),
+    ({}, dict(v=STATS)), ({}, dict(param=WS + 64)),
+])
+def test_adam_over_shared_memory_is_refused(first, second):
+    a, b = dict(FREE, **first), {k: v + (1 << 22) if k in ("param", "grad", "m", "v", "param_f16") else v
+                                 for k, v in FREE.items()}
+    b.update(second)
+    arr = (ia.AdamGroup * 2)(ia.AdamGroup(**a), ia.AdamGroup(**b))
+    assert ia.load().ia_adam_clip_step(arr, 2, 1.0, 0.9, 0.999, 1e-15, 1, WS, 1 << 20, STATS, None) == BAD
+    assert "overlap" in ia.ia_last_error()
