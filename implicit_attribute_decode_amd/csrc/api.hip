@@ -1199,6 +1199,24 @@ ia_status check_product(int64_t M, int64_t N, int64_t K, int32_t act, const floa
     return IA_OK;
 }
 
+ia::Rows input_rows(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+    return ia::rows_of(x, rows, cols, ld, dtype_size(dtype), false);
+}
+ia::Rows output_rows(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+    return ia::rows_of(x, rows, cols, ld, dtype_size(dtype), true);
+}
+ia::Rows codes_rows(const ia_mx4& q, bool written) {
+    return ia::bytes_of(q.codes, (size_t)q.rows * (size_t)((q.cols + 31) / 32) * 16, written);
+}
+ia::Rows scales_rows(const ia_mx4& q, bool written) {
+    return ia::bytes_of(q.scales, (size_t)q.rows * (size_t)((q.cols + 31) / 32), written);
+}
+
+template <int N>
+ia_status check_clash(const ia::Rows (&r)[N]) {
+    return ia::clash(r, N) ? fail(IA_ERR_INVALID_ARG, kClash) : IA_OK;
+}
+
 ia::Mx4View view(const ia_mx4& q) { return ia::Mx4View{q.codes, q.scales, q.rows, q.cols}; }
 
 }  // namespace
@@ -1212,6 +1230,9 @@ ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t co
     if (st != IA_OK) return st;
     if (out->rows != (transpose ? cols : rows) || out->cols != (transpose ? rows : cols))
         return fail(IA_ERR_INVALID_ARG, "out has another shape");
+    const ia::Rows r[] = {input_rows(x, dtype, rows, cols, ld), codes_rows(*out, true), scales_rows(*out, true)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
     hipError_t e = ia::launch_mx4_quantize(ia::Mx4Source{x, nullptr, rows, cols, ld, 0, dtype}, transpose != 0,
                                            view(*out), (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "mx4 quantize launch");
@@ -1221,6 +1242,9 @@ ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t co
 ia_status ia_mx4_dequantize(const ia_mx4* q, int32_t dtype, void* x, int64_t ld, void* stream) {
     ia_status st = check_mx4(q, "q");
     if (st == IA_OK) st = check_matrix(x, dtype, q->rows, q->cols, ld, false, "x");
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {codes_rows(*q, false), scales_rows(*q, false), output_rows(x, dtype, q->rows, q->cols, ld)};
+    st = check_clash(r);
     if (st != IA_OK) return st;
     hipError_t e = ia::launch_mx4_dequantize(view(*q), dtype, x, ld, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "mx4 dequantize launch");
@@ -1243,7 +1267,17 @@ ia_status ia_mx4_matmul(const ia_mx4* a, const ia_mx4* b, const float* bias, int
     if (a->cols != b->cols) return fail(IA_ERR_INVALID_ARG, "a and b have different numbers of columns");
     st = check_product(a->rows, b->rows, a->cols, act, bias);
     if (st == IA_OK) st = check_matrix(c, dtype, a->rows, b->rows, ldc, false, "c");
-    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_matmul_workspace(a->rows, b->rows, a->cols));
+    const size_t need = ia::mx4_matmul_workspace(a->rows, b->rows, a->cols);
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, need);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {codes_rows(*a, false),
+                          scales_rows(*a, false),
+                          codes_rows(*b, false),
+                          scales_rows(*b, false),
+                          input_rows(bias, IA_DTYPE_F32, 1, b->rows, 0),
+                          output_rows(c, dtype, a->rows, b->rows, ldc),
+                          ia::bytes_of(ws, need, true)};
+    st = check_clash(r);
     if (st != IA_OK) return st;
     hipError_t e = ia::launch_mx4_matmul(view(*a), view(*b), bias, act, dtype, c, ldc, ws, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "mx4 matmul launch");
@@ -1265,7 +1299,16 @@ ia_status ia_mx4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, co
     st = check_product(M, w->rows, w->cols, act, bias);
     if (st == IA_OK) st = check_matrix(x, dtype, M, w->cols, ldx, true, "x");
     if (st == IA_OK) st = check_matrix(y, dtype, M, w->rows, ldy, false, "y");
-    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_linear_workspace(M, w->cols, w->rows));
+    const size_t need = ia::mx4_linear_workspace(M, w->cols, w->rows);
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, need);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {input_rows(x, dtype, M, w->cols, ldx),
+                          codes_rows(*w, false),
+                          scales_rows(*w, false),
+                          input_rows(bias, IA_DTYPE_F32, 1, w->rows, 0),
+                          output_rows(y, dtype, M, w->rows, ldy),
+                          ia::bytes_of(ws, need, true)};
+    st = check_clash(r);
     if (st != IA_OK) return st;
     hipError_t e = ia::launch_mx4_linear(ia::Mx4Source{x, nullptr, M, w->cols, ldx, 0, dtype}, view(*w), bias, act, y,
                                          ldy, ws, (hipStream_t)stream);
@@ -1294,7 +1337,20 @@ ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void* y, in
         if (st == IA_OK && (wt->rows != K || wt->cols != N)) st = fail(IA_ERR_INVALID_ARG, "wt must be [K][N]");
         if (st == IA_OK) st = check_matrix(dx, dtype, M, K, lddx, false, "dx");
     }
-    if (st == IA_OK) st = check_ws(ws, ws_bytes, ia::mx4_linear_backward_workspace(M, N, K));
+    const size_t need = ia::mx4_linear_backward_workspace(M, N, K);
+    if (st == IA_OK) st = check_ws(ws, ws_bytes, need);
+    if (st != IA_OK) return st;
+    const ia_mx4 none{};
+    const ia::Rows r[] = {input_rows(dy, dtype, M, N, lddy),
+                          input_rows(y, dtype, M, N, ldy),
+                          input_rows(dw ? x : nullptr, dtype, M, K, ldx),
+                          codes_rows(dx ? *wt : none, false),
+                          scales_rows(dx ? *wt : none, false),
+                          output_rows(dx, dtype, M, K, lddx),
+                          output_rows(dw, IA_DTYPE_F32, N, K, K),
+                          output_rows(db, IA_DTYPE_F32, 1, N, N),
+                          ia::bytes_of(ws, need, true)};
+    st = check_clash(r);
     if (st != IA_OK) return st;
     const ia::Mx4Source d{dy, y, M, N, lddy, ldy, dtype}, xs{x, nullptr, M, K, ldx, 0, dtype};
     hipError_t e = ia::launch_mx4_linear_backward(d, xs, dx ? view(*wt) : ia::Mx4View{}, dx, lddx, dw, db, ws,

@@ -690,7 +690,7 @@ typedef struct {
  * 6; zeros keep their sign.  A block with a NaN or an infinity gets the NaN
  * scale and zero codes.  Empty matrices are allowed.  out must not overlap x.
  * Errors: INVALID_ARG (null, shapes that do not fit, 0 < ld < cols,
- * misalignment, over 2^40 values), UNSUPPORTED (dtype), DEVICE. */
+ * misalignment, over 2^40 values, overlap), UNSUPPORTED (dtype), DEVICE. */
 IA_API ia_status ia_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
                                  int32_t transpose, const ia_mx4* out, void* stream);
 
@@ -708,7 +708,8 @@ IA_API ia_status ia_mx4_dequantize(const ia_mx4* q, int32_t dtype, void* x, int6
  *         256-byte aligned (may be NULL when that is 0).
  * The sums are taken in a fixed order (the same on every run).  K = 0 gives
  * act(bias).  A block with the NaN scale makes every sum it enters NaN.
- * c must not overlap an input.  M, N, K < 2^31.
+ * c must not overlap an input, nor ws anything (their rows may lie between
+ * each other's).  M, N, K < 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, act), WORKSPACE_TOO_SMALL, DEVICE. */
 IA_API ia_status ia_mx4_matmul_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 IA_API ia_status ia_mx4_matmul(const ia_mx4* a, const ia_mx4* b, const float* bias, int32_t act, int32_t dtype, void* c,
@@ -733,8 +734,8 @@ IA_API ia_status ia_mx4_linear(const void* x, int32_t dtype, int64_t M, int64_t 
  *        (ia_mx4_quantize of the [N][K] weights with transpose = 1); NULL
  *        when dx is
  *   dx (rows lddx >= K apart), dw, db: NULL skips that gradient
- * Outputs are overwritten, in a fixed order of summation; M = 0 gives zero
- * dw and db.  ws of ia_mx4_linear_backward_workspace_size bytes, 256-byte
+ * Outputs are overwritten, in a fixed order of summation, and must not overlap
+ * an input or each other; M = 0 gives zero dw and db.  ws of ia_mx4_linear_backward_workspace_size bytes, 256-byte
  * aligned.  Errors: as ia_mx4_matmul. */
 IA_API ia_status ia_mx4_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 IA_API ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void* y, int64_t ldy, const void* x,

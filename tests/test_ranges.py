@@ -165,3 +165,59 @@ def test_adam_over_shared_memory_is_refused(first, second):
     arr = (ia.AdamGroup * 2)(ia.AdamGroup(**a), ia.AdamGroup(**b))
     assert ia.load().ia_adam_clip_step(arr, 2, 1.0, 0.9, 0.999, 1e-15, 1, WS, 1 << 20, STATS, None) == BAD
     assert "overlap" in ia.ia_last_error()
+
+
+def _mx4(at, rows, cols):
+    return ia.Mx4(codes=at, scales=at + rows * ((cols + 31) // 32) * 16, rows=rows, cols=cols)
+
+
+Q = 1 << 24
+
+
+@pytest.mark.parametrize("x,q", [(Q, Q), (Q + 8 * 32 - 4, Q), (Q + 8 * 2 * 17 - 4, Q), (Q - 8 * 64 * 4 + 4, Q)])
+def test_quantising_over_shared_memory_is_refused(x, q):
+    L, t = ia.load(), _mx4(q, 8, 64)
+    assert L.ia_mx4_quantize(x, ia.IA_DTYPE_F32, 8, 64, 64, 0, C.byref(t), None) == BAD
+    assert "overlap" in ia.ia_last_error()
+    assert L.ia_mx4_dequantize(C.byref(t), ia.IA_DTYPE_F32, x, 64, None) == BAD
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=P), dict(y=P + 36), dict(y=Q), dict(y=Q + 8 * 32), dict(bias=P + 16384 + 96), dict(y=WS + 64), dict(x=WS),
+    dict(y=P + 4 * 60, ldy=64), dict(ldx=72, y=P + 4 * 63, ldy=72),
+])
+def test_layers_over_shared_memory_are_refused(kw):
+    d = dict(x=P, ldx=64, bias=None, y=P + 16384, ldy=8)
+    d.update(kw)
+    M, K, N = 70, 64, 8
+    L, w = ia.load(), _mx4(Q, N, K)
+    if WS in (d["x"], d["y"] - 64):  # a layer that needs a workspace
+        M, K, N = 300, 1024, 300
+        w, d["ldx"], d["ldy"] = _mx4(Q, N, K), K, N
+    assert L.ia_mx4_linear(d["x"], ia.IA_DTYPE_F32, M, d["ldx"], C.byref(w), d["bias"], -1, d["y"], d["ldy"], WS,
+                           1 << 40, None) == BAD
+    assert "overlap" in ia.ia_last_error()
+
+
+@pytest.mark.parametrize("c", [Q, Q + 8 * 34 - 4, P, P + 4 * 34 - 4, P - 4 * 8 * 4 + 4])
+def test_products_over_shared_memory_are_refused(c):
+    a, b = _mx4(P, 4, 64), _mx4(Q, 8, 64)
+    assert ia.load().ia_mx4_matmul(C.byref(a), C.byref(b), None, -1, ia.IA_DTYPE_F32, c, 8, WS, 1 << 40, None) == BAD
+    assert "overlap" in ia.ia_last_error()
+
+
+SPARE = {k: (k_ + 1) << 24 for k_, k in enumerate(("dy", "y", "x", "wt", "dx", "dw", "db"))}
+
+
+@pytest.mark.parametrize("kw", [
+    *(dict({out: SPARE[other]}) for out in ("dx", "dw", "db") for other in SPARE if other != out),
+    dict(dx=WS), dict(dy=WS + 128), dict(dx=SPARE["dy"] + 4 * 4, lddx=64), dict(dw=SPARE["db"] - 4 * 8 * 64 + 4),
+])
+def test_gradients_over_shared_memory_are_refused(kw):
+    d = dict(SPARE, lddx=64)
+    d.update(kw)
+    M, N, K = 40, 8, 64
+    wt = _mx4(d["wt"], K, N)
+    assert ia.load().ia_mx4_linear_backward(d["dy"], N, d["y"], N, d["x"], K, ia.IA_DTYPE_F32, M, N, K, C.byref(wt),
+                                            d["dx"], d["lddx"], d["dw"], d["db"], WS, 1 << 40, None) == BAD
+    assert "overlap" in ia.ia_last_error()
