@@ -8,6 +8,7 @@ library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 
@@ -457,6 +458,7 @@ def ia_densify(xyzt, grad_acc, grad_count, scales, quats, opacity, noise, m, v, 
 # ----------------------------------------------------------------- clipping
 
 
+@functools.lru_cache(maxsize=64)  # a number of tensors has one size
 def ia_clip_workspace_size(count: int) -> int:
     n = C.c_size_t()
     _check(load().ia_clip_workspace_size(int(count), C.byref(n)))

@@ -374,6 +374,38 @@ def lr_at(step: int, base: float, warmup: int, total: int, final: float = 1e-7) 
     return ia.ia_lr_at(base, step, warmup, total, final)
 
 
+class _Moments(dict):
+    """name -> (m, v), an optimiser's moments: contiguous float32 tensors of one
+    size on one device, checked when they are put in."""
+
+    def __init__(self, moments):
+        super().__init__()
+        self.update(moments)
+
+    def __setitem__(self, name, moments):
+        m, v = moments
+        if not (m.dtype == v.dtype == torch.float32 and m.is_contiguous() and v.is_contiguous()
+                and m.numel() == v.numel() and m.device == v.device):
+            raise ValueError(f"group {name}: moments must be contiguous float32 tensors of one size on one device")
+        super().__setitem__(name, (m, v))
+
+    def update(self, *args, **moments):
+        for name, mv in dict(*args, **moments).items():
+            self[name] = mv
+
+    def setdefault(self, name, moments=None):
+        if name not in self:
+            self[name] = moments
+        return self[name]
+
+    def __ior__(self, moments):
+        self.update(moments)
+        return self
+
+    def __reduce__(self):
+        return _Moments, (dict(self),)
+
+
 class Adam:
     """Adam over named parameter groups, each an fp32 device tensor with its
     own base learning rate ([SPIN] §4 implementation details: per-group rates,
@@ -391,6 +423,15 @@ class Adam:
         self.warmup, self.total = warmup, total
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
         self.t = 0
+
+    @property
+    def state(self):
+        """name -> (m, v); may be replaced, whole or group by group."""
+        return self._state
+
+    @state.setter
+    def state(self, moments):
+        self._state = _Moments(moments)
 
     def step(self, grads: dict, max_norm: float | None = None):
         """One update of every group that has a gradient in `grads` (name -> tensor).
@@ -418,22 +459,33 @@ class Adam:
                 ia.ia_adam_step_strided(p, grad.contiguous(), m, v, lr, self.beta1, self.beta2, self.eps, self.t)
 
     def _clipped_step(self, grads: dict, max_norm: float):
-        names = [k for k in self.groups if grads.get(k) is not None]
-        arr = (ia.AdamGroup * len(names))()
-        at, pack = 0, ia.AdamGroup.PACK
+        groups = [(k, g, grad) for k, g in self.groups.items() if (grad := grads.get(k)) is not None]
+        arr = (ia.AdamGroup * len(groups))()
+        at, size, pack = 0, ia.AdamGroup.PACK.size, ia.AdamGroup.PACK.pack_into
         keep, rates = [], {}  # contiguous copies live until the call has enqueued its reads
-        for name in names:
-            g, grad = self.groups[name], grads[name]
+        f32, state, device = torch.float32, self._state, None
+        for name, g, grad in groups:
             p, f16, lr = g["param"], g.get("f16"), g["lr"]
-            m, v = self.state[name]
-            if p.dtype is not torch.float32 or grad.dtype is not torch.float32 or grad.shape != p.shape:
+            m, v = state[name]
+            if p.dtype is not f32 or grad.dtype is not f32 or grad.shape != p.shape:
                 raise ValueError(f"group {name}: parameter and gradient must be float32 of one shape")
+            nbytes, dev = grad.nbytes, grad.get_device()
+            if m.nbytes != nbytes or v.nbytes != nbytes or m.get_device() != dev:  # the rest when they were put in
+                raise ValueError(f"group {name}: moments of another size or device than the gradient")
+            if f16 is not None and not (f16.element_size() == 2 and 2 * f16.nbytes == nbytes and f16.is_contiguous()
+                                        and f16.get_device() == dev):
+                raise ValueError(f"group {name}: an fp16 mirror must be contiguous 16-bit values of the parameter's "
+                                 "size and device")
+            if device is None:
+                device = dev
+            if dev < 0 or dev != device or p.get_device() != dev:
+                raise ValueError(f"group {name}: parameters and gradients must be on one GPU")
             if not grad.is_contiguous():
                 grad = grad.contiguous()
                 keep.append(grad)
             if p.is_contiguous():
-                rows, dim, stride = p.numel(), 1, 1
-            elif p.dim() == 2 and p.stride(1) == 1 and p.stride(0) >= p.shape[1] and f16 is None:
+                rows, dim, stride = nbytes // 4, 1, 1
+            elif p.dim() == 2 and p.stride(1) == 1 and p.shape[1] <= p.stride(0) <= _INT32_MAX and f16 is None:
                 rows, dim, stride = p.shape[0], p.shape[1], p.stride(0)
             else:
                 raise ValueError(f"group {name}: the parameter must be contiguous, or [rows, dim] rows of a wider "
@@ -441,12 +493,12 @@ class Adam:
             rate = rates.get(lr)
             if rate is None:
                 rate = rates[lr] = lr_at(self.t - 1, lr, self.warmup, self.total)
-            pack.pack_into(arr, at, p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr(),
-                           0 if f16 is None else f16.data_ptr(), rows, dim, stride, rate)
-            at += pack.size
-        device = p.device if names else "cuda"
-        stats = torch.empty(3, dtype=torch.float32, device=device)
-        ws = torch.empty(ia.ia_clip_workspace_size(len(names)), dtype=torch.uint8, device=device)
+            pack(arr, at, p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr(),
+                 0 if f16 is None else f16.data_ptr(), rows, dim, stride, rate)
+            at += size
+        device = p.device if groups else "cuda"
+        stats = torch.empty(3, dtype=f32, device=device)
+        ws = torch.empty(ia.ia_clip_workspace_size(len(groups)), dtype=torch.uint8, device=device)
         ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t, ws, stats)
         return stats
 

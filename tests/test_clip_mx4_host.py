@@ -1,6 +1,9 @@
 """What the Python calls of clipping and MXFP4 hand to the C ABI, checked on the
 host: the library's entry points are replaced by recorders, so nothing is
 dereferenced and no GPU is needed."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -68,3 +71,75 @@ def test_adam_row_strides_past_32_bits_are_refused(monkeypatch):
     dense = torch.empty((3, 100), dtype=torch.float32, device="meta")
     with pytest.raises(ValueError):
         ia.ia_adam_step_strided(_far(3, 100, 2 ** 32 + 100), dense, dense, dense, 1e-3, 0.9, 0.999, 1e-15, 1)
+
+
+def _adam(**kw):
+    """(an optimiser of one group with a mirror, its gradients), host tensors."""
+    d = dict(param=torch.zeros(6, 4), grad=torch.zeros(6, 4), m=torch.zeros(6, 4), v=torch.zeros(6, 4),
+             f16=torch.zeros(24, dtype=torch.int16))
+    d.update(kw)
+    opt = P.Adam({"w": {"param": d["param"], "lr": 1e-3, "f16": d["f16"]}}, warmup=0, total=10)
+    opt.state["w"] = (d["m"], d["v"])
+    return opt, {"w": d["grad"]}
+
+
+@pytest.mark.parametrize("kw,what", [
+    ({}, "one GPU"),  # all of it on the host
+    (dict(m=torch.zeros(6, 3)), "moments"), (dict(v=torch.zeros(23)), "moments"), (dict(m=torch.zeros(0)), "moments"),
+    (dict(m=torch.zeros(6, 3), v=torch.zeros(6, 3)), "moments"), (dict(m=torch.zeros(25), v=torch.zeros(25)), "moments"),
+    (dict(m=torch.zeros(6, 4, dtype=torch.float16)), "moments"), (dict(v=torch.zeros(3, 4, dtype=torch.float64)), "moments"),
+    (dict(m=torch.zeros(4, 6).t()), "moments"), (dict(v=torch.zeros(6, 8)[:, ::2]), "moments"),
+    (dict(m=torch.empty(6, 4, device="meta")), "moments"),
+    (dict(f16=torch.zeros(23, dtype=torch.float16)), "mirror"), (dict(f16=torch.zeros(24, dtype=torch.float32)), "mirror"),
+    (dict(f16=torch.zeros(12, dtype=torch.float32)), "mirror"), (dict(f16=torch.zeros(24, dtype=torch.uint8)), "mirror"),
+    (dict(f16=torch.zeros(48, dtype=torch.float16)[::2]), "mirror"),
+    (dict(grad=torch.zeros(24)), "one shape"), (dict(grad=torch.zeros(6, 4, dtype=torch.float16)), "one shape"),
+    (dict(param=torch.zeros(4, 6).t()), "contiguous"),
+])
+def test_adam_refuses_arrays_that_the_kernel_would_pass_the_end_of(calls, monkeypatch, kw, what):
+    """Host arrays, and moments or mirrors of another size, type or layout: refused before their addresses are taken."""
+    if what == "contiguous":  # the check after the device's
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    with pytest.raises(ValueError, match=what):
+        opt, grads = _adam(**kw)
+        opt.step(grads, max_norm=1.0)
+    assert "ia_adam_clip_step" not in calls
+
+
+def test_adam_refuses_moments_on_another_device(calls, monkeypatch):
+    opt, grads = _adam()
+    m = opt.state["w"][0]
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    opt.step(grads, max_norm=1.0)
+    assert calls.pop("ia_adam_clip_step")
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: int(t is m))
+    with pytest.raises(ValueError, match="moments"):
+        opt.step(grads, max_norm=1.0)
+    assert "ia_adam_clip_step" not in calls
+
+
+@pytest.mark.parametrize("put", [
+    lambda opt, mv: opt.state.__setitem__("w", mv), lambda opt, mv: opt.state.update(w=mv),
+    lambda opt, mv: opt.state.update({"w": mv}), lambda opt, mv: opt.state.setdefault("x", mv),
+    lambda opt, mv: setattr(opt, "state", {"w": mv}), lambda opt, mv: opt.state.__ior__({"w": mv}),
+    lambda opt, mv: copy.deepcopy(opt).state.update(w=mv), lambda opt, mv: pickle.loads(pickle.dumps(opt.state)).update(w=mv),
+])
+def test_every_way_to_put_moments_in_checks_them(put):
+    opt, _ = _adam()
+    put(opt, [torch.ones(6, 4), torch.ones(6, 4)])
+    with pytest.raises(ValueError, match="moments"):
+        put(_adam()[0], (torch.ones(6, 4), torch.ones(6, 4).half()))
+
+
+def test_adam_refuses_groups_on_several_devices(calls, monkeypatch):
+    opt, grads = _adam()
+    opt.groups["b"] = {"param": torch.zeros(5), "lr": 1e-3}
+    opt.state["b"] = (torch.zeros(5), torch.zeros(5))
+    grads["b"] = torch.zeros(5)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    opt.step(grads, max_norm=1.0)
+    assert len(calls.pop("ia_adam_clip_step")[0]) == 2
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: int(t.numel() == 5))
+    with pytest.raises(ValueError, match="one GPU"):
+        opt.step(grads, max_norm=1.0)
+    assert "ia_adam_clip_step" not in calls
