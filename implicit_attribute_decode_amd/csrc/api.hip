@@ -1075,9 +1075,10 @@ ia_status check_grads(const ia_grad* grads, int32_t count) {
     return IA_OK;
 }
 
-ia_status check_group_ranges(const ia_adam_group* groups, int32_t count, const void* ws, const float* stats) {
+ia_status check_group_ranges(const ia_adam_group* groups, int32_t count, const void* ws, const int32_t* skipped,
+                             const float* stats) {
     ia::Ranges r;
-    if (!r.reserve(5 * (size_t)count + 2)) return fail(IA_ERR_OUT_OF_MEMORY, "no host memory to check the groups");
+    if (!r.reserve(5 * (size_t)count + 3)) return fail(IA_ERR_OUT_OF_MEMORY, "no host memory to check the groups");
     const auto dense = [&](auto member, size_t es, bool written) {
         for (int32_t k = 0; k < count; ++k)
             r.add(ia::rows_of(groups[k].*member, groups[k].rows, groups[k].dim, groups[k].dim, es, written));
@@ -1091,6 +1092,7 @@ ia_status check_group_ranges(const ia_adam_group* groups, int32_t count, const v
     dense(&ia_adam_group::v, 4, true);
     dense(&ia_adam_group::param_f16, 2, true);
     r.add(ia::bytes_of(ws, ia::clip_workspace(count), true));
+    r.add(ia::bytes_of(skipped, sizeof(int32_t), true));
     r.add(ia::bytes_of(stats, 3 * sizeof(float), true));
     r.run_done();
     return r.clash() ? fail(IA_ERR_INVALID_ARG, kClash) : IA_OK;
@@ -1131,10 +1133,18 @@ ia_status ia_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm,
 
 ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
                             float eps, int32_t step, void* ws, size_t ws_bytes, float* stats, void* stream) {
+    return ia_adam_clip_step_counted(groups, count, max_norm, beta1, beta2, eps, step, nullptr, ws, ws_bytes, stats,
+                                     stream);
+}
+
+ia_status ia_adam_clip_step_counted(const ia_adam_group* groups, int32_t count, float max_norm, float beta1,
+                                    float beta2, float eps, int32_t step, int32_t* skipped, void* ws, size_t ws_bytes,
+                                    float* stats, void* stream) {
     ia_status st = check_clip(count, max_norm, ws, ws_bytes, stats);
     if (st != IA_OK) return st;
     if (count > 0 && !groups) return fail(IA_ERR_INVALID_ARG, "groups is null");
     if (step < 1) return fail(IA_ERR_INVALID_ARG, "step must be >= 1");
+    if (!aligned(skipped, 4)) return fail(IA_ERR_INVALID_ARG, "skipped is misaligned");
     if (!(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f))
         return fail(IA_ERR_INVALID_ARG, "betas must be in [0, 1)");
     if (!(eps >= 0.0f)) return fail(IA_ERR_INVALID_ARG, "eps must be >= 0");
@@ -1151,9 +1161,9 @@ ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float ma
             return fail(IA_ERR_INVALID_ARG, "a group's array is misaligned");
         if (!extent_ok(g.rows, g.param_stride)) return fail(IA_ERR_INVALID_ARG, "rows too far apart");
     }
-    st = check_group_ranges(groups, count, ws, stats);
+    st = check_group_ranges(groups, count, ws, skipped, stats);
     if (st != IA_OK) return st;
-    hipError_t e = ia::launch_adam_clip(groups, count, max_norm, beta1, beta2, eps, step, ws, stats,
+    hipError_t e = ia::launch_adam_clip(groups, count, max_norm, beta1, beta2, eps, step, ws, skipped, stats,
                                         (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "clipped adam launch");
     return IA_OK;

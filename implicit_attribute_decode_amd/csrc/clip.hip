@@ -351,7 +351,24 @@ __global__ void __launch_bounds__(kThreads) grad_scale_strided_kernel(StridedArg
     }
 }
 
-__device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, float f, const AdamConsts& c) {
+// Steps that the call before this one left out (device count or null): the bias
+// corrections are those of the steps applied.
+struct Skips {
+    int32_t* count;
+    int32_t step;   // this call's, those left out included
+    int32_t first;  // the first launch of the call counts
+};
+
+// 1 - b^t
+__device__ __forceinline__ double bias_correction(double b, int t) {
+    double p = 1.0;
+    for (; t > 0; t >>= 1, b *= b)
+        if (t & 1) p *= b;
+    return 1.0 - p;
+}
+
+__device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, float f, float step_size,
+                                           const AdamConsts& c) {
     const float* g = t.g + i0;
     float* m = t.m + i0;
     float* v = t.v + i0;
@@ -361,7 +378,7 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
             const int64_t row = (i0 + k) / t.dim;
             float* p = t.p + row * t.stride + (i0 + k - row * t.dim);
             float mi = m[k], vi = v[k];
-            const float pi = adam_element(*p, g[k] * f, mi, vi, c, t.step_size);
+            const float pi = adam_element(*p, g[k] * f, mi, vi, c, step_size);
             m[k] = mi;
             v[k] = vi;
             *p = pi;
@@ -377,7 +394,7 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
         uint16_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            pv.e[e] = adam_element(pv.e[e], gv.e[e] * f, mv.e[e], vv.e[e], c, t.step_size);
+            pv.e[e] = adam_element(pv.e[e], gv.e[e] * f, mv.e[e], vv.e[e], c, step_size);
             h[e] = __builtin_bit_cast(uint16_t, (_Float16)pv.e[e]);
         }
         store_once(p + 4 * i, pv);
@@ -388,7 +405,7 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
     const int k = nv * 4 + (int)threadIdx.x;
     if (k < n) {
         float mi = m[k], vi = v[k];
-        const float pi = adam_element(p[k], g[k] * f, mi, vi, c, t.step_size);
+        const float pi = adam_element(p[k], g[k] * f, mi, vi, c, step_size);
         m[k] = mi;
         v[k] = vi;
         p[k] = pi;
@@ -396,15 +413,24 @@ __device__ __forceinline__ void adam_chunk(const Group& t, int64_t i0, int n, fl
     }
 }
 
-__global__ void __launch_bounds__(kThreads) adam_clip_kernel(GroupArgs a, AdamConsts c, Norm m) {
+__global__ void __launch_bounds__(kThreads) adam_clip_kernel(GroupArgs a, AdamConsts c, Norm m, Skips left_out) {
     bool finite;
     const float f = clip_factor(m, finite);
-    if (!finite) return;  // gradients that are not finite change nothing
+    if (!finite) {  // gradients that are not finite change nothing
+        if (left_out.count && left_out.first && blockIdx.x == 0 && threadIdx.x == 0) *left_out.count += 1;
+        return;
+    }
+    float rate = 1.0f;
+    if (const int skipped = left_out.count ? *left_out.count : 0; skipped > 0) {
+        const int t = max(left_out.step - skipped, 1);
+        rate = (float)(bias_correction((double)c.b1, left_out.step) / bias_correction((double)c.b1, t));
+        c.v_scale = (float)(1.0 / bias_correction((double)c.b2, t));
+    }
     int t = 0;
     for (int k = blockIdx.x; k < a.chunks; k += gridDim.x) {
         t = find(a, k, t);
         const int64_t i0 = (int64_t)(k - a.t[t].first) * kChunk;
-        adam_chunk(a.t[t], i0, (int)min((int64_t)kChunk, a.t[t].n - i0), f, c);
+        adam_chunk(a.t[t], i0, (int)min((int64_t)kChunk, a.t[t].n - i0), f, a.t[t].step_size * rate, c);
     }
 }
 
@@ -533,7 +559,7 @@ hipError_t launch_clip_grad_norm(const ia_grad* grads, int32_t count, float max_
 }
 
 hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
-                            float eps, int32_t step, void* ws, float* stats, hipStream_t s) {
+                            float eps, int32_t step, void* ws, int32_t* skipped, float* stats, hipStream_t s) {
     double* part = reinterpret_cast<double*>(ws);
     Norm m{part, 0, max_norm, stats};
     hipError_t e = each_launch<DenseArgs>(
@@ -546,6 +572,7 @@ hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float ma
     if (e == hipSuccess) e = collect(part, m, s);
     if (e != hipSuccess) return e;
     if (m.parts == 0) return finish(m, s);
+    Skips left_out{skipped, step, 1};
     const AdamConsts c{beta1, beta2, eps, (float)(1.0 / (1.0 - pow((double)beta2, (double)step)))};
     const double correction = 1.0 - pow((double)beta1, (double)step);
     return each_launch<GroupArgs>(
@@ -558,7 +585,8 @@ hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float ma
             return t.n;
         },
         [&](const GroupArgs& a, int blocks) {
-            IA_LAUNCH("adam_clip_kernel", adam_clip_kernel, dim3(blocks), dim3(kThreads), 0, s, a, c, m);
+            IA_LAUNCH("adam_clip_kernel", adam_clip_kernel, dim3(blocks), dim3(kThreads), 0, s, a, c, m, left_out);
+            left_out.first = 0;
         });
 }
 

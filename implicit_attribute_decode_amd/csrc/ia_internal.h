@@ -326,7 +326,7 @@ hipError_t launch_grad_norm(const ia_grad* grads, int32_t count, float max_norm,
 hipError_t launch_clip_grad_norm(const ia_grad* grads, int32_t count, float max_norm, void* ws, float* stats,
                                  hipStream_t s);
 hipError_t launch_adam_clip(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
-                            float eps, int32_t step, void* ws, float* stats, hipStream_t s);
+                            float eps, int32_t step, void* ws, int32_t* skipped, float* stats, hipStream_t s);
 
 // ---------------------------------------------------------------- MXFP4
 

@@ -40,6 +40,7 @@ EXPORTS = ("ia_last_error", "ia_decoder_create", "ia_decoder_set_params", "ia_de
            "ia_image_loss_workspace_size", "ia_image_loss", "ia_adam_step", "ia_adam_step_strided",
            "ia_densify_accumulate", "ia_densify_workspace_size", "ia_densify",
            "ia_clip_workspace_size", "ia_grad_norm", "ia_clip_grad_norm", "ia_adam_clip_step",
+           "ia_adam_clip_step_counted",
            "ia_mx4_quantize", "ia_mx4_dequantize", "ia_mx4_matmul_workspace_size", "ia_mx4_matmul",
            "ia_mx4_linear_workspace_size", "ia_mx4_linear", "ia_mx4_linear_backward_workspace_size",
            "ia_mx4_linear_backward",
@@ -169,6 +170,8 @@ def load(path: str = LIB_PATH):
         L.ia_clip_grad_norm.argtypes = [P, C.c_int32, C.c_float, P, C.c_size_t, P, P]
         L.ia_adam_clip_step.argtypes = [P, C.c_int32, C.c_float, C.c_float, C.c_float, C.c_float, C.c_int32, P,
                                         C.c_size_t, P, P]
+        L.ia_adam_clip_step_counted.argtypes = [P, C.c_int32, C.c_float, C.c_float, C.c_float, C.c_float, C.c_int32, P, P,
+                                                C.c_size_t, P, P]
         L.ia_mx4_quantize.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32, P, P]
         L.ia_mx4_dequantize.argtypes = [P, C.c_int32, P, C.c_int64, P]
         L.ia_mx4_matmul_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
@@ -477,10 +480,12 @@ def ia_clip_grad_norm(grads, max_norm: float, ws, stats, stream=None):
 
 
 def ia_adam_clip_step(groups, max_norm: float, beta1: float, beta2: float, eps: float, step: int, ws, stats,
-                      stream=None):
-    """groups: a ctypes array of AdamGroup; stats: device float32 [3]."""
-    _check(load().ia_adam_clip_step(groups, len(groups), float(max_norm), float(beta1), float(beta2), float(eps),
-                                    int(step), _ptr(ws), _nbytes(ws), _ptr(stats), _stream(stream)))
+                      stream=None, skipped=None):
+    """groups: a ctypes array of AdamGroup; stats: device float32 [3]; skipped: device int32 [1] of
+    ia_adam_clip_step_counted, or None."""
+    _check(load().ia_adam_clip_step_counted(groups, len(groups), float(max_norm), float(beta1), float(beta2),
+                                            float(eps), int(step), _ptr(skipped), _ptr(ws), _nbytes(ws), _ptr(stats),
+                                            _stream(stream)))
 
 
 # ----------------------------------------------------------------- MXFP4

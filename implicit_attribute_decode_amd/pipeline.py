@@ -423,6 +423,7 @@ class Adam:
         self.warmup, self.total = warmup, total
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
         self.t = 0
+        self.skipped = None  # with the first clipped step
 
     @property
     def state(self):
@@ -438,12 +439,14 @@ class Adam:
 
         With max_norm the gradients count as clipped by their global norm over
         the groups updated (they are not modified) and all groups go through
-        one ia_adam_clip_step; returns its stats, a device float32 tensor
-        {norm, factor, 1 if the norm is finite else 0}.  A step whose norm is
-        not finite changes no parameter and no moment."""
-        self.t += 1
+        one launch; returns its stats, a device float32 tensor {norm, factor,
+        1 if the norm is finite else 0}.  A step whose norm is not finite
+        changes no parameter and no moment: it counts in t, which sets the
+        rates, and in `skipped` (device int32 [1]), which the bias corrections
+        of the clipped steps after it leave out."""
         if max_norm is not None:
             return self._clipped_step(grads, max_norm)
+        self.t += 1
         for name, g in self.groups.items():
             grad = grads.get(name)
             if grad is None:
@@ -492,14 +495,19 @@ class Adam:
                                  "array without an fp16 mirror")
             rate = rates.get(lr)
             if rate is None:
-                rate = rates[lr] = lr_at(self.t - 1, lr, self.warmup, self.total)
+                rate = rates[lr] = lr_at(self.t, lr, self.warmup, self.total)
             pack(arr, at, p.data_ptr(), grad.data_ptr(), m.data_ptr(), v.data_ptr(),
                  0 if f16 is None else f16.data_ptr(), rows, dim, stride, rate)
             at += size
         device = p.device if groups else "cuda"
         stats = torch.empty(3, dtype=f32, device=device)
         ws = torch.empty(ia.ia_clip_workspace_size(len(groups)), dtype=torch.uint8, device=device)
-        ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t, ws, stats)
+        if self.skipped is None:
+            self.skipped = torch.zeros(1, dtype=torch.int32, device=device)
+        elif groups and self.skipped.get_device() != dev:
+            self.skipped = self.skipped.to(device)
+        ia.ia_adam_clip_step(arr, max_norm, self.beta1, self.beta2, self.eps, self.t + 1, ws, stats, None, self.skipped)
+        self.t += 1  # a refused call is no step
         return stats
 
 

@@ -664,6 +664,16 @@ typedef struct {
 IA_API ia_status ia_adam_clip_step(const ia_adam_group* groups, int32_t count, float max_norm, float beta1, float beta2,
                                    float eps, int32_t step, void* ws, size_t ws_bytes, float* stats, void* stream);
 
+/* ia_adam_clip_step for a caller that does not wait to learn whether a step was
+ * applied.  skipped: device int32, 0 before the first step, or NULL: the number
+ * of earlier steps that changed nothing because their norm was not finite.  The
+ * bias corrections are those of step - skipped (at least 1), and the call adds 1
+ * to it where its own norm is not finite.  While it is 0 the results are
+ * ia_adam_clip_step's.  Errors: as ia_adam_clip_step. */
+IA_API ia_status ia_adam_clip_step_counted(const ia_adam_group* groups, int32_t count, float max_norm, float beta1,
+                                           float beta2, float eps, int32_t step, int32_t* skipped, void* ws,
+                                           size_t ws_bytes, float* stats, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* 4-bit microscaled floating point (MXFP4)                                  */
 /* ------------------------------------------------------------------------ */

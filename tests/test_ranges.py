@@ -221,3 +221,9 @@ def test_gradients_over_shared_memory_are_refused(kw):
     assert ia.load().ia_mx4_linear_backward(d["dy"], N, d["y"], N, d["x"], K, ia.IA_DTYPE_F32, M, N, K, C.byref(wt),
                                             d["dx"], d["lddx"], d["dw"], d["db"], WS, 1 << 40, None) == BAD
     assert "overlap" in ia.ia_last_error()
+
+
+def test_the_count_of_steps_left_out_is_checked():
+    L, one = ia.load(), (ia.AdamGroup * 1)(ia.AdamGroup(**FREE))
+    for at in (P + 2, P, P + 8192 + 36, STATS, WS):
+        assert L.ia_adam_clip_step_counted(one, 1, 1.0, 0.9, 0.999, 1e-15, 1, at, WS, 1 << 20, STATS, None) == BAD
