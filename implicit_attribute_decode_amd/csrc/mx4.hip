@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
     const int np = (p.N + COLS - 1) / COLS, kp = (p.K + COLS - 1) / COLS, tn = np * E, tk = kp * E;
     const int64_t begin = (int64_t)blockIdx.x * p.run, end = min(begin + p.run, p.M);
     floatx4 acc[2][16] = {};
-    float sum[SUBS][E] = {};
+    double sum[SUBS][E] = {};  // of blocks of 32 rows: a run may be of any length
     // panels in turn: one on its way while the other is quantised (in fp32, which
     // has no registers for it, one)
     constexpr int AHEAD = sizeof(T) == 2 ? 2 : 1;
@@ -749,8 +749,10 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
 #pragma unroll
                             for (int i = 0; i < 16; ++i) b.p[i] = keep_pair(b.p[i], m, i);
                         }
+                        float part = 0.0f;
 #pragma unroll
-                        for (int k = 0; k < kBlock; ++k) sum[sub][e] += (float)b.p[k >> 1][k & 1];
+                        for (int k = 0; k < kBlock; ++k) part += (float)b.p[k >> 1][k & 1];
+                        sum[sub][e] += (double)part;
                     }
                     uint32_t byte;
                     codes[buf][panel * E + e][lane] = quantize(b, byte);
@@ -792,11 +794,11 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
     for (int sub = 0; sub < SUBS; ++sub)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float a = sum[sub][e];
+            double a = sum[sub][e];
             a += __shfl_xor(a, 16, 64);
             a += __shfl_xor(a, 32, 64);
             const int n = (8 * sub + wave) * COLS + E * c + e;
-            if (q == 0 && 8 * sub + wave < np && n < p.N) p.sums[(int64_t)blockIdx.x * p.N + n] = a;
+            if (q == 0 && 8 * sub + wave < np && n < p.N) p.sums[(int64_t)blockIdx.x * p.N + n] = (float)a;
         }
 }
 
