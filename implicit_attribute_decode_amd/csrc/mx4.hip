@@ -622,19 +622,31 @@ struct Panel {
 };
 
 // Rows row0 + 32 q + k of the lane's columns, zero from row `end` on.  The rows'
-// addresses are uniform, the lane adds 32 bits: `ld` is below kMaxGradStride.  A
-// piece that crosses the last column is read from before its place (cols is at
-// least E); shift_panel puts it right.
+// addresses are uniform, the lane adds 32 bits where `ld` is below kMaxGradStride
+// and takes whole addresses where it is not (FAR).  A piece that crosses the last
+// column is read from before its place (cols is at least E); shift_panel puts it
+// right.
 constexpr int64_t kMaxGradStride = 1 << 22;
 
-template <typename T>
+template <bool FAR, typename T>
 __device__ __forceinline__ void load_panel(Panel<T>& v, const T* m, int64_t ld, int cols, int panel, int q, int c,
                                            int64_t row0, int64_t end) {
     constexpr int E = Panel<T>::E, COLS = Panel<T>::COLS;
     const int col = panel * COLS + E * c, from = min(col, cols - E);
     const char* base = reinterpret_cast<const char*>(m + row0 * ld);
     const int64_t pitch = ld * (int64_t)sizeof(T);
-    if (row0 + kGradRows <= end) {
+    if (FAR) {
+        const int r = 32 * q, last = (int)min((int64_t)kGradRows, end - row0) - 1;
+        int64_t off = min(r, last) * pitch + (int64_t)from * (int64_t)sizeof(T);
+        asm volatile("" : "+v"(off));  // one address that goes along, not 32 at once
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) {
+            uint32_t w;
+            __builtin_memcpy(&w, base + off, 4);
+            v.w[k] = r + k <= last ? w : 0u;
+            off += r + k < last ? pitch : 0;
+        }
+    } else if (row0 + kGradRows <= end) {
         // the offset is opaque: else 32 loop-invariant addresses take 64 registers
         uint32_t off = (uint32_t)((32 * q * (int)ld + from) * (int)sizeof(T));
         asm volatile("" : "+v"(off));
@@ -700,7 +712,7 @@ __device__ __forceinline__ T keep_pair(T v, uint32_t m, int i) {
     return __builtin_bit_cast(T, __builtin_bit_cast(uint32_t, v) & ((lo & 0xffffu) | (hi & 0xffff0000u)));
 }
 
-template <typename T>
+template <typename T, bool FAR>
 __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> p) {
     constexpr int E = Panel<T>::E, COLS = Panel<T>::COLS, SUBS = kGradTiles / E / 8;  // panels a wave takes
     __shared__ intx4 codes[2][kGradTiles][64];
@@ -723,7 +735,7 @@ __global__ void __launch_bounds__(512) mx4_narrow_grad_kernel(NarrowGradArgs<T> 
         const int panel = of_d ? all : all - np;
         const int64_t row0 = begin + step * kGradRows;
         if (of_d && p.bits) load_bits(to, p.bits, p.words, panel * COLS + E * c, row0 + 32 * q, end);
-        load_panel(to, of_d ? p.d : p.x, of_d ? p.ldd : p.ldx, of_d ? p.N : p.K, panel, q, c, row0, end);
+        load_panel<FAR>(to, of_d ? p.d : p.x, of_d ? p.ldd : p.ldx, of_d ? p.N : p.K, panel, q, c, row0, end);
     };
     if (steps > 0) {
 #pragma unroll
@@ -995,7 +1007,10 @@ hipError_t narrow_grad_t(const Mx4Source& dy, const Mx4Source& x, const Mx4View&
     const NarrowGradArgs<T> p{src.x, src.ldx, bits, steps * 128, (const T*)x.x, x.ldx, M, g.run, (int)N,
                               dw ? (int)K : 0, part, sums};
     const int tk = dw ? g.tk : 0;
-    IA_LAUNCH("mx4_narrow_grad_kernel", mx4_narrow_grad_kernel<T>, dim3((unsigned)g.blocks), dim3(512), 0, s, p);
+    if (src.ldx < kMaxGradStride && (!dw || x.ldx < kMaxGradStride))
+        IA_LAUNCH("mx4_narrow_grad_kernel", (mx4_narrow_grad_kernel<T, false>), dim3((unsigned)g.blocks), dim3(512), 0, s, p);
+    else
+        IA_LAUNCH("mx4_narrow_grad_kernel", (mx4_narrow_grad_kernel<T, true>), dim3((unsigned)g.blocks), dim3(512), 0, s, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     constexpr int E = Panel<T>::E;
@@ -1087,22 +1102,19 @@ hipError_t launch_mx4_linear(const Mx4Source& x, const Mx4View& w, const float* 
 bool is_narrow_grad(int64_t M, int64_t N, int64_t K) { return M > 0 && N >= 4 && K >= 4 && N <= 256 && K <= 256; }
 
 size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
-    size_t narrow = 0;
     if (is_narrow_grad(M, N, K)) {
         const size_t a = grad_scratch(M, N, grad_plan(M, N, K, 2)).total, b = grad_scratch(M, N, grad_plan(M, N, K, 4)).total;
-        narrow = a > b ? a : b;
+        return a > b ? a : b;
     }
-    // wide row strides take the general path
     const size_t x = mx4_matmul_workspace(M, K, N), w = mx4_matmul_workspace(N, K, M);
-    const size_t general = scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
-                           round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
-    return narrow > general ? narrow : general;
+    return scratch_bytes(M, N) + scratch_bytes(N, M) + scratch_bytes(K, M) +
+           round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float)) + (x > w ? x : w);
 }
 
 hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
                                       float* dw, float* db, void* ws, hipStream_t s) {
     const int64_t M = dy.rows, N = dy.cols, K = x.cols;
-    if (is_narrow_grad(M, N, K) && dy.ldx < kMaxGradStride && (!dw || x.ldx < kMaxGradStride))
+    if (is_narrow_grad(M, N, K))
         return IA_BY_DTYPE(dy.dtype, narrow_grad_t, dy, x, wt, dx, lddx, dw, db, ws, s);
     char* at = (char*)ws;
     const Mx4View dr = scratch_view(at, M, N), dc = scratch_view(at += scratch_bytes(M, N), N, M),

@@ -143,3 +143,9 @@ def test_adam_refuses_groups_on_several_devices(calls, monkeypatch):
     with pytest.raises(ValueError, match="one GPU"):
         opt.step(grads, max_norm=1.0)
     assert "ia_adam_clip_step" not in calls
+
+
+@pytest.mark.parametrize("M,N,K,most", [(8_000_000, 256, 256, 340e6), (8_000_000, 64, 64, 140e6), (300_000, 256, 192, 80e6)])
+def test_workspace_of_narrow_gradients(M, N, K, most):
+    """Mask words and the blocks' sums; not the 4-bit copies of all rows that wider layers need (3.3 GB for the first)."""
+    assert ia.ia_mx4_linear_backward_workspace_size(M, N, K) <= most
