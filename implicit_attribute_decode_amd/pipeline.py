@@ -524,6 +524,14 @@ def _dtype(t: torch.Tensor) -> int:
     return d
 
 
+def _one_device(t: torch.Tensor, *others):
+    """Refuses tensors on several devices (None stands for no tensor)."""
+    device = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != device:
+            raise ValueError("tensors on several devices")
+
+
 class GradClip:
     """Clipping of a list of gradient tensors by their global norm (Pascanu,
     Mikolov & Bengio 2013): factor = max_norm / norm where norm > max_norm,
@@ -558,6 +566,8 @@ class GradClip:
             else:
                 raise ValueError(f"gradient {k} must be contiguous or [rows, dim] with unit column stride")
             d.out = None if self.out is None else o.data_ptr()
+        if self.grads:
+            _one_device(*self.grads)
         self.device = self.grads[0].device if self.grads else torch.device("cuda")
         self._ws_bytes = ia.ia_clip_workspace_size(len(self.grads))
 
@@ -746,6 +756,7 @@ class Mx4Tensor:
         rows = codes.shape[0]
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda or not scales.is_cuda:
             raise ValueError("codes and scales must be uint8 tensors on the GPU")
+        _one_device(codes, scales)
         if (codes.shape != (rows, 16 * blocks) or scales.shape != (rows, blocks)
                 or not codes.is_contiguous() or not scales.is_contiguous()):
             raise ValueError(f"codes [{rows}, {16 * blocks}] and scales [{rows}, {blocks}] expected, contiguous")
@@ -768,6 +779,7 @@ class Mx4Tensor:
         d, rows, cols, ld = _matrix(out, "out")
         if (rows, cols) != (self.rows, self.cols):
             raise ValueError("out has another shape")
+        _one_device(out, self._codes)
         ia.ia_mx4_dequantize(self.c, d, out, ld)
         return out
 
@@ -778,6 +790,8 @@ def mx4_quantize(x: torch.Tensor, transpose: bool = False, out: Mx4Tensor | None
     d, rows, cols, ld = _matrix(x, "x")
     if out is None:
         out = Mx4Tensor.empty(cols, rows, x.device) if transpose else Mx4Tensor.empty(rows, cols, x.device)
+    else:
+        _one_device(x, out._codes)
     ia.ia_mx4_quantize(x, d, rows, cols, ld, transpose, out.c)
     return out
 
@@ -797,6 +811,7 @@ def mx4_matmul(a: Mx4Tensor, b: Mx4Tensor, bias: torch.Tensor | None = None, act
     d, rows, cols, ld = _matrix(out, "out")
     if (rows, cols) != (a.rows, b.rows):
         raise ValueError("out has another shape")
+    _one_device(out, a._codes, b._codes, bias)
     ws = _bytes(ia.ia_mx4_matmul_workspace_size(a.rows, b.rows, a.cols), out.device)
     ia.ia_mx4_matmul(a.c, b.c, _bias(bias, b.rows), _ACTS[act], d, out, ld, ws)
     return out
@@ -815,6 +830,7 @@ def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: torch.Tensor | None = None, 
         do, rows, cols, ldy = _matrix(out, "out")
         if (do, rows, cols) != (d, M, w.rows):
             raise ValueError("out has another shape or type")
+    _one_device(x, w._codes, bias, out)
     ws = _bytes(ia.ia_mx4_linear_workspace_size(M, K, w.rows), x.device)
     ia.ia_mx4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
     return out
@@ -837,6 +853,7 @@ def mx4_linear_backward(dy: torch.Tensor, x: torch.Tensor, wt: Mx4Tensor | None,
             raise ValueError("y must have dy's type and shape")
     if want_x and (wt is None or (wt.rows, wt.cols) != (K, N)):
         raise ValueError(f"wt must be [{K}, {N}]")
+    _one_device(dy, x, y, wt._codes if want_x else None)
     dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if want_x else None
     dw = torch.empty((N, K), dtype=torch.float32, device=x.device)
     db = torch.empty(N, dtype=torch.float32, device=x.device)

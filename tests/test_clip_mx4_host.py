@@ -149,3 +149,50 @@ def test_adam_refuses_groups_on_several_devices(calls, monkeypatch):
 def test_workspace_of_narrow_gradients(M, N, K, most):
     """Mask words and the blocks' sums; not the 4-bit copies of all rows that wider layers need (3.3 GB for the first)."""
     assert ia.ia_mx4_linear_backward_workspace_size(M, N, K) <= most
+
+
+class _Packed:
+    """Stands for an Mx4Tensor with memory on the host."""
+
+    def __init__(self, rows, cols):
+        self._codes = self.codes = torch.zeros((rows, (cols + 31) // 32 * 16), dtype=torch.uint8)
+        self.rows, self.cols, self.c = rows, cols, None
+
+
+@pytest.mark.parametrize("far", ["x", "w", "bias", "out", "dy", "y", "wt", "a", "b", "q", "grad", "codes"])
+def test_tensors_on_several_devices_are_refused(calls, monkeypatch, far):
+    """One argument on another GPU: no entry point is reached."""
+    for name in ("ia_mx4_quantize", "ia_mx4_dequantize", "ia_mx4_matmul", "ia_mx4_linear"):
+        monkeypatch.setattr(ia, name, lambda *a, _n=name: calls.__setitem__(_n, a))
+    monkeypatch.setattr(P, "_bias", lambda bias, n: bias)
+    t = dict(x=torch.zeros(6, 40), bias=torch.zeros(8), out=torch.zeros(6, 8), dy=torch.zeros(6, 8), y=torch.zeros(6, 8),
+             grad=torch.zeros(9), codes=torch.zeros(6, 32, dtype=torch.uint8), w=_Packed(8, 40), wt=_Packed(40, 8),
+             a=_Packed(6, 40), b=_Packed(8, 40), q=_Packed(6, 40))
+    uses = {
+        "linear": (("x", "w", "bias", "out"), lambda: P.mx4_linear(t["x"], t["w"], t["bias"], out=t["out"])),
+        "backward": (("dy", "x", "y", "wt"), lambda: P.mx4_linear_backward(t["dy"], t["x"], t["wt"], t["y"])),
+        "matmul": (("a", "b", "bias", "out"), lambda: P.mx4_matmul(t["a"], t["b"], t["bias"], out=t["out"])),
+        "quantize": (("x", "q"), lambda: P.mx4_quantize(t["x"], out=t["q"])),
+        "dequantize": (("x", "q"), lambda: P.Mx4Tensor.dequantize(t["q"], out=t["x"])),
+        "clip": (("x", "grad"), lambda: P.GradClip([t["x"], t["grad"]])),
+        "tensor": (("codes",), None),
+    }
+    for args, call in uses.values():
+        if call:
+            call()
+    assert len(calls) == 5
+    calls.clear()
+    other = t[far]._codes if isinstance(t[far], _Packed) else t[far]
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda u: int(u is other))
+    refused = 0
+    for args, call in uses.values():
+        if call and far in args:
+            with pytest.raises(ValueError, match="several devices"):
+                call()
+            refused += 1
+    assert refused or far == "codes"
+    if far == "codes":
+        monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda u: True), raising=False)
+        with pytest.raises(ValueError, match="several devices"):
+            P.Mx4Tensor(t["codes"], torch.zeros(6, 2, dtype=torch.uint8), 40)
+    assert not calls
