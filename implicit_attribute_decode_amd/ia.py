@@ -206,8 +206,11 @@ def _stream(stream=None) -> int:
     import torch
 
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without the Stream object (1.4 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # torch.cuda.current_stream().cuda_stream without the Stream object (1.4 us a call), where torch has it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
 

@@ -196,3 +196,16 @@ def test_tensors_on_several_devices_are_refused(calls, monkeypatch, far):
         with pytest.raises(ValueError, match="several devices"):
             P.Mx4Tensor(t["codes"], torch.zeros(6, 2, dtype=torch.uint8), 40)
     assert not calls
+
+
+def test_the_current_stream_by_either_way(monkeypatch):
+    """torch's raw handle is not part of its public interface: without it the public call serves."""
+    class Stream:
+        cuda_stream = 4711
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    assert ia._stream() == 103 and ia._stream(Stream) == 4711
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert ia._stream() == 4711
