@@ -1122,10 +1122,14 @@ hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, c
     float* part = (float*)(at += scratch_bytes(K, M));
     void* mat = at + round_up((size_t)ceil_div(M, kTileRows) * (size_t)N * sizeof(float));
     ColumnOut o{};
-    // dx is a layer of N inputs and K outputs on d.  With few rows and more than two
-    // steps of them, d's blocks along the rows come cheaper from the tile that is
-    // quantised for dw: 3,122 x 817 -> 18 in bf16 21 -> 10 us.
-    const bool narrow = dx && M > 0 && is_narrow(M, N, K) && (M >= 16384 || N <= 256 || !(dw || db));
+    // dx is a layer of N inputs and K outputs on d.  Where d is quantised for dw
+    // anyway, its blocks along the rows come cheaper from the same tiles, but for few
+    // columns of 16 bits.  A backward of 30,000 rows so, and with a second reading:
+    //   817 -> 18 bf16 85, 106     600 -> 64 f32 90, 100      192 -> 300 f32 71, 79
+    //   256 -> 1,000 f32 137, 155  64 -> 2,000 f32 190, 198   64 -> 2,000 bf16 157, 149
+    // (us; 1,700 -> 11 in bf16 at 3,122 and at 60,000 rows 56, 66 and 239, 297).
+    const bool few = N <= 64 && dy.dtype != IA_DTYPE_F32;
+    const bool narrow = dx && M > 0 && is_narrow(M, N, K) && (few || !(dw || db));
     if (dx && !narrow) {
         o.rcodes = dr.codes;
         o.rscales = dr.scales;
