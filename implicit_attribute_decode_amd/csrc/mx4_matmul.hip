@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) mx4_matmul_kernel(MatA
     }
     // The sums leave through LDS, 32 rows of a wave at a time: a lane holds 16
     // columns of one row, and stores of those alone write lines piece by piece
-    // (4096^3 in bf16 58 -> 48 us, 150,000 x 32 -> 512 in fp16 127 -> 76 us).
+    // (measured with that change alone: 4,096^3 in bf16 58 -> 48 us, 150,000 x 32 -> 512
+    // in fp16 127 -> 76).
     constexpr int C = 32 * TJ;
     static_assert(32 * C * 4 * WAVES <= 4 * R * 8 * 16, "the buffers hold every wave's rows");
     __syncthreads();
@@ -398,12 +399,15 @@ __global__ void __launch_bounds__(256) mx4_join_kernel(MatArgs p, const float* p
 // copy) or two of 128 x 128, one of which multiplies while the other starts or
 // stores.  Measured, a round of 256 of the former takes 16 + 2.4 stages us, of
 // 512 of the latter 3.5 + 1.7 stages; the larger tiles leave CUs idle in their
-// last round, the smaller ones hardly.  Us with tiles of 256 and of 128:
-//   8,192^3 bf16 369, 452           4,096^3 bf16 54, 60
-//   4,096 x 4,096 -> 4,400 bf16 88, 74       3,328 x 16,384 -> 4,096 bf16 154, 185
-//   20,000 x 1,438 -> 1,548 bf16 79, 67      100,000 x 512 -> 512 f16 72, 61
-//   6,000^3 f16 207, 213            200,000 x 380 -> 1,000 f32 273, 293
-// (in the last line the rule takes tiles of 128).
+// last round, the smaller ones hardly.  Us with tiles of 256 and of 128 (products
+// of normally distributed values alone, one after another):
+//   8,192^3 bf16 317, 376           4,096^3 bf16 49, 55
+//   4,096 x 4,096 -> 4,400 bf16 79, 68       3,328 x 16,384 -> 4,096 bf16 133, 161
+//   20,000 x 1,438 -> 1,548 bf16 70, 59      100,000 x 512 -> 512 f16 61, 52
+//   8,704 x 1,000 -> 1,920 f16 36, 27        150,000 x 300 -> 512 f16 75, 74
+//   6,000^3 f16 180, 182            200,000 x 380 -> 1,000 f32 247, 259
+// The two times leave out what the stores of a large output cost: in the last line
+// the rule takes tiles of 128, 1 % and 5 % slower.
 // Where blocks of 128 are few, the sum over k goes in up to `splits` parts of
 // at least 4 stages (1,024 values), joined in order: 130 tiles of 68 stages so
 // 60 us, whole 85; but 225 tiles of 10 stages would take 29 instead of 20.

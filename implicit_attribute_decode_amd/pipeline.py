@@ -413,7 +413,7 @@ class Adam:
     mirror (e.g. the decoder's hash table) that every step refreshes, and its
     parameter may be a [rows, dim] view with rows further apart than dim (the
     x, y, z of xyzt positions).  Every update runs in ia_adam_step or
-    ia_adam_step_strided."""
+    ia_adam_step_strided, with max_norm in ia_adam_clip_step_counted."""
 
     def __init__(self, groups: dict, warmup: int, total: int, beta1: float = 0.9, beta2: float = 0.999,
                  eps: float = 1e-15):
@@ -538,7 +538,8 @@ class GradClip:
     else 1.  The tensors (float32, float16 or bfloat16 in any mix; contiguous,
     or [rows, dim] rows of a wider array) are described once and may be filled
     anew before every call; `out` (same shapes and types) receives the clipped
-    values, without it they are scaled in place.
+    values, without it they are scaled in place.  What is written must not share
+    memory with another tensor of the lists.
 
     clip(max_norm) clips and norm() only measures; both return a new device
     float32 tensor {norm, factor, 1 if the norm is finite else 0}."""

@@ -616,8 +616,9 @@ IA_API ia_status ia_clip_workspace_size(int32_t count, size_t* bytes);
  *   max_norm >= 0; +infinity never clips
  *   stats: device float[3], overwritten: {norm, factor, 1 if norm is finite
  *          else 0}.  The squares are summed in double in a fixed order (the
- *          same on every run).  An infinite element gives norm = infinity and
- *          factor 0, a NaN gives NaN for both.
+ *          same on every run; a norm past fp32's range is finite and reads
+ *          infinity).  An infinite element gives norm = infinity and factor 0
+ *          (1 where max_norm is infinite too), a NaN gives NaN for both.
  *   ws, ws_bytes: device workspace of ia_clip_workspace_size(count) bytes,
  *          256-byte aligned.
  * Asynchronous on stream; no host synchronisation.
