@@ -423,7 +423,9 @@ class Adam:
         self.warmup, self.total = warmup, total
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
         self.t = 0
-        self.skipped = None  # with the first clipped step
+        # steps that changed nothing, kept by the library on the parameters' device
+        self.skipped = next((torch.zeros(1, dtype=torch.int32, device=g["param"].device) for g in groups.values()),
+                            None)
 
     @property
     def state(self):

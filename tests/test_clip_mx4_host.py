@@ -209,3 +209,15 @@ def test_the_current_stream_by_either_way(monkeypatch):
     assert ia._stream() == 103 and ia._stream(Stream) == 4711
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert ia._stream() == 4711
+
+
+def test_the_count_of_steps_left_out_is_made_with_the_optimiser(calls, monkeypatch):
+    """Not within the first step, where a captured graph would clear it in every replay."""
+    opt, grads = _adam()
+    count = opt.skipped
+    assert count.dtype == torch.int32 and count.tolist() == [0] and count.device == grads["w"].device
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    opt.step(grads, max_norm=1.0)
+    assert opt.skipped is count and calls["ia_adam_clip_step"][-1] is count
+    empty = P.Adam({}, warmup=0, total=1)
+    assert empty.skipped is None
