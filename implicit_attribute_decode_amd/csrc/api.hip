@@ -12,6 +12,7 @@
 #include <string>
 
 #include "ia_internal.h"
+#include "philox.h"
 #include "ranges.h"
 
 namespace {
@@ -1366,6 +1367,240 @@ ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void* y, in
     hipError_t e = ia::launch_mx4_linear_backward(d, xs, dx ? view(*wt) : ia::Mx4View{}, dx, lddx, dw, db, ws,
                                                   (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "mx4 linear backward launch");
+    return IA_OK;
+}
+
+}  // extern "C"
+
+// ============================================================== dropout, embedding
+
+namespace {
+
+// The kernels' form of a dropout (null: none) and scale / (1 - p) in `factor`; `used` says whether values may drop.
+ia_status check_drop(const ia_drop* d, double scale, ia::DropArgs* a, float* factor, bool* used) {
+    *used = false;
+    double f = scale;
+    if (d) {
+        if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(IA_ERR_INVALID_ARG, "p must be in [0, 1]");
+        if (!aligned(d->step, 8)) return fail(IA_ERR_INVALID_ARG, "step is misaligned");
+        *a = ia::DropArgs{(uint64_t)std::llrint(d->p * 4294967296.0), d->seed, d->offset, d->step};
+        *used = a->limit > 0;
+        f = d->p < 1.0 ? scale / (1.0 - d->p) : 0.0;
+    }
+    *factor = (float)f;
+    if (!std::isfinite(*factor)) return fail(IA_ERR_INVALID_ARG, "scale / (1 - p) must be a finite float");
+    return IA_OK;
+}
+
+ia_status check_index(const void* index, int32_t bytes, int64_t n, int64_t stride) {
+    if (bytes != 4 && bytes != 8) return fail(IA_ERR_UNSUPPORTED, "indices have 4 or 8 bytes");
+    if (n < 0 || n > kMaxMatmulDim) return fail(IA_ERR_INVALID_ARG, "n must be in [0, 2^31)");
+    if (n == 0) return IA_OK;
+    if (stride < 0 || stride > kMaxElements / n) return fail(IA_ERR_INVALID_ARG, "the indices' stride is out of range");
+    if (!index || !aligned(index, (size_t)bytes)) return fail(IA_ERR_INVALID_ARG, "index is null or misaligned");
+    return IA_OK;
+}
+
+ia_status check_table(int64_t entries, int64_t dim) {
+    if (entries < 0 || entries > kMaxMatmulDim || dim < 0 || dim > kMaxMatmulDim)
+        return fail(IA_ERR_INVALID_ARG, "entries and dim must be in [0, 2^31)");
+    return IA_OK;
+}
+
+ia::Rows index_rows(const void* index, int32_t bytes, int64_t n, int64_t stride) {
+    return ia::rows_of(index, n, 1, stride, (size_t)bytes, false);
+}
+ia::Rows step_rows(const ia_drop* d) { return ia::bytes_of(d ? d->step : nullptr, sizeof(int64_t), false); }
+
+}  // namespace
+
+extern "C" {
+
+ia_status ia_dropout(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const ia_drop* drop, void* out,
+                     int64_t ldo, void* stream) {
+    if (!drop) return fail(IA_ERR_INVALID_ARG, "drop is null");
+    ia_status st = check_matrix(x, dtype, rows, cols, ldx, true, "x");
+    if (st == IA_OK) st = check_matrix(out, dtype, rows, cols, ldo, false, "out");
+    if (st == IA_OK && (rows > kMaxMatmulDim || cols > kMaxMatmulDim))
+        st = fail(IA_ERR_INVALID_ARG, "rows and cols must be in [0, 2^31)");
+    ia::DropArgs a{};
+    float factor;
+    bool used;
+    if (st == IA_OK) st = check_drop(drop, 1.0, &a, &factor, &used);
+    if (st != IA_OK) return st;
+    const bool in_place = out == x && (ldo == ldx || rows <= 1);
+    const ia::Rows r[] = {in_place ? ia::Rows{} : input_rows(x, dtype, rows, cols, ldx),
+                          output_rows(out, dtype, rows, cols, ldo), step_rows(drop)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_dropout(x, dtype, rows, cols, ldx, a, factor, out, ldo, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "dropout launch");
+    return IA_OK;
+}
+
+ia_status ia_embedding(const void* table, int32_t dtype, int64_t entries, int64_t dim, int64_t ld, const void* index,
+                       int32_t index_bytes, int64_t n, int64_t index_stride, double scale, const ia_drop* drop,
+                       int32_t out_dtype, void* out, int64_t ldo, void* stream) {
+    ia_status st = check_table(entries, dim);
+    if (st == IA_OK) st = check_matrix(table, dtype, entries, dim, ld, true, "table");
+    if (st == IA_OK) st = check_index(index, index_bytes, n, index_stride);
+    if (st == IA_OK) st = check_matrix(out, out_dtype, n, dim, ldo, false, "out");
+    ia::DropArgs a{};
+    float factor;
+    bool used;
+    if (st == IA_OK) st = check_drop(drop, scale, &a, &factor, &used);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {input_rows(table, dtype, entries, dim, ld), index_rows(index, index_bytes, n, index_stride),
+                          step_rows(drop), output_rows(out, out_dtype, n, dim, ldo)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_embedding(table, dtype, entries, dim, ld, ia::Indices{index, n, index_stride, index_bytes},
+                                        factor, used ? &a : nullptr, out_dtype, out, ldo, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "embedding launch");
+    return IA_OK;
+}
+
+ia_status ia_embedding_mx4(const ia_mx4* table, const void* index, int32_t index_bytes, int64_t n, int64_t index_stride,
+                           double scale, const ia_drop* drop, int32_t out_dtype, void* out, int64_t ldo, void* stream) {
+    ia_status st = check_mx4(table, "table");
+    if (st == IA_OK) st = check_table(table->rows, table->cols);
+    if (st == IA_OK) st = check_index(index, index_bytes, n, index_stride);
+    if (st == IA_OK) st = check_matrix(out, out_dtype, n, table->cols, ldo, false, "out");
+    ia::DropArgs a{};
+    float factor;
+    bool used;
+    if (st == IA_OK) st = check_drop(drop, scale, &a, &factor, &used);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {codes_rows(*table, false), scales_rows(*table, false),
+                          index_rows(index, index_bytes, n, index_stride), step_rows(drop),
+                          output_rows(out, out_dtype, n, table->cols, ldo)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_embedding_mx4(view(*table), ia::Indices{index, n, index_stride, index_bytes}, factor,
+                                            used ? &a : nullptr, out_dtype, out, ldo, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "embedding launch");
+    return IA_OK;
+}
+
+ia_status ia_embedding_backward_workspace_size(int64_t n, int64_t entries, int64_t dim, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    ia_status st = check_table(entries, dim);
+    if (st == IA_OK && (n < 0 || n > kMaxMatmulDim)) st = fail(IA_ERR_INVALID_ARG, "n must be in [0, 2^31)");
+    if (st == IA_OK && dim > 0 && !(size_ok(n, dim) && size_ok(entries, dim)))
+        st = fail(IA_ERR_INVALID_ARG, "at most 2^40 values");
+    if (st != IA_OK) return st;
+    *bytes = ia::embedding_backward_workspace(n, entries, dim);
+    return IA_OK;
+}
+
+ia_status ia_embedding_backward(const void* dy, int32_t dtype, int64_t dim, int64_t lddy, const void* index,
+                                int32_t index_bytes, int64_t n, int64_t index_stride, int64_t entries, double scale,
+                                const ia_drop* drop, float* grad, void* ws, size_t ws_bytes, void* stream) {
+    ia_status st = check_table(entries, dim);
+    if (st == IA_OK) st = check_index(index, index_bytes, n, index_stride);
+    if (st == IA_OK) st = check_matrix(dy, dtype, n, dim, lddy, true, "dy");
+    if (st == IA_OK) st = check_matrix(grad, IA_DTYPE_F32, entries, dim, dim, false, "grad");
+    ia::DropArgs a{};
+    float factor;
+    bool used;
+    if (st == IA_OK) st = check_drop(drop, scale, &a, &factor, &used);
+    if (st != IA_OK) return st;
+    const size_t need = ia::embedding_backward_workspace(n, entries, dim);
+    st = check_ws(ws, ws_bytes, need);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {input_rows(dy, dtype, n, dim, lddy), index_rows(index, index_bytes, n, index_stride),
+                          step_rows(drop), output_rows(grad, IA_DTYPE_F32, entries, dim, dim), ia::bytes_of(ws, need, true)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_embedding_backward(dy, dtype, dim, lddy, ia::Indices{index, n, index_stride, index_bytes},
+                                                 entries, factor, used ? &a : nullptr, grad, ws, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "embedding backward launch");
+    return IA_OK;
+}
+
+}  // extern "C"
+
+// ============================================================== group-scaled 4 bits
+
+namespace {
+
+ia_status check_q4(const ia_q4* q, const char* name) {
+    if (!q) return fail(IA_ERR_INVALID_ARG, std::string(name) + " is null");
+    if (q->group != 32 && q->group != 64 && q->group != 128)
+        return fail(IA_ERR_UNSUPPORTED, std::string(name) + ": groups are of 32, 64 or 128 values");
+    if (q->rows < 0 || q->cols < 0 || (q->cols > 0 && !size_ok(q->rows, q->cols)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": sizes must be >= 0 with at most 2^40 values");
+    if (q->rows > 0 && q->cols > 0 && (!q->codes || !q->words || !aligned(q->codes, 16) || !aligned(q->words, 16)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": codes or words null or not 16-byte aligned");
+    return IA_OK;
+}
+
+int64_t groups_of(const ia_q4& q) { return (q.cols + q.group - 1) / q.group; }
+ia::Rows q4_codes(const ia_q4& q, bool written) {
+    return ia::bytes_of(q.codes, (size_t)q.rows * (size_t)groups_of(q) * (size_t)(q.group / 2), written);
+}
+ia::Rows q4_words(const ia_q4& q, bool written) {
+    return ia::bytes_of(q.words, (size_t)q.rows * (size_t)((groups_of(q) + 3) / 4 * 16), written);
+}
+ia::Q4View view(const ia_q4& q) { return ia::Q4View{q.codes, q.words, q.rows, q.cols, q.group}; }
+
+}  // namespace
+
+extern "C" {
+
+ia_status ia_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const ia_q4* out, void* stream) {
+    ia_status st = check_q4(out, "out");
+    if (st == IA_OK) st = check_matrix(x, dtype, out->rows, out->cols, ldx, true, "x");
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {input_rows(x, dtype, out->rows, out->cols, ldx), q4_codes(*out, true), q4_words(*out, true)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_q4_quantize(x, dtype, ldx, view(*out), (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "q4 quantize launch");
+    return IA_OK;
+}
+
+ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_t ldx, void* stream) {
+    ia_status st = check_q4(q, "q");
+    if (st == IA_OK) st = check_matrix(x, dtype, q->rows, q->cols, ldx, false, "x");
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {q4_codes(*q, false), q4_words(*q, false), output_rows(x, dtype, q->rows, q->cols, ldx)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_q4_dequantize(view(*q), dtype, x, ldx, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "q4 dequantize launch");
+    return IA_OK;
+}
+
+ia_status ia_q4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes) {
+    if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    ia_status st = check_product(M, N, K, IA_ACT_NONE, nullptr);
+    if (st != IA_OK) return st;
+    *bytes = ia::q4_linear_workspace(M, K, N);
+    return IA_OK;
+}
+
+ia_status ia_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const ia_q4* w, const float* bias, int32_t act,
+                       void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    ia_status st = check_q4(w, "w");
+    if (st != IA_OK) return st;
+    st = check_product(M, w->rows, w->cols, act, bias);
+    if (st == IA_OK) st = check_matrix(x, dtype, M, w->cols, ldx, true, "x");
+    if (st == IA_OK) st = check_matrix(y, dtype, M, w->rows, ldy, false, "y");
+    if (st != IA_OK) return st;
+    const size_t need = ia::q4_linear_workspace(M, w->cols, w->rows);
+    st = check_ws(ws, ws_bytes, need);
+    if (st != IA_OK) return st;
+    const ia::Rows r[] = {input_rows(x, dtype, M, w->cols, ldx),
+                          q4_codes(*w, false),
+                          q4_words(*w, false),
+                          input_rows(bias, IA_DTYPE_F32, 1, w->rows, 0),
+                          output_rows(y, dtype, M, w->rows, ldy),
+                          ia::bytes_of(ws, need, true)};
+    st = check_clash(r);
+    if (st != IA_OK) return st;
+    hipError_t e = ia::launch_q4_linear(x, dtype, M, ldx, view(*w), bias, act, y, ldy, ws, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "q4 linear launch");
     return IA_OK;
 }
 

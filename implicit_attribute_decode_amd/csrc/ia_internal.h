@@ -363,4 +363,45 @@ size_t mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_linear_backward(const Mx4Source& dy, const Mx4Source& x, const Mx4View& wt, void* dx, int64_t lddx,
                                       float* dw, float* db, void* ws, hipStream_t s);
 
+// ---------------------------------------------------------------- dropout, embedding
+
+struct DropArgs;  // philox.h
+
+hipError_t launch_dropout(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const DropArgs& a,
+                          float factor, void* out, int64_t ldo, hipStream_t s);
+
+// n indices of `bytes` (4 or 8) each, `stride` elements apart
+struct Indices {
+    const void* index;
+    int64_t n, stride;
+    int32_t bytes;
+};
+
+// out[i] = factor * table[index[i]], with `drop` where kept; zeros where the index is no entry
+hipError_t launch_embedding(const void* table, int32_t dtype, int64_t entries, int64_t dim, int64_t ld, const Indices& ix,
+                            float factor, const DropArgs* drop, int32_t out_dtype, void* out, int64_t ldo, hipStream_t s);
+hipError_t launch_embedding_mx4(const Mx4View& table, const Indices& ix, float factor, const DropArgs* drop,
+                                int32_t out_dtype, void* out, int64_t ldo, hipStream_t s);
+// grad [entries][dim] = factor * the sums of the rows of dy, overwritten
+size_t embedding_backward_workspace(int64_t n, int64_t entries, int64_t dim);
+hipError_t launch_embedding_backward(const void* dy, int32_t dtype, int64_t dim, int64_t lddy, const Indices& ix,
+                                     int64_t entries, float factor, const DropArgs* drop, float* grad, void* ws,
+                                     hipStream_t s);
+
+// ---------------------------------------------------------------- group-scaled 4 bits
+
+// codes [rows][groups][group / 2], words [rows][groups rounded up to a multiple of 4]
+struct Q4View {
+    uint8_t* codes;
+    uint32_t* words;
+    int64_t rows, cols;
+    int32_t group;
+};
+
+hipError_t launch_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const Q4View& out, hipStream_t s);
+hipError_t launch_q4_dequantize(const Q4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s);
+size_t q4_linear_workspace(int64_t M, int64_t K, int64_t N);
+hipError_t launch_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const Q4View& w, const float* bias,
+                            int32_t act, void* y, int64_t ldy, void* ws, hipStream_t s);
+
 }  // namespace ia

@@ -44,6 +44,9 @@ EXPORTS = ("ia_last_error", "ia_decoder_create", "ia_decoder_set_params", "ia_de
            "ia_mx4_quantize", "ia_mx4_dequantize", "ia_mx4_matmul_workspace_size", "ia_mx4_matmul",
            "ia_mx4_linear_workspace_size", "ia_mx4_linear", "ia_mx4_linear_backward_workspace_size",
            "ia_mx4_linear_backward",
+           "ia_dropout", "ia_embedding", "ia_embedding_mx4", "ia_embedding_backward_workspace_size",
+           "ia_embedding_backward",
+           "ia_q4_quantize", "ia_q4_dequantize", "ia_q4_linear_workspace_size", "ia_q4_linear",
            "ia_profile_enable", "ia_profile_report", "ia_profile_reset")
 
 
@@ -116,6 +119,15 @@ class Mx4(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64)]
 
 
+class Drop(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64), ("step", C.c_void_p)]
+
+
+class Q4(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("words", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("group", C.c_int32)]
+
+
 _lib = None
 P = C.c_void_p
 
@@ -182,6 +194,17 @@ def load(path: str = LIB_PATH):
         L.ia_mx4_linear_backward_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
         L.ia_mx4_linear_backward.argtypes = [P, C.c_int64, P, C.c_int64, P, C.c_int64, C.c_int32, C.c_int64, C.c_int64,
                                              C.c_int64, P, P, C.c_int64, P, P, P, C.c_size_t, P]
+        L.ia_dropout.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, P, P, C.c_int64, P]
+        L.ia_embedding.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, P, C.c_int32, C.c_int64, C.c_int64,
+                                   C.c_double, P, C.c_int32, P, C.c_int64, P]
+        L.ia_embedding_mx4.argtypes = [P, P, C.c_int32, C.c_int64, C.c_int64, C.c_double, P, C.c_int32, P, C.c_int64, P]
+        L.ia_embedding_backward_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_embedding_backward.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, P, C.c_int32, C.c_int64, C.c_int64,
+                                            C.c_int64, C.c_double, P, P, P, C.c_size_t, P]
+        L.ia_q4_quantize.argtypes = [P, C.c_int32, C.c_int64, P, P]
+        L.ia_q4_dequantize.argtypes = [P, C.c_int32, P, C.c_int64, P]
+        L.ia_q4_linear_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_q4_linear.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, P, P, C.c_int32, P, C.c_int64, P, C.c_size_t, P]
         L.ia_profile_enable.argtypes = [C.c_int32]
         L.ia_profile_report.argtypes = [P, C.c_size_t, P]
         L.ia_profile_reset.argtypes = []
@@ -540,6 +563,67 @@ def ia_mx4_linear_backward(dy, lddy: int, y, ldy: int, x, ldx: int, dtype: int, 
     _check(load().ia_mx4_linear_backward(_ptr(dy), lddy, _ptr(y), ldy, _ptr(x), ldx, dtype, M, N, K,
                                          None if wt is None else C.byref(wt), _ptr(dx), lddx, _ptr(dw), _ptr(db),
                                          _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+# ----------------------------------------------------------------- embeddings, dropout
+
+
+def _ref(s):
+    return None if s is None else C.byref(s)
+
+
+def ia_dropout(x, dtype: int, rows: int, cols: int, ldx: int, drop: Drop, out, ldo: int, stream=None):
+    _check(load().ia_dropout(_ptr(x), dtype, rows, cols, ldx, _ref(drop), _ptr(out), ldo, _stream(stream)))
+
+
+def ia_embedding(table, dtype: int, entries: int, dim: int, ld: int, index, index_bytes: int, n: int, index_stride: int,
+                 scale: float, drop: Drop | None, out_dtype: int, out, ldo: int, stream=None):
+    _check(load().ia_embedding(_ptr(table), dtype, entries, dim, ld, _ptr(index), index_bytes, n, index_stride, scale,
+                               _ref(drop), out_dtype, _ptr(out), ldo, _stream(stream)))
+
+
+def ia_embedding_mx4(table: Mx4, index, index_bytes: int, n: int, index_stride: int, scale: float, drop: Drop | None,
+                     out_dtype: int, out, ldo: int, stream=None):
+    _check(load().ia_embedding_mx4(C.byref(table), _ptr(index), index_bytes, n, index_stride, scale, _ref(drop), out_dtype,
+                                   _ptr(out), ldo, _stream(stream)))
+
+
+def ia_embedding_backward_workspace_size(n: int, entries: int, dim: int) -> int:
+    b = C.c_size_t()
+    _check(load().ia_embedding_backward_workspace_size(n, entries, dim, C.byref(b)))
+    return b.value
+
+
+def ia_embedding_backward(dy, dtype: int, dim: int, lddy: int, index, index_bytes: int, n: int, index_stride: int,
+                          entries: int, scale: float, drop: Drop | None, grad, ws=None, stream=None):
+    _check(load().ia_embedding_backward(_ptr(dy), dtype, dim, lddy, _ptr(index), index_bytes, n, index_stride, entries,
+                                        scale, _ref(drop), _ptr(grad), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+# ----------------------------------------------------------------- group-scaled 4 bits
+
+
+def q4(codes, words, rows: int, cols: int, group: int) -> Q4:
+    return Q4(_ptr(codes), _ptr(words), rows, cols, group)
+
+
+def ia_q4_quantize(x, dtype: int, ldx: int, out: Q4, stream=None):
+    _check(load().ia_q4_quantize(_ptr(x), dtype, ldx, C.byref(out), _stream(stream)))
+
+
+def ia_q4_dequantize(q: Q4, dtype: int, x, ldx: int, stream=None):
+    _check(load().ia_q4_dequantize(C.byref(q), dtype, _ptr(x), ldx, _stream(stream)))
+
+
+def ia_q4_linear_workspace_size(M: int, K: int, N: int) -> int:
+    n = C.c_size_t()
+    _check(load().ia_q4_linear_workspace_size(M, K, N, C.byref(n)))
+    return n.value
+
+
+def ia_q4_linear(x, dtype: int, M: int, ldx: int, w: Q4, bias, act: int, y, ldy: int, ws=None, stream=None):
+    _check(load().ia_q4_linear(_ptr(x), dtype, M, ldx, C.byref(w), _ptr(bias), act, _ptr(y), ldy, _ptr(ws), _nbytes(ws),
+                               _stream(stream)))
 
 
 # ----------------------------------------------------------------- diagnostics

@@ -892,3 +892,216 @@ class Mx4Linear:
         if self.act == "relu" and y is None:
             raise ValueError("a ReLU layer's backward needs its output y")
         return mx4_linear_backward(dy, x, self.wt, y if self.act == "relu" else None, want_x)
+
+
+def _here(t: torch.Tensor):
+    """Refuses a tensor that is not on the current GPU, whose stream the call takes."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current device")
+
+
+class Dropout:
+    """Dropout with probability p whose mask is computed from the place of a
+    value and stored nowhere: value (r, c) is kept, and divided by 1 - p, where
+    word c mod 4 of Philox4x32-10 (counter (c // 4, r, offset), key seed) is at
+    least p 2^32.  The same p, seed and offset give the same mask: each layer and
+    each step takes an offset of its own, and the backward that of its forward.
+
+    step: a device int64 tensor of one element that is added to offset when the
+    work runs (not when it is enqueued), for captured graphs that are replayed."""
+
+    __slots__ = ("p", "seed", "offset", "_step", "c")
+
+    def __init__(self, p: float, seed: int, offset: int = 0, step: torch.Tensor | None = None):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError("p must be in [0, 1]")
+        if not (0 <= seed < 2 ** 64 and 0 <= offset < 2 ** 64):
+            raise ValueError("seed and offset must be in [0, 2^64)")
+        if step is not None and (step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda):
+            raise ValueError("step must be an int64 tensor of one element on the GPU")
+        self.p, self.seed, self.offset, self._step = p, seed, offset, step
+        self.c = ia.Drop(p, seed, offset, None if step is None else step.data_ptr())
+
+    step = property(lambda self: self._step)
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """x [rows, cols] (float32, float16 or bfloat16) with dropout; out may be x."""
+        d, rows, cols, ldx = _matrix(x, "x")
+        if out is None:
+            out, ldo = torch.empty((rows, cols), dtype=x.dtype, device=x.device), cols
+        else:
+            do, r, c, ldo = _matrix(out, "out")
+            if (do, r, c) != (d, rows, cols):
+                raise ValueError("out has another shape or type")
+        _here(x)
+        _one_device(x, out, self._step)
+        ia.ia_dropout(x, d, rows, cols, ldx, self.c, out, ldo)
+        return out
+
+    def backward(self, dy: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The input's gradient for upstream dy: the same values kept, the same factor."""
+        return self(dy, out)
+
+
+_INDEX_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _index(index: torch.Tensor):
+    """(bytes of an index, their number, their stride)."""
+    b = _INDEX_BYTES.get(index.dtype)
+    if b is None or index.dim() != 1 or not index.is_cuda:
+        raise ValueError("index must be a 1-D int32 or int64 tensor on the GPU")
+    return b, index.shape[0], index.stride(0)
+
+
+def embedding(table, index: torch.Tensor, scale: float = 1.0, dtype=None, dropout: Dropout | None = None,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """scale * table[index], with dropout of the result where asked: [n, dim] of
+    dtype (the table's type by default, float32 for an Mx4Tensor).  table is a
+    [entries, dim] tensor (float32, float16 or bfloat16) or an Mx4Tensor, whose
+    picked rows alone are read back.  An index outside [0, entries) gives a row
+    of zeros."""
+    b, n, stride = _index(index)
+    if packed := isinstance(table, Mx4Tensor):
+        entries, dim, device, own = table.rows, table.cols, table._codes.device, torch.float32
+    else:
+        d, entries, dim, ld = _matrix(table, "table")
+        device, own = table.device, table.dtype
+    if out is None:
+        out, ldo = torch.empty((n, dim), dtype=dtype or own, device=device), dim
+        do = _dtype(out)
+    else:
+        do, rows, cols, ldo = _matrix(out, "out")
+        if (rows, cols) != (n, dim) or dtype not in (None, out.dtype):
+            raise ValueError("out has another shape or type")
+    _here(index)
+    _one_device(index, table._codes if packed else table, out, dropout and dropout._step)
+    drop = dropout and dropout.c
+    if packed:
+        ia.ia_embedding_mx4(table.c, index, b, n, stride, scale, drop, do, out, ldo)
+    else:
+        ia.ia_embedding(table, d, entries, dim, ld, index, b, n, stride, scale, drop, do, out, ldo)
+    return out
+
+
+def embedding_backward(dy: torch.Tensor, index: torch.Tensor, entries: int, scale: float = 1.0,
+                       dropout: Dropout | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The table's gradient [entries, dim] (float32, dense) of embedding(table,
+    index, scale, dropout=dropout) for upstream dy [n, dim]: the sum of the rows
+    that picked an entry, zeros where none did; the same on every run."""
+    b, n, stride = _index(index)
+    d, rows, dim, ld = _matrix(dy, "dy")
+    if rows != n:
+        raise ValueError(f"dy has {rows} rows for {n} indices")
+    if out is None:
+        out = torch.empty((entries, dim), dtype=torch.float32, device=dy.device)
+    elif out.dtype != torch.float32 or out.shape != (entries, dim) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous float32 [{entries}, {dim}]")
+    _here(index)
+    _one_device(index, dy, out, dropout and dropout._step)
+    ws = _bytes(ia.ia_embedding_backward_workspace_size(n, entries, dim), dy.device)
+    ia.ia_embedding_backward(dy, d, dim, ld, index, b, n, stride, entries, scale, dropout and dropout.c, out, ws)
+    return out
+
+
+class Q4Tensor:
+    """A [rows, cols] matrix in 4 bits with a scale and a zero for each group of
+    32, 64 or 128 values of a row, which stand for scale * (code - zero): codes
+    uint8 [rows, groups * group / 2] (two a byte, the earlier one in the low
+    half), words int32 [rows, groups rounded up to 4] (the bits of the scale as a
+    float32 whose lowest byte is zero, and in that byte the zero, 0..15)."""
+
+    __slots__ = ("_codes", "_words", "rows", "cols", "group", "c")
+
+    def __init__(self, codes: torch.Tensor, words: torch.Tensor, cols: int, group: int):
+        if group not in (32, 64, 128):
+            raise ValueError("groups are of 32, 64 or 128 values")
+        groups, rows = (cols + group - 1) // group, codes.shape[0]
+        if codes.dtype != torch.uint8 or words.dtype != torch.int32 or not codes.is_cuda or not words.is_cuda:
+            raise ValueError("codes must be uint8 and words int32 tensors on the GPU")
+        _one_device(codes, words)
+        shapes = (rows, groups * group // 2), (rows, (groups + 3) // 4 * 4)
+        if (codes.shape, words.shape) != shapes or not codes.is_contiguous() or not words.is_contiguous():
+            raise ValueError(f"codes {list(shapes[0])} and words {list(shapes[1])} expected, contiguous")
+        self._codes, self._words, self.rows, self.cols, self.group = codes, words, rows, cols, group
+        self.c = ia.q4(codes, words, rows, cols, group)
+
+    codes = property(lambda self: self._codes)
+    words = property(lambda self: self._words)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, group: int = 128, device="cuda"):
+        if group not in (32, 64, 128):
+            raise ValueError("groups are of 32, 64 or 128 values")
+        groups = (cols + group - 1) // group
+        return cls(torch.empty((rows, groups * group // 2), dtype=torch.uint8, device=device),
+                   torch.empty((rows, (groups + 3) // 4 * 4), dtype=torch.int32, device=device), cols, group)
+
+    @classmethod
+    def from_parts(cls, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | int, cols: int, group: int):
+        """From codes and a [rows, groups] tensor of scales (rounded to 16
+        significant bits; exact for float16 and bfloat16) and of zeros in 0..15
+        (or one zero for all)."""
+        bits = scales.to(torch.float32).contiguous().view(torch.int32)
+        bits = torch.where(torch.isfinite(scales), bits + 127 + ((bits >> 8) & 1), bits) & ~255
+        zeros = torch.as_tensor(zeros, device=scales.device)
+        if zeros.dtype.is_floating_point or bool(((zeros < 0) | (zeros > 15)).any()):
+            raise ValueError("zeros must be whole numbers in 0..15")
+        words = bits | zeros.to(torch.int32)
+        return cls(codes, torch.nn.functional.pad(words, (0, -words.shape[1] % 4)).contiguous(), cols, group)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """[rows, groups] float32."""
+        return (self._words[:, :(self.cols + self.group - 1) // self.group] & ~255).view(torch.float32)
+
+    @property
+    def zeros(self) -> torch.Tensor:
+        """[rows, groups] int32."""
+        return self._words[:, :(self.cols + self.group - 1) // self.group] & 255
+
+    def dequantize(self, dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The values, rounded once to dtype (float32, float16 or bfloat16)."""
+        if out is None:
+            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self._codes.device)
+        d, rows, cols, ld = _matrix(out, "out")
+        if (rows, cols) != (self.rows, self.cols):
+            raise ValueError("out has another shape")
+        _here(out)
+        _one_device(out, self._codes)
+        ia.ia_q4_dequantize(self.c, d, out, ld)
+        return out
+
+
+def q4_quantize(x: torch.Tensor, group: int = 128, out: Q4Tensor | None = None) -> Q4Tensor:
+    """x [rows, cols] in 4 bits with a scale and a zero for each group of a row:
+    scale = (greatest - least) / 15, zero included, codes rounded to nearest."""
+    d, rows, cols, ld = _matrix(x, "x")
+    if out is None:
+        out = Q4Tensor.empty(rows, cols, group, x.device)
+    elif (out.rows, out.cols) != (rows, cols):
+        raise ValueError("out has another shape")
+    _here(x)
+    _one_device(x, out._codes)
+    ia.ia_q4_quantize(x, d, ld, out.c)
+    return out
+
+
+def q4_linear(x: torch.Tensor, w: Q4Tensor, bias: torch.Tensor | None = None, act: str = "none",
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """A linear layer with 4-bit weights and its input as it is: act(x w^T +
+    bias), x [M, K], w [N, K]; returns [M, N] of x's type; act "none" or "relu"."""
+    d, M, K, ldx = _matrix(x, "x")
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, the weights {w.cols}")
+    if out is None:
+        out, ldy = torch.empty((M, w.rows), dtype=x.dtype, device=x.device), w.rows
+    else:
+        do, rows, cols, ldy = _matrix(out, "out")
+        if (do, rows, cols) != (d, M, w.rows):
+            raise ValueError("out has another shape or type")
+    _here(x)
+    _one_device(x, w._codes, bias, out)
+    ws = _bytes(ia.ia_q4_linear_workspace_size(M, K, w.rows), x.device)
+    ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
+    return out

@@ -56,7 +56,7 @@ typedef int32_t ia_status;
 
 #define IA_DTYPE_F32 0
 #define IA_DTYPE_F16 1
-#define IA_DTYPE_BF16 2 /* gradient norm / clipping and MXFP4 entry points only */
+#define IA_DTYPE_BF16 2 /* gradient norm / clipping, 4-bit, embedding and dropout entry points only */
 
 #define IA_ACT_NONE (-1) /* ia_mx4_matmul and ia_mx4_linear only                */
 #define IA_ACT_RELU 0
@@ -753,6 +753,121 @@ IA_API ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void
                                         int64_t ldx, int32_t dtype, int64_t M, int64_t N, int64_t K, const ia_mx4* wt,
                                         void* dx, int64_t lddx, float* dw, float* db, void* ws, size_t ws_bytes,
                                         void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Tables of codes (embeddings) and dropout                                  */
+/* ------------------------------------------------------------------------ */
+
+/* Dropout with probability p.  Nothing is stored: value (r, c) of a matrix is
+ * kept where word c mod 4 of Philox4x32-10 (Salmon, Moraes, Dror & Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) of the counter
+ * (c / 4, r, low half of o, high half of o) and the key (low half, high half of
+ * seed) is at least p 2^32 rounded to a whole number, and then divided by
+ * 1 - p.  o = offset + *step numbers the call: give each layer and each step
+ * its own, and the gradient the one of its forward. */
+typedef struct {
+    double p;            /* in [0, 1]; 1 drops everything                      */
+    uint64_t seed;
+    uint64_t offset;
+    const int64_t* step; /* device, 8-byte aligned, or NULL: read when the work
+                            runs, so that a captured graph drops anew on every
+                            replay                                             */
+} ia_drop;
+
+/* out[r][c] = x[r][c] / (1 - p) where kept, else 0 (also for a NaN), rounded
+ * once: x, out [rows][cols] of dtype (F32, F16, BF16), rows ldx (0 repeats one
+ * row) and ldo apart; rows, cols < 2^31.  out may be x (with the same stride).
+ * Its gradient is the same call on the upstream gradient.
+ * Errors: INVALID_ARG (null, sizes, strides, misalignment, p, other overlap),
+ * UNSUPPORTED (dtype), DEVICE. */
+IA_API ia_status ia_dropout(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, const ia_drop* drop,
+                            void* out, int64_t ldo, void* stream);
+
+/* out[i] = scale * table[index[i]] for i < n, with dropout of out's values
+ * where drop is not NULL; one product in fp32 by scale / (1 - p), rounded once
+ * to out_dtype.  An index outside [0, entries) (such as -1 for padding) gives
+ * a row of zeros.
+ *   table: device [entries][dim] of dtype, rows ld apart (0 repeats one row)
+ *   index: device, index_bytes = 4 (int32) or 8 (int64), index_stride elements
+ *          apart (0 repeats one)
+ *   out:   device [n][dim] of out_dtype (any of F32, F16, BF16), rows ldo apart;
+ *          must not overlap an input
+ * n, entries, dim < 2^31.  Errors: INVALID_ARG (null, sizes, strides,
+ * misalignment, p, a scale / (1 - p) that is no finite float, overlap),
+ * UNSUPPORTED (dtype, index_bytes), DEVICE. */
+IA_API ia_status ia_embedding(const void* table, int32_t dtype, int64_t entries, int64_t dim, int64_t ld, const void* index,
+                              int32_t index_bytes, int64_t n, int64_t index_stride, double scale, const ia_drop* drop,
+                              int32_t out_dtype, void* out, int64_t ldo, void* stream);
+
+/* ia_embedding of a table kept in MXFP4 (entries = table->rows, dim =
+ * table->cols): the rows picked are read back, no others.  Blocks with the NaN
+ * scale give NaN. */
+IA_API ia_status ia_embedding_mx4(const ia_mx4* table, const void* index, int32_t index_bytes, int64_t n,
+                                  int64_t index_stride, double scale, const ia_drop* drop, int32_t out_dtype, void* out,
+                                  int64_t ldo, void* stream);
+
+/* The table's gradient for upstream dy [n][dim] (dtype, rows lddy apart, 0
+ * repeats one row):
+ *   grad[v] = scale / (1 - p) * sum over i with index[i] = v of dy[i] where kept
+ * for every entry (zeros where no index picks it), device fp32 [entries][dim]
+ * dense, overwritten.  The rows are sorted by entry and added in that order in
+ * fp32, many rows of one entry in blocks joined in double: the same result on
+ * every run.  Indices outside [0, entries) take no part.  drop as in the
+ * forward call.  grad, ws (ia_embedding_backward_workspace_size bytes, 256-byte
+ * aligned, may be NULL when that is 0) must not overlap other memory of the call.
+ * Errors: as ia_embedding, WORKSPACE_TOO_SMALL. */
+IA_API ia_status ia_embedding_backward_workspace_size(int64_t n, int64_t entries, int64_t dim, size_t* bytes);
+IA_API ia_status ia_embedding_backward(const void* dy, int32_t dtype, int64_t dim, int64_t lddy, const void* index,
+                                       int32_t index_bytes, int64_t n, int64_t index_stride, int64_t entries, double scale,
+                                       const ia_drop* drop, float* grad, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit weights with group scales                                           */
+/* ------------------------------------------------------------------------ */
+
+/* A matrix whose rows are groups of 32, 64 or 128 values.  A group has a scale
+ * s and a zero z in 0..15 and stands for s (q - z), q in 0..15; two codes q to
+ * a byte, the earlier one in the low half.  groups = ceil(cols / group); codes
+ * past a row's end are ignored.  One word holds a group's scale and zero: the
+ * bits of s as a float whose lowest byte is zero, and z in that byte.  Rows of
+ * words are padded to a multiple of four (the padding is ignored). */
+typedef struct {
+    uint8_t* codes;  /* device [rows][groups * group / 2], 16-byte aligned     */
+    uint32_t* words; /* device [rows][groups rounded up to 4], 16-byte aligned */
+    int64_t rows;
+    int64_t cols;
+    int32_t group;   /* 32, 64 or 128                                          */
+} ia_q4;
+
+/* Quantise x [out->rows][out->cols] (dtype F32, F16 or BF16, rows ldx apart, 0
+ * repeats one row).  For each group, lo and hi its least and greatest value, 0
+ * included:
+ *   s = (hi - lo) / 15 in double, rounded up to 16 significant bits, at least
+ *       2^-100 (0 for a group of zeros)
+ *   z = -lo / s rounded to nearest, ties to even
+ *   q = x / s rounded to nearest, ties to even, plus z, held to 0..15.
+ * A group with a NaN or an infinity has the scale NaN and zero codes.  out must
+ * not overlap x.  Errors: INVALID_ARG (null, sizes, 0 < ldx < cols,
+ * misalignment, over 2^40 values, overlap), UNSUPPORTED (dtype, group), DEVICE. */
+IA_API ia_status ia_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const ia_q4* out, void* stream);
+
+/* x[rows][cols] (rows ldx >= cols apart) = s (q - z), rounded once to dtype.
+ * Errors: as ia_q4_quantize. */
+IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_t ldx, void* stream);
+
+/* A linear layer with such weights and its input as it is: y = act(x w^T +
+ * bias), x [M][K] of dtype (rows ldx apart, 0 repeats one row), w [N][K], y
+ * [M][N] of dtype (rows ldy apart).  Any M from one row (serving) up.  A group's
+ * products are summed in fp32 (those of fp32 rows exactly taken apart), scaled in
+ * fp32 and added in fp32, rounded once, in a fixed order.  bias: device fp32 [N]
+ * or NULL; act: IA_ACT_NONE or IA_ACT_RELU.  K = 0 gives act(bias).  y must not
+ * overlap an input, nor ws (ia_q4_linear_workspace_size bytes, 256-byte aligned,
+ * may be NULL when that is 0) anything.  M, N, K < 2^31.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, act, group), WORKSPACE_TOO_SMALL,
+ * DEVICE. */
+IA_API ia_status ia_q4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes);
+IA_API ia_status ia_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const ia_q4* w, const float* bias,
+                              int32_t act, void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Diagnostics: per-kernel timing with HIP events                            */

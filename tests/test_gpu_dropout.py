@@ -1,0 +1,119 @@
+"""Dropout through the C ABI against the fp64 oracle: which values drop is fixed
+by the generator (exact); a kept value is one fp32 product by an fp32 factor
+(2^-24 each), then half a step of its type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import codes as O
+from implicit_attribute_decode_amd.pipeline import Dropout
+
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+TYPES = list(UNIT)
+ids = lambda v: str(v).replace("torch.", "") if isinstance(v, torch.dtype) else None  # noqa: E731
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _assert_dropped(got, x, p, seed, offset=0):
+    want = O.dropout(_f64(x), p, seed, offset)
+    on = O.kept(*x.shape, p, seed, offset)
+    g = _f64(got)
+    assert (g[~on] == 0).all()
+    tol = (2 * 2.0 ** -24 + UNIT[got.dtype]) * (1 + 2.0 ** -10) * np.abs(want) + TINY[got.dtype]
+    assert (np.abs(g - want) <= tol).all()
+
+
+def _matrix(rows, cols, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn((rows, cols), generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 3), (5, 4), (3, 5), (7, 8), (2, 9), (100, 64), (33, 250), (1, 5000),
+                                       (5000, 1), (4099, 30)])
+def test_dropout(rows, cols, dtype):
+    x = _matrix(rows, cols, dtype)
+    for p, seed, offset in ((0.1, 1, 0), (0.5, 2 ** 64 - 1, 2 ** 64 - 1), (0.97, 2 ** 40, 2 ** 33 + 1)):
+        d = Dropout(p, seed, offset)
+        y = d(x)
+        _assert_dropped(y, x, p, seed, offset)
+        assert torch.equal(d.backward(x), y)
+
+
+def test_dropout_of_none_and_all():
+    x = _matrix(40, 21, torch.float32)
+    assert torch.equal(Dropout(0.0, 3)(x), x)
+    assert (Dropout(1.0, 3)(x) == 0).all()
+    assert torch.equal(Dropout(2.0 ** -34, 3)(x), x)  # rounds to a border of 0: nothing is below it
+    x[0] = float("nan")
+    y = host(Dropout(0.5, 3)(x))
+    assert np.array_equal(np.isnan(y[0]), O.kept(40, 21, 0.5, 3)[0])
+    assert Dropout(0.5, 3)(x[:0]).shape == (0, 21) and Dropout(0.5, 3)(x[:, :0]).shape == (40, 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_dropout_layouts(dtype):
+    """The mask goes by a value's row and column, whatever the strides and alignment."""
+    wide = _matrix(60, 200, dtype)
+    d = Dropout(0.3, 5, 6)
+    for x in (wide[:, 1:90], wide[::3, 64:192], wide[7:8, 3:], wide[9:10, 5:77].expand(50, 72)):
+        y = d(x)
+        _assert_dropped(y, x, 0.3, 5, 6)
+        out = torch.full((x.shape[0], 256), 4.0, device="cuda", dtype=dtype)
+        d(x, out=out[:, 3:3 + x.shape[1]])
+        assert torch.equal(out[:, 3:3 + x.shape[1]], y)
+        assert (out[:, :3] == 4).all() and (out[:, 3 + x.shape[1]:] == 4).all()
+    y, part = d(wide[:, 1:90]), wide[:, 1:90]
+    before = wide.clone()
+    assert d(part, out=part) is part and torch.equal(part, y)
+    before[:, 1:90] = y
+    assert torch.equal(wide, before)
+
+
+def test_dropout_gradient():
+    """The gradient against differences: the map is linear in x, value by value."""
+    x, h, dy = (_matrix(30, 50, torch.float32, s) for s in range(3))
+    d = Dropout(0.4, 8)
+    moved = d(x + h).double() - d(x).double()
+    got, want = (d.backward(dy).double() * h.double()).sum(), (dy.double() * moved).sum()
+    size = (dy.abs() * (2 * x.abs() + 2 * h.abs())).double().sum() / 0.6
+    assert abs((got - want).item()) <= 6 * 2.0 ** -24 * size.item()
+
+
+def test_step_is_read_when_the_work_runs():
+    x = _matrix(64, 96, torch.float16)
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    d = Dropout(0.5, 21, 40, step)
+    y = torch.empty_like(x)
+    d(x, out=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d(x, out=y)
+        step.add_(1)
+    for k in range(4):
+        g.replay()
+        other = Dropout(0.5, 21, 40 + k)(x)  # eager, between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(y, other)
+    assert int(step) == 4
+    step.fill_(-1)
+    assert torch.equal(d(x), Dropout(0.5, 21, 39)(x))
+
+
+def test_large_matrix_share():
+    """300,000 x 256 values: the share kept is within six standard deviations of 1 - p."""
+    x = torch.ones((300_000, 256), device="cuda", dtype=torch.float16)
+    for p in (0.1, 0.5):
+        kept = (Dropout(p, 1)(x) != 0).double()
+        assert abs(kept.mean().item() - (1 - p)) < 6 * (p * (1 - p) / x.numel()) ** 0.5
+        rows = kept.mean(1)
+        assert (rows - (1 - p)).abs().max().item() < 8 * (p * (1 - p) / 256) ** 0.5

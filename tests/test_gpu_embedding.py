@@ -1,0 +1,234 @@
+"""Table lookups, their gradient and dropout through the C ABI against the fp64
+oracle.
+
+A looked-up value is one fp32 product by an fp32 factor: 2^-24 each, then half a
+step of its type.  A gradient adds an entry's rows in fp32, at most 64 in a row
+before they are joined in double, and multiplies by the factor: (64 + 3) 2^-24 of
+the sum of magnitudes.  Which values drop is fixed by the generator: exact."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import codes as O
+from oracle import mx4 as O4
+from implicit_attribute_decode_amd.pipeline import Dropout, Mx4Tensor, embedding, embedding_backward, mx4_quantize
+
+from gpu_util import cuda, host
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+TYPES = list(UNIT)
+ids = lambda v: str(v).replace("torch.", "") if isinstance(v, torch.dtype) else None  # noqa: E731
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _table(rng, rows, cols, dtype=torch.float32):
+    return torch.as_tensor(rng.normal(size=(rows, cols)).astype(np.float32), device="cuda").to(dtype)
+
+
+def _assert_rows(got, want):
+    g = _f64(got)
+    assert np.array_equal(np.isnan(g), np.isnan(want))
+    assert np.array_equal(g == 0, want == 0) or TINY[got.dtype] > 2.0 ** -100
+    tol = (2 * 2.0 ** -24 + UNIT[got.dtype]) * (1 + 2.0 ** -10) * np.abs(want) + TINY[got.dtype]
+    ok = ~np.isnan(want)
+    assert (np.abs(g - want)[ok] <= tol[ok]).all()
+
+
+def _assert_gradient(got, want):
+    g, size, _ = want
+    assert got.dtype == torch.float32
+    assert (np.abs(_f64(got) - g) <= 67 * 2.0 ** -24 * size + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("out", TYPES, ids=ids)
+@pytest.mark.parametrize("dim", [1, 7, 8, 33, 64, 513])
+def test_lookup(dtype, out, dim):
+    rng = np.random.default_rng(dim)
+    table = _table(rng, 50, dim, dtype)
+    index = rng.integers(-3, 54, 77)
+    for ix in (cuda(index), cuda(index.astype(np.int32)), cuda(np.repeat(index, 3))[::3]):
+        _assert_rows(embedding(table, ix, 1.7, out), O.lookup(_f64(table), index, 1.7))
+    d = Dropout(0.3, 2 ** 63 + 12345, 2 ** 40 + 7)
+    _assert_rows(embedding(table, cuda(index), 0.5, out, d), O.lookup(_f64(table), index, 0.5, 0.3, d.seed, d.offset))
+
+
+@pytest.mark.parametrize("dim", [1, 30, 32, 64, 100])
+def test_lookup_in_a_4_bit_table(dim):
+    rng = np.random.default_rng(dim)
+    x = _table(rng, 40, dim)
+    x[7, dim - 1] = float("inf")  # its block reads back as NaN
+    q = mx4_quantize(x)
+    index = rng.integers(-2, 43, 200)
+    for out in TYPES:
+        _assert_rows(embedding(q, cuda(index), 3.0, out), O.lookup(O4.values(_f64(x)), index, 3.0))
+    assert embedding(q, cuda(index)).dtype == torch.float32
+    d = Dropout(0.5, 9, 1)
+    _assert_rows(embedding(q, cuda(index), dropout=d), O.lookup(O4.values(_f64(x)), index, 1.0, 0.5, 9, 1))
+
+
+def test_lookup_indices_out_of_range_and_layouts():
+    rng = np.random.default_rng(1)
+    wide = _table(rng, 20, 90)
+    index = torch.tensor([0, 19, 20, -1, 2 ** 40, -2 ** 62, 2 ** 32, 3], device="cuda")
+    want = O.lookup(_f64(wide[:, 5:47]), index.cpu().numpy())
+    out = torch.full((8, 60), 7.0, device="cuda")
+    got = embedding(wide[:, 5:47], index, out=out[:, 9:51])
+    _assert_rows(got, want)
+    assert (out[:, :9] == 7).all() and (out[:, 51:] == 7).all()
+    one = torch.tensor([3], device="cuda").expand(6)
+    _assert_rows(embedding(wide, one), O.lookup(_f64(wide), [3] * 6))
+    same = wide[4:5].expand(20, 90)
+    _assert_rows(embedding(same, index), O.lookup(_f64(same), index.cpu().numpy()))
+    assert embedding(wide, index[:0]).shape == (0, 90)
+    assert embedding(wide[:, :0], index).shape == (8, 0)
+    assert (embedding(wide[:0], index) == 0).all()
+
+
+def test_dropped_values_are_zero_whatever_they_were():
+    table = torch.full((3, 400), float("nan"), device="cuda")
+    got = host(embedding(table, torch.tensor([1, 2], device="cuda"), dropout=Dropout(0.5, 4, 4)))
+    on = O.kept(2, 400, 0.5, 4, 4)
+    assert np.array_equal(np.isnan(got), on) and (got[~on] == 0).all()
+    assert (embedding(table, torch.tensor([1, 2], device="cuda"), dropout=Dropout(1.0, 4, 4)) == 0).all()
+
+
+# ------------------------------------------------------------------ gradient
+
+
+def _indices(kind, rng, n, entries):
+    if kind == "one":
+        return np.full(n, entries - 1)
+    if kind == "frames":
+        return np.sort(rng.integers(0, entries, n))
+    if kind == "back":
+        return np.arange(n)[::-1] % entries
+    if kind == "few":  # a few entries with many rows among single ones
+        return np.where(rng.random(n) < 0.7, rng.integers(0, min(3, entries), n), rng.integers(0, entries, n))
+    if kind == "none":
+        return np.full(n, -1)
+    return rng.integers(-1, entries + 1, n)
+
+
+@pytest.mark.parametrize("kind", ["random", "one", "frames", "back", "few", "none"])
+@pytest.mark.parametrize("n,entries,dim", [(1, 1, 1), (31, 2, 8), (32, 5, 3), (33, 1, 64), (64, 70, 9), (65, 64, 1),
+                                           (97, 3, 130), (1000, 150, 64), (4097, 1024, 5), (9000, 70000, 12),
+                                           (700, 40, 520)])
+def test_gradient(kind, n, entries, dim):
+    rng = np.random.default_rng(n + dim)
+    index = _indices(kind, rng, n, entries)
+    dy = _table(rng, n, dim)
+    got = embedding_backward(dy, cuda(index), entries, 1.5)
+    _assert_gradient(got, O.lookup_gradient(_f64(dy), index, entries, 1.5))
+    assert torch.equal(got, embedding_backward(dy, cuda(index.astype(np.int32)), entries, 1.5))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_gradient_types_dropout_and_layouts(dtype):
+    rng = np.random.default_rng(3)
+    n, entries, dim = 500, 60, 41
+    wide = _table(rng, n, 100, dtype)
+    dy = wide[:, 3:44]
+    index = rng.integers(-1, entries + 2, n)
+    d = Dropout(0.4, 77, 5)
+    for ix in (cuda(index), cuda(np.repeat(index, 2))[::2]):
+        got = embedding_backward(dy, ix, entries, 0.25, d)
+        _assert_gradient(got, O.lookup_gradient(_f64(dy), index, entries, 0.25, 0.4, 77, 5))
+    row = wide[2:3, 3:44].expand(n, dim)  # a broadcast gradient
+    _assert_gradient(embedding_backward(row, cuda(index), entries), O.lookup_gradient(_f64(row), index, entries))
+    same = cuda(np.array([5])).expand(n)
+    _assert_gradient(embedding_backward(dy, same, entries), O.lookup_gradient(_f64(dy), [5] * n, entries))
+    out = torch.full((entries, dim), 3.0, device="cuda")
+    assert embedding_backward(dy, cuda(index), entries, out=out) is out
+    _assert_gradient(out, O.lookup_gradient(_f64(dy), index, entries))
+
+
+def test_gradient_of_nothing():
+    index, dy = torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros((0, 6), device="cuda")
+    assert (embedding_backward(dy, index, 9, out=torch.full((9, 6), 2.0, device="cuda")) == 0).all()
+    one = torch.zeros(4, dtype=torch.int64, device="cuda")
+    assert embedding_backward(torch.ones((4, 6), device="cuda"), one, 0).shape == (0, 6)
+    assert embedding_backward(torch.ones((4, 0), device="cuda"), one, 5).shape == (5, 0)
+
+
+def test_gradient_is_that_of_the_lookup():
+    """The lookup is linear: <dy, E(T + H) - E(T)> = <G, H>, both sums of n dim fp32 products near 1."""
+    rng = np.random.default_rng(8)
+    table, step = _table(rng, 30, 20), _table(rng, 30, 20)
+    index = cuda(rng.integers(-1, 30, 300))
+    dy = _table(rng, 300, 20)
+    d = Dropout(0.2, 5)
+    moved = (embedding(table + step, index, 2.0, dropout=d).double() - embedding(table, index, 2.0, dropout=d).double())
+    g = embedding_backward(dy, index, 30, 2.0, d).double()
+    size = (dy.abs().double() * embedding((table.abs() + step.abs()) * 2, index, 2.0, dropout=d).double()).sum().item()
+    assert abs((dy.double() * moved).sum().item() - (g * step.double()).sum().item()) <= 80 * 2.0 ** -24 * size
+
+
+def test_gradient_nan_and_infinity_stay_with_their_entry():
+    dy = torch.ones((200, 16), device="cuda")
+    index = torch.arange(200, device="cuda") % 10
+    dy[3, 2], dy[14, 5] = float("nan"), float("inf")
+    g = host(embedding_backward(dy, index, 11))
+    assert np.isnan(g[3, 2]) and np.isinf(g[4, 5]) and np.isfinite(g).sum() == g.size - 2
+    assert (np.delete(g, [3, 4], 0)[:8] == 20).all() and (g[10] == 0).all()
+
+
+def test_gradient_of_many_rows_is_the_same_every_time():
+    """300,000 rows of 150 entries, and of one."""
+    rng = np.random.default_rng(2)
+    dy = _table(rng, 300_000, 8)
+    for index in (np.sort(rng.integers(0, 150, 300_000)), rng.integers(0, 150, 300_000), np.zeros(300_000, np.int64)):
+        ix = cuda(index)
+        first = embedding_backward(dy, ix, 150)
+        _assert_gradient(first, O.lookup_gradient(_f64(dy), index, 150))
+        assert all(torch.equal(first, embedding_backward(dy, ix, 150)) for _ in range(3))
+
+
+def test_calls_on_two_streams():
+    rng = np.random.default_rng(6)
+    dy = [_table(rng, 20_000, 64) for _ in range(2)]
+    index = [cuda(rng.integers(0, 900, 20_000)) for _ in range(2)]
+    want = [embedding_backward(d, i, 900) for d, i in zip(dy, index)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, d, i in zip(streams, dy, index):
+            with torch.cuda.stream(s):
+                got.append(embedding_backward(d, i, 900))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_graph_replays_with_new_inputs_and_masks():
+    rng = np.random.default_rng(7)
+    table = _table(rng, 300, 48)
+    index = cuda(rng.integers(-1, 300, 3000))
+    dy = _table(rng, 3000, 48)
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    d = Dropout(0.25, 11, 100, step)
+
+    def both():
+        return embedding(table, index, 2.0, dropout=d), embedding_backward(dy, index, 300, 2.0, d)
+
+    both()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, grad = both()
+    for k in range(4):
+        index.copy_(cuda(rng.integers(-1, 300, 3000)))
+        dy.normal_()
+        step.fill_(k)
+        g.replay()
+        want = both()  # eager, between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(grad, want[1])
+        on = O.kept(3000, 48, 0.25, 11, 100 + k)
+        assert not host(out)[~on].any()
