@@ -31,7 +31,7 @@ ARCH = "gfx950"
 # backward's VALU instructions).
 EXTRA_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
                for name in ("decode.hip", "decode_branch.hip", "decode_bwd.hip", "mx4.hip",
-                            "mx4_matmul.hip", "q4.hip")}
+                            "mx4_matmul.hip", "q4.hip", "q4_matmul.hip")}
 
 
 def sources() -> list[str]:

@@ -1572,11 +1572,14 @@ ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_t ldx, 
     return IA_OK;
 }
 
-ia_status ia_q4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes) {
+ia_status ia_q4_linear_workspace_size(int32_t dtype, int64_t M, int64_t K, int64_t N, size_t* bytes) {
     if (!bytes) return fail(IA_ERR_INVALID_ARG, "bytes is null");
+    if (dtype_size(dtype) == 0) return fail(IA_ERR_UNSUPPORTED, "dtype must be F32, F16 or BF16");
     ia_status st = check_product(M, N, K, IA_ACT_NONE, nullptr);
+    if (st == IA_OK && !((K == 0 || (size_ok(M, K) && size_ok(N, K))) && (N == 0 || size_ok(M, N))))
+        st = fail(IA_ERR_INVALID_ARG, "at most 2^40 values");
     if (st != IA_OK) return st;
-    *bytes = ia::q4_linear_workspace(M, K, N);
+    *bytes = ia::q4_linear_workspace(dtype, M, K, N);
     return IA_OK;
 }
 
@@ -1588,7 +1591,7 @@ ia_status ia_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, con
     if (st == IA_OK) st = check_matrix(x, dtype, M, w->cols, ldx, true, "x");
     if (st == IA_OK) st = check_matrix(y, dtype, M, w->rows, ldy, false, "y");
     if (st != IA_OK) return st;
-    const size_t need = ia::q4_linear_workspace(M, w->cols, w->rows);
+    const size_t need = ia::q4_linear_workspace(dtype, M, w->cols, w->rows);
     st = check_ws(ws, ws_bytes, need);
     if (st != IA_OK) return st;
     const ia::Rows r[] = {input_rows(x, dtype, M, w->cols, ldx),

@@ -400,7 +400,7 @@ struct Q4View {
 
 hipError_t launch_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const Q4View& out, hipStream_t s);
 hipError_t launch_q4_dequantize(const Q4View& q, int32_t dtype, void* x, int64_t ldx, hipStream_t s);
-size_t q4_linear_workspace(int64_t M, int64_t K, int64_t N);
+size_t q4_linear_workspace(int32_t dtype, int64_t M, int64_t K, int64_t N);
 hipError_t launch_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const Q4View& w, const float* bias,
                             int32_t act, void* y, int64_t ldy, void* ws, hipStream_t s);
 

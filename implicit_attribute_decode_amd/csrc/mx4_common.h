@@ -39,6 +39,31 @@ __device__ __forceinline__ float activate(float v, int act) {
     return act == IA_ACT_RELU && v < 0.0f ? 0.0f : v;  // a NaN stays
 }
 
+// Tile index of a block so that blocks of one XCD (every eighth block) take
+// neighbouring tiles: runs of 8 tile rows, column by column.
+__device__ __forceinline__ void tile_of(int64_t b, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
+    const int64_t total = tm * tn, per = total / 8, rest = total % 8, x = b % 8;
+    int64_t t = x * per + min(x, rest) + b / 8;
+    const int64_t group = 8 * tn, g = t / group, h = min((int64_t)8, tm - 8 * g);
+    t -= g * group;
+    im = 8 * g + t % h;
+    in = t / h;
+}
+
+// LDS written by the lanes of one wave is read back by other lanes of the same
+// wave: order the accesses at wavefront scope.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Every copy of this wave has landed, and every wave's after the barrier.
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+}
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
 inline int64_t mx4_blocks(int64_t cols) { return ceil_div(cols, kBlock); }

@@ -183,17 +183,6 @@ __device__ __forceinline__ void store_rows(const floatx4* sums, const MatArgs& p
     }
 }
 
-// Tile index of a block so that blocks of one XCD (every eighth block) take
-// neighbouring tiles: runs of 8 tile rows, column by column.
-__device__ __forceinline__ void tile_of(int64_t b, int64_t tm, int64_t tn, int64_t& im, int64_t& in) {
-    const int64_t total = tm * tn, per = total / 8, rest = total % 8, x = b % 8;
-    int64_t t = x * per + min(x, rest) + b / 8;
-    const int64_t group = 8 * tn, g = t / group, h = min((int64_t)8, tm - 8 * g);
-    t -= g * group;
-    im = 8 * g + t % h;
-    in = t / h;
-}
-
 // Operands of one step of 64 values.
 template <int TI, int TJ>
 struct Step {
@@ -238,20 +227,6 @@ __device__ __forceinline__ void multiply(const Step<TI, TJ>& o, const Scales<TI,
 #pragma unroll
         for (int j = 0; j < TJ; ++j) asm volatile("" : "+v"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// LDS written by the lanes of one wave is read back by other lanes of the same
-// wave: order the accesses at wavefront scope.
-__device__ __forceinline__ void wave_lds_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// Every copy of this wave has landed, and every wave's after the barrier.
-__device__ __forceinline__ void stage_barrier() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
 }
 
 template <typename T, typename OFF, int R, int WAVES_M, int WAVES_N>

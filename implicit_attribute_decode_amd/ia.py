@@ -203,7 +203,7 @@ def load(path: str = LIB_PATH):
                                             C.c_int64, C.c_double, P, P, P, C.c_size_t, P]
         L.ia_q4_quantize.argtypes = [P, C.c_int32, C.c_int64, P, P]
         L.ia_q4_dequantize.argtypes = [P, C.c_int32, P, C.c_int64, P]
-        L.ia_q4_linear_workspace_size.argtypes = [C.c_int64, C.c_int64, C.c_int64, P]
+        L.ia_q4_linear_workspace_size.argtypes = [C.c_int32, C.c_int64, C.c_int64, C.c_int64, P]
         L.ia_q4_linear.argtypes = [P, C.c_int32, C.c_int64, C.c_int64, P, P, C.c_int32, P, C.c_int64, P, C.c_size_t, P]
         L.ia_profile_enable.argtypes = [C.c_int32]
         L.ia_profile_report.argtypes = [P, C.c_size_t, P]
@@ -615,9 +615,9 @@ def ia_q4_dequantize(q: Q4, dtype: int, x, ldx: int, stream=None):
     _check(load().ia_q4_dequantize(C.byref(q), dtype, _ptr(x), ldx, _stream(stream)))
 
 
-def ia_q4_linear_workspace_size(M: int, K: int, N: int) -> int:
+def ia_q4_linear_workspace_size(dtype: int, M: int, K: int, N: int) -> int:
     n = C.c_size_t()
-    _check(load().ia_q4_linear_workspace_size(M, K, N, C.byref(n)))
+    _check(load().ia_q4_linear_workspace_size(dtype, M, K, N, C.byref(n)))
     return n.value
 
 

@@ -1102,6 +1102,6 @@ def q4_linear(x: torch.Tensor, w: Q4Tensor, bias: torch.Tensor | None = None, ac
             raise ValueError("out has another shape or type")
     _here(x)
     _one_device(x, w._codes, bias, out)
-    ws = _bytes(ia.ia_q4_linear_workspace_size(M, K, w.rows), x.device)
+    ws = _bytes(ia.ia_q4_linear_workspace_size(d, M, K, w.rows), x.device)
     ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
     return out

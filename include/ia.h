@@ -865,7 +865,7 @@ IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_
  * may be NULL when that is 0) anything.  M, N, K < 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, act, group), WORKSPACE_TOO_SMALL,
  * DEVICE. */
-IA_API ia_status ia_q4_linear_workspace_size(int64_t M, int64_t K, int64_t N, size_t* bytes);
+IA_API ia_status ia_q4_linear_workspace_size(int32_t dtype, int64_t M, int64_t K, int64_t N, size_t* bytes);
 IA_API ia_status ia_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const ia_q4* w, const float* bias,
                               int32_t act, void* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 

@@ -98,11 +98,15 @@ def test_workspace_sizes():
             size(*args)
         assert e.value.status == BAD
     linear = ia.ia_q4_linear_workspace_size
-    assert linear(0, 0, 0) >= 0 and linear(300_000, 256, 256) >= 0
-    for args in ((-1, 1, 1), (1, -1, 1), (1, 1, -1), (1 << 31, 1, 1), (1, 1 << 31, 1), (1, 1, 1 << 31)):
+    assert linear(0, 0, 0, 0) == 0 and all(linear(d, 300_000, 256, 256) >= linear(d, 1, 256, 256) for d in (0, 1, 2))
+    for args in ((0, -1, 1, 1), (0, 1, -1, 1), (1, 1, 1, -1), (2, 1 << 31, 1, 1), (0, 1, 1 << 31, 1), (0, 1, 1, 1 << 31),
+                 (0, 1 << 30, 1 << 30, 1)):
         with pytest.raises(ia.IAError) as e:
             linear(*args)
         assert e.value.status == BAD
+    with pytest.raises(ia.IAError) as e:
+        linear(3, 1, 1, 1)
+    assert e.value.status == UNSUPPORTED
 
 
 def _q(**kw):

@@ -116,7 +116,7 @@ def test_quantize_layouts():
 @pytest.mark.parametrize("group", GROUPS)
 @pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 64, 16), (1, 250, 58), (2, 4096, 33), (5, 128, 300), (16, 1000, 17),
                                    (17, 96, 100), (31, 2049, 7), (33, 250, 58), (64, 129, 64), (65, 160, 65),
-                                   (130, 512, 257), (300, 96, 40)])
+                                   (130, 512, 257), (300, 96, 40), (515, 640, 530)])
 def test_linear(M, K, N, group, dtype):
     rng = np.random.default_rng(M + K + N)
     x, w = _matrix(rng, M, K, dtype), q4_quantize(_matrix(rng, N, K, scale=K ** -0.5), group)
@@ -190,6 +190,27 @@ def test_large_and_small_fp32_values():
     got = _f64(q4_linear(x, w))
     want = _f64(x) @ v.T
     assert (np.abs(got - want) <= 2.0 ** -22 * (np.abs(_f64(x)) @ np.abs(v).T)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M", [3, 90])
+def test_scales_of_any_size_and_sign(M, dtype):
+    """Neighbouring groups whose scales differ by up to 2^60, groups of zeros (scale 0), negative scales: every sum within
+    its own terms' error."""
+    rng = np.random.default_rng(M)
+    N, groups = 40, 9
+    scales = rng.normal(size=(N, groups)) * 2.0 ** rng.integers(-30, 1, (N, groups))
+    scales[:, 0] *= 2.0 ** -30
+    scales[3:9, 4] = 0.0
+    scales[11, 5] = 2.0 ** -110
+    scales[5] *= 2.0 ** -20
+    codes = torch.as_tensor(rng.integers(0, 256, (N, groups * 32)).astype(np.uint8), device="cuda")
+    w = Q4Tensor.from_parts(codes, cuda(scales.astype(np.float32)), cuda(rng.integers(0, 16, (N, groups))), groups * 64 - 5, 64)
+    v = _values(w)
+    x = _matrix(rng, M, groups * 64 - 5, dtype)
+    _assert_linear(q4_linear(x, w), _f64(x), v)
+    x[:, :64 * 5] = 0  # small terms alone
+    _assert_linear(q4_linear(x, w), _f64(x), v)
 
 
 def test_empty_products():
