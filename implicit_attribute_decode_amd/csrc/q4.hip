@@ -279,18 +279,19 @@ hipError_t launch_q4_dequantize(const Q4View& q, int32_t dtype, void* x, int64_t
     return IA_BY_DTYPE(dtype, launch_dequantize, q, x, ldx, s);
 }
 
-// Up to 64 rows in one reading of the weights, more in tiles.
-constexpr int64_t kFewRows = 64;
+// Up to 64 rows in one reading of the weights, more in tiles (whose offsets have
+// 32 bits).
+bool is_few(int64_t M, int64_t K) { return M <= 64 || K == 0 || K >= (int64_t)1 << 22; }
 
 size_t q4_linear_workspace(int32_t dtype, int64_t M, int64_t K, int64_t N) {
-    return M <= kFewRows || K == 0 || N == 0 ? 0 : q4_matmul_workspace(dtype, M, K, N);
+    return is_few(M, K) || N == 0 ? 0 : q4_matmul_workspace(dtype, M, K, N);
 }
 
 hipError_t launch_q4_linear(const void* x, int32_t dtype, int64_t M, int64_t ldx, const Q4View& w, const float* bias,
                             int32_t act, void* y, int64_t ldy, void* ws, hipStream_t s) {
     if (M == 0 || w.rows == 0) return hipSuccess;
     const Q4Linear p{w.codes, w.words, w.rows, w.cols, q4_groups(w.cols, w.group), bias, act, y, ldy};
-    if (M > kFewRows && w.cols > 0) return launch_q4_matmul(x, dtype, M, ldx, w.group, p, ws, s);
+    if (!is_few(M, w.cols)) return launch_q4_matmul(x, dtype, M, ldx, w.group, p, ws, s);
     return IA_BY_DTYPE(dtype, launch_linear, x, M, ldx, w.group, p, s);
 }
 

@@ -17,13 +17,32 @@ namespace ia {
 
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bfloatx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bfloatx8 __attribute__((ext_vector_type(8)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
 
 __host__ __device__ inline int64_t q4_groups(int64_t cols, int group) { return (cols + group - 1) / group; }
 __host__ __device__ inline int64_t q4_word_stride(int64_t groups) { return (groups + 3) & ~(int64_t)3; }
 
 __device__ __forceinline__ float scale_of(uint32_t word) { return __builtin_bit_cast(float, word & ~255u); }
 __device__ __forceinline__ float zero_of(uint32_t word) { return (float)(word & 255u); }
+
+// Eight codes as bytes.
+struct Nibbles {
+    uint32_t even, odd;
+
+    __device__ __forceinline__ explicit Nibbles(uint32_t codes) {
+        even = codes & 0x0f0f0f0fu;
+        odd = (codes >> 4) & 0x0f0f0f0fu;
+        // a byte is converted by one instruction as long as the compiler does not know that half of it is zero
+        asm("" : "+v"(even), "+v"(odd));
+    }
+    // code 2 j + ODD
+    template <int ODD>
+    __device__ __forceinline__ float value(int j) const {
+        return (float)(((ODD ? odd : even) >> (8 * j)) & 255u);
+    }
+};
 
 // q - z of eight codes (exact: whole numbers of at most 15).
 __device__ __forceinline__ halfx8 codes_less(uint32_t u, float z, halfx8) {
@@ -45,12 +64,13 @@ __device__ __forceinline__ halfx8 codes_less(uint32_t u, float z, halfx8) {
     return r;
 }
 __device__ __forceinline__ bfloatx8 codes_less(uint32_t u, float z, bfloatx8) {
-    const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;
+    const Nibbles n(u);
     bfloatx8 r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        r[2 * j] = (__bf16)((float)((even >> (8 * j)) & 255u) - z);
-        r[2 * j + 1] = (__bf16)((float)((odd >> (8 * j)) & 255u) - z);
+        const bfloatx2 w = __builtin_convertvector((floatx2{n.value<0>(j) - z, n.value<1>(j) - z}), bfloatx2);
+        r[2 * j] = w[0];
+        r[2 * j + 1] = w[1];
     }
     return r;
 }

@@ -44,34 +44,61 @@ template <typename V>
 __device__ __forceinline__ float unit_of(uint32_t word);
 template <>
 __device__ __forceinline__ float unit_of<_Float16>(uint32_t word) {
-    const float s = scale_of(word);
-    return fabsf(s) < 0x1p-80f ? 0x1p-80f : s;
+    return fabsf(scale_of(word)) < 0x1p-80f ? 0x1p-80f : scale_of(word);
 }
 template <>
 __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
     const uint32_t e = word & 0x7f800000u;
-    if (e == 0x7f800000u || (word & 0x7fffff00u) == 0) return 1.0f;
-    return e ? __builtin_bit_cast(float, (word & 0x807fff00u) | 0x3f800000u) : scale_of(word) * 0x1p126f;
+    const bool other = e == 0x7f800000u || (word & 0x7fffff00u) == 0;  // not finite, or zero
+    const float m = __builtin_bit_cast(float, (word & 0x807fff00u) | 0x3f800000u), small = scale_of(word) * 0x1p126f;
+    return other ? 1.0f : e ? m : small;
 }
 
-// u (q - z) of eight codes.
-__device__ __forceinline__ halfx8 operand(uint32_t codes, uint32_t word, halfx8) {
-    if (fabsf(scale_of(word)) < 0x1p-80f) codes = 0, word = 0;
-    return codes_less(codes, zero_of(word), halfx8());
-}
-__device__ __forceinline__ bfloatx8 operand(uint32_t codes, uint32_t word, bfloatx8) {
-    const uint32_t e = word & 0x7f800000u;
-    // a scale that is not finite goes into the operand as it is
-    const float u = e == 0x7f800000u ? scale_of(word) : __builtin_bit_cast(float, e ? e : (word & 0x7fff00u) ? 0x00800000u : 0u);
-    const float zu = zero_of(word) * u;
-    const uint32_t even = codes & 0x0f0f0f0fu, odd = (codes >> 4) & 0x0f0f0f0fu;
-    bfloatx8 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        r[2 * j] = (__bf16)__builtin_fmaf((float)((even >> (8 * j)) & 255u), u, -zu);
-        r[2 * j + 1] = (__bf16)__builtin_fmaf((float)((odd >> (8 * j)) & 255u), u, -zu);
+// What a group's word does to its codes; operands are u (q - z).
+template <typename V>
+struct Group;
+template <>
+struct Group<_Float16> {
+    uint32_t keep;
+    float z;
+    __device__ __forceinline__ explicit Group(uint32_t word) {
+        const bool none = fabsf(scale_of(word)) < 0x1p-80f;
+        keep = none ? 0u : ~0u;
+        z = none ? 0.0f : zero_of(word);
     }
-    return r;
+    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes & keep, z, halfx8()); }
+};
+template <>
+struct Group<__bf16> {
+    float u, zu;
+    __device__ __forceinline__ explicit Group(uint32_t word) {
+        const uint32_t e = word & 0x7f800000u, low = (word & 0x7fff00u) ? 0x00800000u : 0u;
+        // a scale that is not finite goes into the operand as it is
+        u = __builtin_bit_cast(float, e == 0x7f800000u ? word & ~255u : e ? e : low);
+        zu = -zero_of(word) * u;
+    }
+    __device__ __forceinline__ bfloatx8 operand(uint32_t codes) const {
+        const Nibbles n(codes);
+        floatx2 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = floatx2{__builtin_fmaf(n.value<0>(j), u, zu), __builtin_fmaf(n.value<1>(j), u, zu)};
+        bfloatx8 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bfloatx2 w = __builtin_convertvector(v[j], bfloatx2);
+            r[2 * j] = w[0];
+            r[2 * j + 1] = w[1];
+        }
+        return r;
+    }
+};
+
+// A pointer that is the same for all lanes, in scalar registers.
+__device__ __forceinline__ const char* uniform(const char* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
 }
 
 struct ManyArgs {
@@ -119,136 +146,180 @@ __device__ __forceinline__ void store_tile(const float* sums, int pitch, const M
 template <typename V, typename T, int G, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
     typedef typename Elem<V>::vec vec;
-    constexpr int WAVES = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32, PER = 128 / G;
+    constexpr int WAVES = WM * WN, TI = BM / WM / 32, TJ = BN / WN / 32;
     constexpr int COPIES = BM / 8 / WAVES;
     static_assert(2 * BN == 64 * WAVES, "two threads for every row of codes");
     // apart, so that a read of one buffer need not wait for copies into the other
-    __shared__ uintx4 x0[BM * 8], x1[BM * 8], w0[BN * 8], w1[BN * 8];
+    __shared__ uintx4 x0[BM * 8], x1[BM * 8], x2[BM * 8], w0[BN * 8], w1[BN * 8];
     const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t im, in;
     tile_of(blockIdx.x, p.tiles_m, p.tiles_n, im, in);
     const int64_t m0 = im * BM, n0 = in * BN;
     const int wm = wave % WM * 32 * TI, wn = wave / WM * 32 * TJ;
-    const int64_t total = p.parts * p.pairs, q0 = blockIdx.y * p.per_split, q1 = min(q0 + p.per_split, total);
     const int64_t ldc = p.w.groups * (G / 2), ldw = q4_word_stride(p.w.groups);
 
+    // The pairs of stages of this split, one after the other through the parts of
+    // x.  Addresses are uniform, the threads' offsets to them have 32 bits.
+    struct At {
+        const char* x;  // the tile's first row there
+        int k;          // pair of the weights
+    };
+    const int pairs = (int)p.pairs, groups = (int)p.w.groups;
+    const int q0 = (int)(blockIdx.y * p.per_split), q1 = (int)min((int64_t)q0 + p.per_split, p.parts * p.pairs);
+    At at{(const char*)p.x + (q0 / pairs * p.plane + m0 * p.ldx + q0 % pairs * 128) * 2, q0 % pairs};
+    const auto advance = [&](At& t) {
+        t.x += 256;
+        if (++t.k == pairs) {
+            t.k = 0;
+            t.x += (p.plane - p.pairs * 128) * 2;
+        }
+    };
     // this thread's copies of x: rows 8 (WAVES i + wave) + lane / 8
-    const char* xrow[COPIES];
+    uint32_t xoff[COPIES];
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
         const int row = 8 * (WAVES * i + wave) + (lane >> 3);
-        xrow[i] = (const char*)p.x + (min(m0 + row, p.M - 1) * p.ldx + 8 * slot_of(row, lane & 7)) * 2;
+        xoff[i] = (uint32_t)((min((int64_t)row, p.M - 1 - m0) * p.ldx + 8 * slot_of(row, lane & 7)) * 2);
     }
-    const auto copy = [&](int64_t pair, int s) {
-        const int64_t part = pair / p.pairs, at = (part * p.plane + (pair - part * p.pairs) * 128 + s * kStage) * 2;
+    const auto copy = [&](const char* x, uintx4* to) {
+        x = uniform(x);
 #pragma unroll
         for (int i = 0; i < COPIES; ++i)
-            __builtin_amdgcn_global_load_lds((const void*)(xrow[i] + at),
-                                             (__attribute__((address_space(3))) void*)((s ? x1 : x0) + (WAVES * i + wave) * 64), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void*)(x + xoff[i]),
+                                             (__attribute__((address_space(3))) void*)(to + (WAVES * i + wave) * 64), 16, 0, 0);
     };
-    // and its half row of codes
+    // and its half row of codes: 16 bytes and their word each stage
     const int crow = threadIdx.x >> 1, half = threadIdx.x & 1;
-    const int64_t cn = min(n0 + crow, p.w.N - 1);
+    const uint8_t* const codes = p.w.codes + n0 * ldc;
+    const uint32_t* const words = p.w.words + n0 * ldw;
+    const uint32_t cn = (uint32_t)min((int64_t)crow, p.w.N - 1 - n0), coff = cn * (uint32_t)ldc + 16 * half, cw = cn * (uint32_t)ldw;
+    const int last_block = groups * (G / 32) - 1;  // of 32 inputs
     struct Codes {
-        uintx4 q[2];
-        uint32_t w[2];
+        uintx4 q;
+        uint32_t w;
     };
-    const auto load_codes = [&](int64_t pair) {
+    const auto load_codes = [&](int k, int s) {
+        const int here = min(4 * k + 2 * s + half, last_block);  // past the row's end: the last codes again
         Codes c;
-        const int64_t k = pair % p.pairs;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int64_t at = k * 64 + 32 * s + 16 * half, g = at / (G / 2);
-            c.q[s] = uintx4{0, 0, 0, 0};
-            c.w[s] = 0;
-            if (at < ldc) {
-                c.q[s] = *reinterpret_cast<const uintx4*>(p.w.codes + cn * ldc + at);
-                c.w[s] = p.w.words[cn * ldw + g];
-            }
-        }
+        c.q = *reinterpret_cast<const uintx4*>(codes + (coff + 16 * (here - half)));
+        c.w = words[cw + here / (G / 32)];
         return c;
     };
-    const auto convert = [&](const Codes& c, int s, int i, int buf) {
-        const vec v = operand(c.q[s][i], c.w[s], vec());
-        (buf ? w1 : w0)[crow * 8 + slot_of(crow, 4 * half + i)] = __builtin_bit_cast(uintx4, v);
-    };
-    // the words of this lane's columns
-    const auto load_words = [&](int64_t pair, uint32_t (&w)[TJ][PER]) {
-        const int64_t k = pair % p.pairs;
+    // and there their scale is zero
+    const auto group_of = [&](const Codes& c, int k, int s) { return Group<V>(4 * k + 2 * s + half <= last_block ? c.w : 0u); };
+    int wslot[4];
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const int64_t n = min(n0 + wn + 32 * j + r, p.w.N - 1);
-            __builtin_memcpy(w[j], p.w.words + n * ldw + k * PER, sizeof(w[j]));
+    for (int i = 0; i < 4; ++i) wslot[i] = crow * 8 + slot_of(crow, 4 * half + i);
+    // the words of this lane's columns, those of a stage
+    constexpr int PER = G < kStage ? kStage / G : 1;
+    uint32_t dw[TJ];
 #pragma unroll
-            for (int g = 0; g < PER; ++g)
-                if (k * PER + g >= p.w.groups) w[j][g] = 0;
-        }
+    for (int j = 0; j < TJ; ++j) dw[j] = (uint32_t)min((int64_t)(wn + 32 * j + r), p.w.N - 1 - n0) * (uint32_t)ldw;
+    const auto load_words = [&](int k, int s, uint32_t (&w)[TJ][PER]) {
+        const int g0 = (128 * k + kStage * s) / G;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int g = 0; g < PER; ++g) w[j][g] = words[dw[j] + min(g0 + g, groups - 1)];  // past the end: no matter, times zero
     };
 
     floatx16 acc[TI][TJ] = {};
     float unit[TJ];
-    if (q0 < q1) {
-        Codes cur = load_codes(q0), nxt;
-        uint32_t word[TJ][PER], word_next[TJ][PER];
-        load_words(q0, word);
-        copy(q0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) convert(cur, 0, i, 0);
+    for (int j = 0; j < TJ; ++j) unit[j] = 1.0f;
+    if (q0 < q1) {
+        uint32_t word[TJ][PER];
+        load_words(at.k, 0, word);
+        Codes code = load_codes(at.k, 0);
+        copy(at.x, x0);
+        copy(at.x + 128, x1);
+        {
+            const Group<V> g = group_of(code, at.k, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w0[wslot[i]] = __builtin_bit_cast(uintx4, g.operand(code.q[i]));
+        }
+        code = load_codes(at.k, 1);
 #pragma unroll
         for (int j = 0; j < TJ; ++j) unit[j] = unit_of<V>(word[j][0]);
         stage_barrier();
-        for (int64_t pair = q0; pair < q1; ++pair) {
-            const bool more = pair + 1 < q1;
-            if (more) {
-                nxt = load_codes(pair + 1);
-                load_words(pair + 1, word_next);
-            }
+        // Copies land in the order of their issue: the next stage has landed when
+        // no more are under way than the last COPIES.
+        const auto ready = [] { asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(COPIES) : "memory"); };
+        // Stage s of a pair out of xa and wb; meanwhile the next one's codes become
+        // operands in wc, those of the one after it are loaded and its x is
+        // copied from `from` to xc.
+        const auto stage = [&](auto half_pair, const At& then, const uintx4* xa, const uintx4* wb, uintx4* xc, uintx4* wc) {
+            constexpr int s = decltype(half_pair)::value;
+            Codes more = load_codes(then.k, s);
+            uint32_t word_next[TJ][PER];
+            if (s == 1 || G < 128) load_words(s ? then.k : at.k, s ^ 1, word_next);
+            __builtin_amdgcn_sched_barrier(0);  // the copies come last
+            copy(then.x + s * 128, xc);
+            __builtin_amdgcn_sched_barrier(0);
+            const Group<V> group = s ? group_of(code, then.k, 0) : group_of(code, at.k, 1);
+            // the next step's operands are read ahead where registers are left
+            constexpr int AHEAD = G > 32 || TI < 4;
+            vec a[1 + AHEAD][TI], b[1 + AHEAD][TJ];
+            const auto read = [&](int k) {
+                const int slot = slot_of(r, 2 * k + h);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s == 0)
-                    copy(pair, 1);
-                else if (more)
-                    copy(pair + 1, 0);
+                for (int i = 0; i < TI; ++i) a[k & AHEAD][i] = __builtin_bit_cast(vec, xa[(wm + 32 * i + r) * 8 + slot]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if ((kStage * s + 16 * k) % G == 0) {
+                for (int j = 0; j < TJ; ++j) b[k & AHEAD][j] = __builtin_bit_cast(vec, wb[(wn + 32 * j + r) * 8 + slot]);
+            };
+            if (AHEAD) read(0);
 #pragma unroll
-                        for (int j = 0; j < TJ; ++j) {
-                            const float u = unit_of<V>(word[j][(kStage * s + 16 * k) / G]), f = unit[j] / u;
-                            unit[j] = u;
+            for (int k = 0; k < 4; ++k) {
+                if (k + AHEAD < 4) read(k + AHEAD);
+                if ((kStage * s + 16 * k) % G == 0) {
 #pragma unroll
-                            for (int i = 0; i < TI; ++i)
+                    for (int j = 0; j < TJ; ++j) {
+                        const float u = unit_of<V>(word[j][16 * k / G]), f = unit[j] / u;
+                        unit[j] = u;
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) acc[i][j][e] *= f;
-                        }
+                        for (int i = 0; i < TI; ++i)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) acc[i][j][e] *= f;
                     }
-                    vec a[TI], b[TJ];
-                    const int slot = slot_of(r, 2 * k + h);
-#pragma unroll
-                    for (int i = 0; i < TI; ++i) a[i] = __builtin_bit_cast(vec, (s ? x1 : x0)[(wm + 32 * i + r) * 8 + slot]);
-#pragma unroll
-                    for (int j = 0; j < TJ; ++j) b[j] = __builtin_bit_cast(vec, (s ? w1 : w0)[(wn + 32 * j + r) * 8 + slot]);
-#pragma unroll
-                    for (int i = 0; i < TI; ++i)
-#pragma unroll
-                        for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(a[i], b[j], acc[i][j]);
-                    if (s == 0)
-                        convert(cur, 1, k, 1);
-                    else if (more)
-                        convert(nxt, 0, k, 0);
                 }
-                stage_barrier();
+#pragma unroll
+                for (int i = 0; i < TI; ++i)
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(a[k & AHEAD][i], b[k & AHEAD][j], acc[i][j]);
+                wc[wslot[k]] = __builtin_bit_cast(uintx4, group.operand(code.q[k]));
             }
-            cur = nxt;
+            // what was loaded is used from here on, not waited for above
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" : "+v"(more.q), "+v"(more.w));
+            code = more;
+            if (s == 1 || G < 128)
 #pragma unroll
-            for (int j = 0; j < TJ; ++j)
+                for (int j = 0; j < TJ; ++j)
 #pragma unroll
-                for (int g = 0; g < PER; ++g) word[j][g] = word_next[j][g];
+                    for (int g = 0; g < PER; ++g) {
+                        asm volatile("" : "+v"(word_next[j][g]));
+                        word[j][g] = word_next[j][g];
+                    }
+            ready();
+        };
+        const auto pair_of = [&](int pair, uintx4* xa, uintx4* xb, uintx4* xc) {
+            // the last pair makes itself ready again, for nothing
+            At then = at;
+            if (pair + 1 < q1) advance(then);
+            stage(std::integral_constant<int, 0>{}, then, xa, w0, xc, w1);
+            stage(std::integral_constant<int, 1>{}, then, xb, w1, xa, w0);
+            at = then;
+        };
+        for (int pair = q0;;) {
+            pair_of(pair, x0, x1, x2);
+            if (++pair >= q1) break;
+            pair_of(pair, x2, x0, x1);
+            if (++pair >= q1) break;
+            pair_of(pair, x1, x2, x0);
+            if (++pair >= q1) break;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) unit[j] = 1.0f;
+        stage_barrier();
     }
 
     // The sums leave through LDS, 32 rows of a wave at a time, as whole lines.
@@ -296,14 +367,20 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
 }
 
 struct Plan {
-    int tile;    // rows of a tile; outputs of a tile
+    bool large;  // tiles of 256 x 256, else of 128 x 128
     int splits;
     int64_t per_split;
 };
 
 Plan plan_of(int parts, int64_t M, int64_t K, int64_t N) {
     const int64_t pairs = ceil_div(K, 128) * parts;
-    Plan p{256, 1, pairs};
+    Plan p;
+    const int64_t small = ceil_div(M, 128) * ceil_div(N, 128), large = ceil_div(M, 256) * ceil_div(N, 256);
+    p.large = large >= 256;
+    const int64_t tiles = p.large ? large : small;
+    int64_t splits = 1;
+    p.per_split = ceil_div(pairs, splits);
+    p.splits = (int)ceil_div(pairs, p.per_split);
     return p;
 }
 
@@ -329,8 +406,8 @@ hipError_t matmul(const T* x, int64_t M, int64_t ldx, const Q4Linear& w, void* w
     p.pairs = Kp / 128;
     p.w = w;
     p.per_split = plan.per_split;
-    // x as it is where its rows are whole lines of 16-bit values
-    if (PARTS == 1 && w.K == Kp && (uintptr_t)x % 16 == 0 && ldx % 8 == 0) {
+    // x as it is where its rows are whole lines of 16-bit values and a tile's offsets fit 32 bits
+    if (PARTS == 1 && w.K == Kp && (uintptr_t)x % 16 == 0 && ldx % 8 == 0 && ldx < (int64_t)1 << 22) {
         p.x = x;
         p.ldx = ldx;
     } else {
@@ -341,7 +418,7 @@ hipError_t matmul(const T* x, int64_t M, int64_t ldx, const Q4Linear& w, void* w
         p.plane = M * Kp;
     }
     if (plan.splits > 1) p.sums = (float*)((char*)ws + pack_bytes(PARTS, M, w.K));
-    hipError_t e = run<V, T, G, 256, 256, 2, 4>(p, plan.splits, s);
+    hipError_t e = plan.large ? run<V, T, G, 256, 256, 2, 4>(p, plan.splits, s) : run<V, T, G, 128, 128, 2, 2>(p, plan.splits, s);
     if (e != hipSuccess || plan.splits == 1) return e;
     IA_LAUNCH("q4_join_kernel", q4_join_kernel<T>, dim3(grid_for(M * w.N)), dim3(256), 0, s, p.sums, plan.splits, M, w);
     return hipGetLastError();
