@@ -122,8 +122,9 @@ struct Q4Linear {
     int64_t ldy;
 };
 
-// Many rows (q4_matmul.hip); the workspace holds the parts of x that cannot be
-// read as they are and the sums of splits.
+// Many rows, in tiles (q4_matmul.hip), where that is faster; the workspace holds
+// rows of x that cannot be read as they are, and the sums of splits.
+bool q4_takes_tiles(int32_t dtype, int group, int64_t M, int64_t K, int64_t N);
 size_t q4_matmul_workspace(int32_t dtype, int64_t M, int64_t K, int64_t N);
 hipError_t launch_q4_matmul(const void* x, int32_t dtype, int64_t M, int64_t ldx, int group, const Q4Linear& p, void* ws,
                             hipStream_t s);

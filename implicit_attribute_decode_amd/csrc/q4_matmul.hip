@@ -16,6 +16,10 @@
 //   which add up to them exactly, one part after the other.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
 #include "q4_common.h"
 
 namespace ia {
@@ -258,20 +262,18 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
             copy(then.x + s * 128, xc);
             __builtin_amdgcn_sched_barrier(0);
             const Group<V> group = s ? group_of(code, then.k, 0) : group_of(code, at.k, 1);
-            // the next step's operands are read ahead where registers are left
-            constexpr int AHEAD = G > 32 || TI < 4;
-            vec a[1 + AHEAD][TI], b[1 + AHEAD][TJ];
+            vec a[2][TI], b[2][TJ];  // this step's operands and the next one's
             const auto read = [&](int k) {
                 const int slot = slot_of(r, 2 * k + h);
 #pragma unroll
-                for (int i = 0; i < TI; ++i) a[k & AHEAD][i] = __builtin_bit_cast(vec, xa[(wm + 32 * i + r) * 8 + slot]);
+                for (int i = 0; i < TI; ++i) a[k & 1][i] = __builtin_bit_cast(vec, xa[(wm + 32 * i + r) * 8 + slot]);
 #pragma unroll
-                for (int j = 0; j < TJ; ++j) b[k & AHEAD][j] = __builtin_bit_cast(vec, wb[(wn + 32 * j + r) * 8 + slot]);
+                for (int j = 0; j < TJ; ++j) b[k & 1][j] = __builtin_bit_cast(vec, wb[(wn + 32 * j + r) * 8 + slot]);
             };
-            if (AHEAD) read(0);
+            read(0);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (k + AHEAD < 4) read(k + AHEAD);
+                if (k < 3) read(k + 1);
                 if ((kStage * s + 16 * k) % G == 0) {
 #pragma unroll
                     for (int j = 0; j < TJ; ++j) {
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
 #pragma unroll
                 for (int i = 0; i < TI; ++i)
 #pragma unroll
-                    for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(a[k & AHEAD][i], b[k & AHEAD][j], acc[i][j]);
+                    for (int j = 0; j < TJ; ++j) acc[i][j] = mfma(a[k & 1][i], b[k & 1][j], acc[i][j]);
                 wc[wslot[k]] = __builtin_bit_cast(uintx4, group.operand(code.q[k]));
             }
             // what was loaded is used from here on, not waited for above
@@ -366,22 +368,45 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
     }
 }
 
+// Microseconds that a product takes, as measured on bf16 in groups of 128 over M of
+// 33 to 100,000, K of 32 to 8,192 and N of 58 to 11,008 (in brackets a case):
+//   few rows' kernel: 16 outputs of 64 rows a block, 256 blocks side by side take
+//     16.3 for 4,096 inputs, 1.75 at least (256 x 8,192 -> 1,024: 36)
+//   tiles of 128: 6.5 and 1.75 a pair of stages for up to 256 blocks, 0.8 of that
+//     for each 256 more, two to a CU (2,048 x 4,096 -> 4,096: 101)
+//   tiles of 256: 4 and 3.7 a pair for up to 128 blocks, 8 and 4.8 for 256 (4,096
+//     cubed: 163, in tiles of 128 226)
+//   joining splits: 3 and 8 bytes a sum at 4 TB/s (128 x 4,096 -> 4,096 in four
+//     splits: 28, in one 59).
+enum Way { kFew, kSmall, kLarge };
 struct Plan {
-    bool large;  // tiles of 256 x 256, else of 128 x 128
+    Way way;
     int splits;
     int64_t per_split;
 };
 
-Plan plan_of(int parts, int64_t M, int64_t K, int64_t N) {
+Plan plan_of(int parts, int group, int64_t M, int64_t K, int64_t N) {
     const int64_t pairs = ceil_div(K, 128) * parts;
-    Plan p;
-    const int64_t small = ceil_div(M, 128) * ceil_div(N, 128), large = ceil_div(M, 256) * ceil_div(N, 256);
-    p.large = large >= 256;
-    const int64_t tiles = p.large ? large : small;
-    int64_t splits = 1;
-    p.per_split = ceil_div(pairs, splits);
-    p.splits = (int)ceil_div(pairs, p.per_split);
-    return p;
+    const auto tiles = [&](int64_t m, int64_t n) { return (double)(ceil_div(M, m) * ceil_div(N, n)); };
+    Plan best{kFew, 1, pairs};
+    if (M <= 16 || K >= (int64_t)1 << 22) return best;  // a tile's offsets have 32 bits
+    double least = 2.5 + std::max(0.8, tiles(64, 16) / 256) * std::max(1.75, 16.3 * (double)K / 4096);
+    const auto offer = [&](Way way, int64_t splits, double blocks) {
+        const int64_t per = ceil_div(pairs, splits);
+        double t;
+        if (way == kSmall)
+            t = std::max(1.0, 0.8 * blocks / 256) * (6.5 + 1.75 * (double)per);
+        else
+            t = blocks <= 128 ? 4 + 3.7 * (double)per : std::ceil(blocks / 256) * (8 + 4.8 * (double)per);
+        if (splits > 1) t += 3 + (double)splits * (double)M * (double)N * 8 / 4e6;
+        if (t < least) least = t, best = Plan{way, (int)ceil_div(pairs, per), per};
+    };
+    for (int64_t s = 1; s <= 8 && s <= pairs; s *= 2) {
+        offer(kSmall, s, tiles(128, 128) * (double)s);
+        // with groups of 32 the wide tile's sums do not fit the registers
+        if (group > 32) offer(kLarge, s, tiles(256, 256) * (double)s);
+    }
+    return best;
 }
 
 size_t pack_bytes(int parts, int64_t M, int64_t K) { return round_up((size_t)parts * (size_t)M * (size_t)ceil_div(K, 128) * 256); }
@@ -397,8 +422,7 @@ hipError_t run(const ManyArgs& a, int splits, hipStream_t s) {
 }
 
 template <typename V, typename T, int PARTS, int G>
-hipError_t matmul(const T* x, int64_t M, int64_t ldx, const Q4Linear& w, void* ws, hipStream_t s) {
-    const Plan plan = plan_of(PARTS, M, w.K, w.N);
+hipError_t matmul(const Plan& plan, const T* x, int64_t M, int64_t ldx, const Q4Linear& w, void* ws, hipStream_t s) {
     const int64_t Kp = ceil_div(w.K, 128) * 128;
     ManyArgs p{};
     p.M = M;
@@ -418,7 +442,11 @@ hipError_t matmul(const T* x, int64_t M, int64_t ldx, const Q4Linear& w, void* w
         p.plane = M * Kp;
     }
     if (plan.splits > 1) p.sums = (float*)((char*)ws + pack_bytes(PARTS, M, w.K));
-    hipError_t e = plan.large ? run<V, T, G, 256, 256, 2, 4>(p, plan.splits, s) : run<V, T, G, 128, 128, 2, 2>(p, plan.splits, s);
+    hipError_t e;
+    if constexpr (G > 32)
+        e = plan.way == kLarge ? run<V, T, G, 256, 256, 2, 4>(p, plan.splits, s) : run<V, T, G, 128, 128, 2, 2>(p, plan.splits, s);
+    else
+        e = run<V, T, G, 128, 128, 2, 2>(p, plan.splits, s);
     if (e != hipSuccess || plan.splits == 1) return e;
     IA_LAUNCH("q4_join_kernel", q4_join_kernel<T>, dim3(grid_for(M * w.N)), dim3(256), 0, s, p.sums, plan.splits, M, w);
     return hipGetLastError();
@@ -429,17 +457,29 @@ hipError_t launch_matmul(const void* x, int64_t M, int64_t ldx, int group, const
     typedef std::conditional_t<std::is_same<T, _Float16>::value, _Float16, __bf16> V;
     constexpr int PARTS = std::is_same<T, float>::value ? 3 : 1;
     const T* const t = (const T*)x;
-    return group == 32   ? matmul<V, T, PARTS, 32>(t, M, ldx, w, ws, s)
-           : group == 64 ? matmul<V, T, PARTS, 64>(t, M, ldx, w, ws, s)
-                         : matmul<V, T, PARTS, 128>(t, M, ldx, w, ws, s);
+    const Plan plan = plan_of(PARTS, group, M, w.K, w.N);
+    return group == 32   ? matmul<V, T, PARTS, 32>(plan, t, M, ldx, w, ws, s)
+           : group == 64 ? matmul<V, T, PARTS, 64>(plan, t, M, ldx, w, ws, s)
+                         : matmul<V, T, PARTS, 128>(plan, t, M, ldx, w, ws, s);
 }
+
+int parts_of(int32_t dtype) { return dtype == IA_DTYPE_F32 ? 3 : 1; }
 
 }  // namespace
 
+bool q4_takes_tiles(int32_t dtype, int group, int64_t M, int64_t K, int64_t N) {
+    return K > 0 && plan_of(parts_of(dtype), group, M, K, N).way != kFew;
+}
+
 size_t q4_matmul_workspace(int32_t dtype, int64_t M, int64_t K, int64_t N) {
-    const int parts = dtype == IA_DTYPE_F32 ? 3 : 1;
-    const Plan p = plan_of(parts, M, K, N);
-    return pack_bytes(parts, M, K) + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0);
+    const int parts = parts_of(dtype);
+    size_t most = 0;  // of any group
+    for (int group : {32, 128}) {
+        const Plan p = plan_of(parts, group, M, K, N);
+        if (K > 0 && p.way != kFew)
+            most = std::max(most, pack_bytes(parts, M, K) + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0));
+    }
+    return most;
 }
 
 hipError_t launch_q4_matmul(const void* x, int32_t dtype, int64_t M, int64_t ldx, int group, const Q4Linear& p, void* ws,

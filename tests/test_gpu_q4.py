@@ -115,7 +115,7 @@ def test_quantize_layouts():
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("group", GROUPS)
 @pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 64, 16), (1, 250, 58), (2, 4096, 33), (5, 128, 300), (16, 1000, 17),
-                                   (17, 96, 100), (31, 2049, 7), (33, 250, 58), (64, 129, 64), (65, 160, 65),
+                                   (17, 96, 100), (31, 2049, 7), (33, 250, 58), (5, 600, 16400), (64, 129, 64), (65, 160, 65),
                                    (130, 512, 257), (300, 96, 40), (515, 640, 530)])
 def test_linear(M, K, N, group, dtype):
     rng = np.random.default_rng(M + K + N)
