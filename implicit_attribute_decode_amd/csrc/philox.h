@@ -55,6 +55,13 @@ struct Dropper {
         o0 = (uint32_t)o;
         o1 = (uint32_t)(o >> 32);
     }
+    // zero where dropped, for values c .. c + 3 of row r (c a multiple of 4)
+    template <typename V>
+    __device__ __forceinline__ void apply(V& v, uint32_t r, uint32_t c) const {
+        const Words4 x = philox(c >> 2, r, o0, o1, k0, k1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = x.w[j] >= limit ? v[j] : 0.0f;
+    }
     // v times factor where kept, else 0, for values c0 .. c0 + 7 of row r (c0 a multiple of 8)
     __device__ __forceinline__ void apply(float (&v)[8], uint32_t r, uint32_t c0, float factor) const {
 #pragma unroll
