@@ -1528,8 +1528,9 @@ ia_status check_q4(const ia_q4* q, const char* name) {
     if (!q) return fail(IA_ERR_INVALID_ARG, std::string(name) + " is null");
     if (q->group != 32 && q->group != 64 && q->group != 128)
         return fail(IA_ERR_UNSUPPORTED, std::string(name) + ": groups are of 32, 64 or 128 values");
-    if (q->rows < 0 || q->cols < 0 || (q->cols > 0 && !size_ok(q->rows, q->cols)))
-        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": sizes must be >= 0 with at most 2^40 values");
+    if (q->rows < 0 || q->cols < 0 || q->rows > kMaxMatmulDim || q->cols > kMaxMatmulDim ||
+        (q->cols > 0 && !size_ok(q->rows, q->cols)))
+        return fail(IA_ERR_INVALID_ARG, std::string(name) + ": sizes must be in [0, 2^31) with at most 2^40 values");
     if (q->rows > 0 && q->cols > 0 && (!q->codes || !q->words || !aligned(q->codes, 16) || !aligned(q->words, 16)))
         return fail(IA_ERR_INVALID_ARG, std::string(name) + ": codes or words null or not 16-byte aligned");
     return IA_OK;

@@ -3,6 +3,8 @@
 // gradient is the same call on the upstream gradient.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "mx4_common.h"
 #include "philox.h"
 
@@ -10,26 +12,38 @@ namespace ia {
 namespace {
 
 // A thread takes eight values of a row: two counters give their eight words.
+// Rows from row0 on, fewer than 2^31 threads.
 template <typename T>
-__global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, T* out, int64_t ldo, int64_t rows,
-                                                      uint32_t cols, float factor, DropArgs a) {
-    const uint32_t chunks = (cols + 7) / 8;
-    const int64_t total = rows * chunks;
+__global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, T* out, int64_t ldo, uint32_t row0,
+                                                      uint32_t rows, uint32_t cols, Divisor chunks, float factor, bool stream, DropArgs a) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, k = chunks.of(i), r = row0 + k, c = (i - k * chunks.d) * 8;
+    if (k >= rows) return;
     const Dropper drop(a);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const uint32_t r = (uint32_t)(i / chunks), c = (uint32_t)(i - (int64_t)r * chunks) * 8;
-        float v[8];
-        load8(x + (int64_t)r * ldx + c, (int64_t)cols - c, v);
+    const T* const from = x + r * ldx + c;
+    T* const to = out + r * ldo + c;
+    float v[8];
+    if (c + 8 <= cols) {
+        load8(from, 8, v);
         drop.apply(v, r, c, factor);
-        store8(out + (int64_t)r * ldo + c, (int64_t)cols - c, v);
+        store8(to, 8, v, stream);
+    } else {
+        load8(from, (int64_t)cols - c, v);
+        drop.apply(v, r, c, factor);
+        store8(to, (int64_t)cols - c, v);
     }
 }
 
 template <typename T>
 hipError_t launch(const void* x, int64_t ldx, void* out, int64_t ldo, int64_t rows, int64_t cols, float factor,
                   const DropArgs& a, hipStream_t s) {
-    IA_LAUNCH("dropout_kernel", dropout_kernel<T>, dim3(grid_for(rows * ceil_div(cols, 8))), dim3(256), 0, s,
-              (const T*)x, ldx, (T*)out, ldo, rows, (uint32_t)cols, factor, a);
+    const Divisor chunks((uint32_t)ceil_div(cols, 8));
+    const int64_t most = (((int64_t)1 << 31) - 256) / chunks.d;
+    for (int64_t r = 0; r < rows; r += most) {
+        const int64_t here = std::min(most, rows - r);
+        IA_LAUNCH("dropout_kernel", dropout_kernel<T>, dim3((unsigned)ceil_div(here * chunks.d, 256)), dim3(256), 0, s,
+                  (const T*)x, ldx, (T*)out, ldo, (uint32_t)r, (uint32_t)here, (uint32_t)cols, chunks, factor,
+                  rows * cols * (int64_t)sizeof(T) >= kStreamBytes, a);
+    }
     return hipGetLastError();
 }
 

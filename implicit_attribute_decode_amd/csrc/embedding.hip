@@ -7,6 +7,7 @@
 // the same on every run, no floating-point atomics take part.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "mx4_common.h"
@@ -23,9 +24,24 @@ struct DenseTable {
     int64_t ld;
     uint32_t dim;
 
-    // values c .. c + 7 of entry v
-    __device__ __forceinline__ void load(int64_t v, uint32_t c, float (&x)[8]) const {
-        load8(t + v * ld + c, (int64_t)dim - c, x);
+    struct Raw {
+        T v[8];
+    };
+    // values c .. c + 7 of entry v: loaded at once where they all exist, and as floats
+    __device__ __forceinline__ Raw load(int64_t v, uint32_t c) const {
+        Raw r;
+        __builtin_memcpy(&r, t + v * ld + c, sizeof(r));
+        return r;
+    }
+    __device__ __forceinline__ Raw load_some(int64_t v, uint32_t c) const {
+        Raw r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.v[j] = t[v * ld + min(c + j, dim - 1)];
+        return r;
+    }
+    __device__ __forceinline__ void get(const Raw& r, float (&x)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (float)r.v[j];
     }
 };
 
@@ -36,41 +52,73 @@ struct Mx4Table {
     const uint8_t* scales;
     int64_t blocks;
 
-    __device__ __forceinline__ void load(int64_t v, uint32_t c, float (&x)[8]) const {
+    struct Raw {
+        uint32_t codes;
+        uint8_t scale;
+    };
+    __device__ __forceinline__ Raw load(int64_t v, uint32_t c) const {
         const int64_t block = v * blocks + (c >> 5);
-        const uint32_t q = codes[4 * block + ((c >> 3) & 3)], byte = scales[block];
+        return Raw{codes[4 * block + ((c >> 3) & 3)], scales[block]};
+    }
+    __device__ __forceinline__ Raw load_some(int64_t v, uint32_t c) const { return load(v, c); }
+    __device__ __forceinline__ void get(const Raw& r, float (&x)[8]) const {
+        const uint32_t byte = r.scale;
         const float s = __builtin_bit_cast(float, byte << 23);
-        typedef float pair __attribute__((ext_vector_type(2)));
-        const pair p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
-        const pair p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
-        const pair p[4] = {p0, p1, p2, p3};
+        const floatx2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.codes, s, 0),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.codes, s, 1),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.codes, s, 2),
+                              __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r.codes, s, 3)};
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = byte == (uint32_t)kNaNByte ? __builtin_nanf("") : (float)p[j >> 1][j & 1];
     }
 };
 
-// Eight values of a row a thread.  An index outside [0, entries) gives zeros.
-template <typename Table, typename I, typename O, bool DROP>
-__global__ void __launch_bounds__(256) embedding_kernel(Table t, const I* index, int64_t istride, int64_t n, int64_t entries,
-                                                        uint32_t dim, float factor, O* out, int64_t ldo, DropArgs a) {
-    const uint32_t chunks = (dim + 7) / 8;
-    const int64_t total = n * chunks;
-    const Dropper drop(a);
-    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < total; k += (int64_t)gridDim.x * 256) {
-        const uint32_t r = (uint32_t)(k / chunks), c = (uint32_t)(k - (int64_t)r * chunks) * 8;
-        const int64_t v = (int64_t)index[(int64_t)r * istride];
-        float x[8] = {};
-        if (v >= 0 && v < entries) {
-            t.load(v, c, x);
-            if (DROP) {
-                drop.apply(x, r, c, factor);
-            } else {
+// Eight values of EACH rows a thread: rows k, k + step, ... of `rows` from row0 on,
+// fewer than 2^31 threads.  An index outside [0, entries) gives zeros (entry 0 is
+// loaded for it).  A row's load waits for its index's, so several are under way.
+template <typename Table, typename I, typename O, bool DROP, int EACH>
+__global__ void __launch_bounds__(256) embedding_kernel(Table t, const I* index, int64_t istride, uint32_t row0, uint32_t rows,
+                                                        uint32_t step, int64_t entries, uint32_t dim, Divisor chunks,
+                                                        float factor, O* out, int64_t ldo, bool stream, DropArgs a) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, k = chunks.of(i), c = (i - k * chunks.d) * 8;
+    if (k >= step) return;
+    int64_t v[EACH];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= factor;
-            }
+    for (int e = 0; e < EACH; ++e) v[e] = (int64_t)index[(int64_t)(row0 + min(k + e * step, rows - 1)) * istride];
+    const Dropper drop(a);
+    const auto there = [&](int e) { return v[e] >= 0 && v[e] < entries; };
+    const auto put = [&](const typename Table::Raw& raw, int e, int64_t count) {
+        const uint32_t r = row0 + k + e * step;
+        if (k + e * step >= rows) return;
+        float x[8];
+        t.get(raw, x);
+        if (DROP) {
+            drop.apply(x, r, c, factor);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= factor;
         }
-        store8(out + (int64_t)r * ldo + c, (int64_t)dim - c, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = there(e) ? x[j] : 0.0f;
+        store8(out + (int64_t)r * ldo + c, count, x, stream);
+    };
+    if (c + 8 <= dim) {
+        typename Table::Raw raw[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) raw[e] = t.load(there(e) ? v[e] : 0, c);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) put(raw[e], e, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) put(t.load_some(there(e) ? v[e] : 0, c), e, (int64_t)dim - c);
     }
+}
+
+// No entries: zeros.
+template <typename O>
+__global__ void __launch_bounds__(256) embedding_none_kernel(O* out, int64_t ldo, int64_t n, int64_t dim) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * dim; i += (int64_t)gridDim.x * 256)
+        out[i / dim * ldo + i % dim] = (O)0.0f;
 }
 
 struct LookupArgs {
@@ -84,15 +132,35 @@ struct LookupArgs {
     hipStream_t s;
 };
 
+template <typename O, typename Table, typename I, bool DROP, int EACH>
+void launch_rows(const Table& t, const LookupArgs& p, const Divisor& chunks, int64_t row0, int64_t rows) {
+    const int64_t step = ceil_div(rows, EACH);
+    IA_LAUNCH("embedding_kernel", (embedding_kernel<Table, I, O, DROP, EACH>), dim3((unsigned)ceil_div(step * chunks.d, 256)),
+              dim3(256), 0, p.s, t, (const I*)p.index, p.istride, (uint32_t)row0, (uint32_t)rows, (uint32_t)step, p.entries,
+              (uint32_t)p.dim, chunks, p.factor, (O*)p.out, p.ldo, p.n * p.dim * (int64_t)sizeof(O) >= kStreamBytes,
+              p.drop ? *p.drop : DropArgs{});
+}
 template <typename O, typename Table, typename I, bool DROP>
 hipError_t launch_lookup(const Table& t, const LookupArgs& p) {
-    IA_LAUNCH("embedding_kernel", (embedding_kernel<Table, I, O, DROP>), dim3(grid_for(p.n * ceil_div(p.dim, 8))),
-              dim3(256), 0, p.s, t, (const I*)p.index, p.istride, p.n, p.entries, (uint32_t)p.dim, p.factor, (O*)p.out,
-              p.ldo, p.drop ? *p.drop : DropArgs{});
+    const Divisor chunks((uint32_t)ceil_div(p.dim, 8));
+    const int64_t most = (((int64_t)1 << 31) - 256) / chunks.d;
+    for (int64_t r = 0; r < p.n; r += most) {
+        const int64_t here = std::min(most, p.n - r);
+        // four rows a thread where that leaves waves for the whole chip
+        if (here * chunks.d >= (int64_t)4 * 64 * 8192)
+            launch_rows<O, Table, I, DROP, 4>(t, p, chunks, r, here);
+        else
+            launch_rows<O, Table, I, DROP, 1>(t, p, chunks, r, here);
+    }
     return hipGetLastError();
 }
 template <typename O, typename Table>
 hipError_t lookup(const Table& t, const LookupArgs& p) {
+    if (p.entries == 0) {
+        IA_LAUNCH("embedding_none_kernel", embedding_none_kernel<O>, dim3(grid_for(p.n * p.dim)), dim3(256), 0, p.s, (O*)p.out,
+                  p.ldo, p.n, p.dim);
+        return hipGetLastError();
+    }
     if (p.index_bytes == 8)
         return p.drop ? launch_lookup<O, Table, int64_t, true>(t, p) : launch_lookup<O, Table, int64_t, false>(t, p);
     return p.drop ? launch_lookup<O, Table, int32_t, true>(t, p) : launch_lookup<O, Table, int32_t, false>(t, p);

@@ -167,15 +167,6 @@ struct Source {
     int64_t rows, cols, ldx, ldy;
 };
 
-// Row of block i of a matrix with `blocks` blocks a row, where i is at most 255
-// past `base`, which is the same for all threads: one 64-bit division for the
-// workgroup and a 32-bit one a thread.
-__device__ __forceinline__ int64_t row_of(int64_t i, int64_t blocks, int64_t base) {
-    const int64_t r = base / blocks;
-    const int64_t k = i - r * blocks;
-    return r + (blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)k / (uint32_t)blocks) : k / blocks);
-}
-
 // One thread per block of a row.  Bound by its bytes: 8,192 x 8,192 in bf16, 170 MB
 // in 36 us (4.7 TB/s).
 template <typename T>

@@ -10,6 +10,7 @@ namespace ia {
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
@@ -62,6 +63,15 @@ __device__ __forceinline__ void wave_lds_sync() {
 __device__ __forceinline__ void stage_barrier() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+}
+
+// Row of block i of a matrix with `blocks` blocks a row, where i is at most 255
+// past `base`, which is the same for all threads: one 64-bit division for the
+// workgroup and a 32-bit one a thread.
+__device__ __forceinline__ int64_t row_of(int64_t i, int64_t blocks, int64_t base) {
+    const int64_t r = base / blocks;
+    const int64_t k = i - r * blocks;
+    return r + (blocks < ((int64_t)1 << 31) ? (int64_t)((uint32_t)k / (uint32_t)blocks) : k / blocks);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

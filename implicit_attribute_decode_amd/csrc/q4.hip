@@ -2,6 +2,9 @@
 // product of a few unquantised rows with them.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "q4_common.h"
 
 namespace ia {
@@ -9,81 +12,150 @@ namespace {
 
 // ------------------------------------------------------------ quantisation
 
-// w / s rounded to the nearest whole number, ties to even, exactly: the product
-// with the reciprocal is off by one at most, and next to a border only; r s and
-// the rest of w are exact in fp32 (r has 4 bits, s 16).
+// The scale of a group from its least and greatest value (at most 0 and at least
+// 0): (hi - lo) / 15 rounded up to 16 bits, which is the least 16-bit number s with
+// 15 s >= hi - lo.  (Where 15 s is below hi - lo in double, it is so by at least the
+// last place of 15 s, more than the rounding of the quotient can hide.)  The
+// quotient in fp32 is off by a few 2^-24, so one of three numbers.
+__device__ __forceinline__ float group_scale(float lo, float hi) {
+    constexpr float k15 = 1.0f / 15.0f;
+    const uint32_t c = __builtin_bit_cast(uint32_t, __builtin_fmaf(-lo, k15, hi * k15)) & ~255u;
+    const double range = (double)hi - (double)lo;
+    const float s0 = __builtin_bit_cast(float, c), s1 = __builtin_bit_cast(float, c + 256u);
+    const float s = 15.0 * (double)s0 >= range ? s0 : 15.0 * (double)s1 >= range ? s1 : __builtin_bit_cast(float, c + 512u);
+    return fmaxf(s, 0x1p-100f);
+}
+
+// w / s rounded to the nearest whole number r, ties to even: the product with the
+// reciprocal is off by one at most, and next to a border only.  r s and d = w - r s
+// are exact in fp32 (r has 4 bits, s 16), so d tells.
+__device__ __forceinline__ float near_code(float w, float s, float inverse, float& d) {
+    const float r = rintf(w * inverse);
+    d = __builtin_fmaf(-r, s, w);
+    return r;
+}
 __device__ __forceinline__ float nearest_code(float w, float s, float inverse) {
-    float r = rintf(w * inverse);
-    const float d = __builtin_fmaf(-r, s, w), h = 0.5f * s;
+    float d, r = near_code(w, s, inverse, d);
+    const float h = 0.5f * s;
     const bool odd = ((int)r & 1) != 0;
     if (d > h || (d == h && odd)) r += 1.0f;
     if (d < -h || (d == -h && odd)) r -= 1.0f;
     return r;
 }
 
-// Eight values a thread, G / 8 threads a group.  lo and hi include zero; s =
-// (hi - lo) / 15 in double, rounded up to 16 bits (at least 2^-100), z = the
-// code nearest to -lo / s.  A group that is not finite has the scale NaN.
+// A value of another lane: of pairs, pairs of pairs and so on exchanged (once the
+// lanes of a pair agree, mirrored ones do as well).
+constexpr int kPairs = 0xB1, kTwos = 0x4E, kFours = 0x141, kEights = 0x140;  // DPP: quad permutations, half row and row mirrored
+template <int CTRL>
+__device__ __forceinline__ float exchanged(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, CTRL, 0xf, 0xf, true));
+}
+
+// Rows from row0 on, fewer than 2^31 threads.
+struct Q4Rows {
+    uint32_t row0, rows;
+    int64_t cols;
+    Divisor chunks;  // of eight values a row, all its groups' (threads)
+};
+
+// Eight values a thread, G / 8 threads a group.  z = the code nearest to -lo / s.  A
+// group that is not finite has the scale NaN.
 template <typename T, int G>
-__global__ void __launch_bounds__(256) q4_quantize_kernel(const T* x, int64_t ldx, int64_t rows, int64_t cols, uint32_t* codes,
-                                                          uint32_t* words) {
-    constexpr int LANES = G / 8;
-    const int64_t groups = q4_groups(cols, G), chunks = groups * LANES, total = rows * chunks, ldw = q4_word_stride(groups);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / chunks, k = i - r * chunks, g = k / LANES;
-        float v[8];
-        load8(x + r * ldx + 8 * k, cols - 8 * k, v);
-        float lo = 0.0f, hi = 0.0f;
-        uint32_t top = 0;
+__global__ void __launch_bounds__(256) q4_quantize_kernel(const T* x, int64_t ldx, Q4Rows p, uint32_t* codes, uint32_t* words) {
+    constexpr uint32_t LANES = G / 8;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, at = p.chunks.of(i), r = p.row0 + at, k = i - at * p.chunks.d;
+    if (at >= p.rows) return;  // whole groups of threads
+    float v[8];
+    const T* const from = x + r * ldx + 8 * (int64_t)k;
+    if (8 * ((int64_t)k + 1) <= p.cols) {
+        load8(from, 8, v);
+    } else {
+        load8(from, p.cols - 8 * (int64_t)k, v);
+    }
+    float lo = 0.0f, hi = 0.0f;
+    uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            lo = fminf(lo, v[j]);
-            hi = fmaxf(hi, v[j]);
-            top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
-        }
+    for (int j = 0; j < 8; ++j) {
+        lo = fminf(lo, v[j]);
+        hi = fmaxf(hi, v[j]);
+        top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+    }
+    if (top >= 0x7f800000u) hi = __builtin_huge_valf();  // also for a NaN
+    const auto reduce = [&](auto exchange) {
+        constexpr int CTRL = decltype(exchange)::value;
+        lo = fminf(lo, exchanged<CTRL>(lo));
+        hi = fmaxf(hi, exchanged<CTRL>(hi));
+    };
+    reduce(std::integral_constant<int, kPairs>{});
+    reduce(std::integral_constant<int, kTwos>{});
+    if (LANES > 4) reduce(std::integral_constant<int, kFours>{});
+    if (LANES > 8) reduce(std::integral_constant<int, kEights>{});
+    const float s = group_scale(lo, hi), inverse = 1.0f / s, z = nearest_code(-lo, s, inverse);
+    float c[8], most = 0.0f;
 #pragma unroll
-        for (int m = 1; m < LANES; m *= 2) {
-            lo = fminf(lo, __shfl_xor(lo, m));
-            hi = fmaxf(hi, __shfl_xor(hi, m));
-            top = max(top, (uint32_t)__shfl_xor((int)top, m));
-        }
-        const double range = ((double)hi - (double)lo) / 15.0;
-        const uint64_t low = ((uint64_t)1 << 37) - 1;
-        const uint64_t bits = (__builtin_bit_cast(uint64_t, range) + low) & ~low;
-        float s = fmaxf((float)__builtin_bit_cast(double, bits), 0x1p-100f);
-        const float inverse = 1.0f / s;
-        const float z = nearest_code(-lo, s, inverse);
-        uint32_t q = 0, word = __builtin_bit_cast(uint32_t, s) | (uint32_t)z;
+    for (int j = 0; j < 8; ++j) {
+        float d;
+        c[j] = near_code(v[j], s, inverse, d);
+        most = fmaxf(most, fabsf(d));
+    }
+    if (most >= 0.5f * s) {  // a border
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q |= (uint32_t)fminf(fmaxf(nearest_code(v[j], s, inverse) + z, 0.0f), 15.0f) << (4 * j);
-        if (hi == lo) q = word = 0;  // zeros
-        if (top >= 0x7f800000u) {
-            q = 0;
-            word = 0x7fc00000u;
-        }
-        codes[r * chunks + k] = q;
-        if (k % LANES == 0) {
-            words[r * ldw + g] = word;
-            if (g == groups - 1)
-                for (int64_t j = groups; j < ldw; ++j) words[r * ldw + j] = 0;
-        }
+        for (int j = 0; j < 8; ++j) c[j] = nearest_code(v[j], s, inverse);
+    }
+    uint32_t q = 0, word = __builtin_bit_cast(uint32_t, s) | (uint32_t)z;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = fminf(fmaxf(c[j] + z, 0.0f), 15.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_fmaf(c[2 * j + 1], 16.0f, c[2 * j]), j, q);
+    if (hi == lo) q = word = 0;  // zeros
+    if (hi == __builtin_huge_valf()) {
+        q = 0;
+        word = 0x7fc00000u;
+    }
+    const uint32_t groups = p.chunks.d / LANES, g = k / LANES;
+    const int64_t ldw = q4_word_stride(groups);
+    codes[(int64_t)r * p.chunks.d + k] = q;
+    if (k % LANES == 0) {
+        words[r * ldw + g] = word;
+        if (g == groups - 1)
+            for (int64_t j = groups; j < ldw; ++j) words[r * ldw + j] = 0;
     }
 }
 
 // Eight values a thread.  s (q - z) is exact in fp32, then rounded once.
 template <typename T, int G>
-__global__ void __launch_bounds__(256) q4_dequantize_kernel(const uint32_t* codes, const uint32_t* words, int64_t rows,
-                                                            int64_t cols, T* x, int64_t ldx) {
-    const int64_t groups = q4_groups(cols, G), chunks = groups * (G / 8), total = rows * chunks, ldw = q4_word_stride(groups);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / chunks, k = i - r * chunks;
-        const uint32_t q = codes[i], w = words[r * ldw + k / (G / 8)];
-        float v[8];
+__global__ void __launch_bounds__(256) q4_dequantize_kernel(const uint32_t* codes, const uint32_t* words, Q4Rows p, T* x,
+                                                            int64_t ldx, bool stream) {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, at = p.chunks.of(i), r = p.row0 + at, k = i - at * p.chunks.d;
+    if (at >= p.rows) return;
+    const int64_t ldw = q4_word_stride(p.chunks.d / (G / 8));
+    const uint32_t w = words[r * ldw + k / (G / 8)];
+    const Nibbles q(codes[(int64_t)r * p.chunks.d + k]);
+    const float s = scale_of(w), z = zero_of(w);
+    float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = scale_of(w) * ((float)((q >> (4 * j)) & 15u) - zero_of(w));
-        store8(x + r * ldx + 8 * k, cols - 8 * k, v);
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = s * (q.value<0>(j) - z);
+        v[2 * j + 1] = s * (q.value<1>(j) - z);
     }
+    T* const to = x + r * ldx + 8 * (int64_t)k;
+    if (8 * ((int64_t)k + 1) <= p.cols)
+        store8(to, 8, v, stream);
+    else
+        store8(to, p.cols - 8 * (int64_t)k, v);
+}
+
+// Launches over at most 2^31 threads each.
+template <typename Fn>
+hipError_t for_rows(const Q4View& q, const Fn& launch) {
+    const Divisor chunks((uint32_t)(q4_groups(q.cols, q.group) * (q.group / 8)));
+    const int64_t most = (((int64_t)1 << 31) - 256) / chunks.d;
+    for (int64_t r = 0; r < q.rows; r += most) {
+        const int64_t here = std::min(most, q.rows - r);
+        launch(Q4Rows{(uint32_t)r, (uint32_t)here, q.cols, chunks}, dim3((unsigned)ceil_div(here * chunks.d, 256)));
+    }
+    return hipGetLastError();
 }
 
 // ------------------------------------------------------------ product
@@ -338,9 +410,10 @@ hipError_t launch_linear(const void* x, int64_t M, int64_t ldx, int group, const
 
 template <typename T, int G>
 hipError_t quantize(const void* x, int64_t ldx, const Q4View& o, hipStream_t s) {
-    IA_LAUNCH("q4_quantize_kernel", (q4_quantize_kernel<T, G>), dim3(grid_for(o.rows * q4_groups(o.cols, G) * (G / 8))),
-              dim3(256), 0, s, (const T*)x, ldx, o.rows, o.cols, (uint32_t*)o.codes, o.words);
-    return hipGetLastError();
+    return for_rows(o, [&](const Q4Rows& p, dim3 grid) {
+        IA_LAUNCH("q4_quantize_kernel", (q4_quantize_kernel<T, G>), grid, dim3(256), 0, s, (const T*)x, ldx, p,
+                  (uint32_t*)o.codes, o.words);
+    });
 }
 template <typename T>
 hipError_t launch_quantize(const void* x, int64_t ldx, const Q4View& o, hipStream_t s) {
@@ -350,9 +423,10 @@ hipError_t launch_quantize(const void* x, int64_t ldx, const Q4View& o, hipStrea
 
 template <typename T, int G>
 hipError_t dequantize(const Q4View& q, void* x, int64_t ldx, hipStream_t s) {
-    IA_LAUNCH("q4_dequantize_kernel", (q4_dequantize_kernel<T, G>), dim3(grid_for(q.rows * q4_groups(q.cols, G) * (G / 8))),
-              dim3(256), 0, s, (const uint32_t*)q.codes, q.words, q.rows, q.cols, (T*)x, ldx);
-    return hipGetLastError();
+    return for_rows(q, [&](const Q4Rows& p, dim3 grid) {
+        IA_LAUNCH("q4_dequantize_kernel", (q4_dequantize_kernel<T, G>), grid, dim3(256), 0, s, (const uint32_t*)q.codes, q.words,
+                  p, (T*)x, ldx, q.rows * q.cols * (int64_t)sizeof(T) >= kStreamBytes);
+    });
 }
 template <typename T>
 hipError_t launch_dequantize(const Q4View& q, void* x, int64_t ldx, hipStream_t s) {

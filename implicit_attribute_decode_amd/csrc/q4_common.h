@@ -19,7 +19,6 @@ typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bfloatx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bfloatx8 __attribute__((ext_vector_type(8)));
-typedef float floatx2 __attribute__((ext_vector_type(2)));
 
 __host__ __device__ inline int64_t q4_groups(int64_t cols, int group) { return (cols + group - 1) / group; }
 __host__ __device__ inline int64_t q4_word_stride(int64_t groups) { return (groups + 3) & ~(int64_t)3; }

@@ -848,7 +848,8 @@ typedef struct {
  *   q = x / s rounded to nearest, ties to even, plus z, held to 0..15.
  * A group with a NaN or an infinity has the scale NaN and zero codes.  out must
  * not overlap x.  Errors: INVALID_ARG (null, sizes, 0 < ldx < cols,
- * misalignment, over 2^40 values, overlap), UNSUPPORTED (dtype, group), DEVICE. */
+ * misalignment, rows or cols of 2^31 and more, over 2^40 values, overlap),
+ * UNSUPPORTED (dtype, group), DEVICE. */
 IA_API ia_status ia_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const ia_q4* out, void* stream);
 
 /* x[rows][cols] (rows ldx >= cols apart) = s (q - z), rounded once to dtype.

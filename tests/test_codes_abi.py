@@ -116,7 +116,8 @@ def _q(**kw):
 
 
 Q4 = [(dict(codes=None), BAD), (dict(codes=_far(1) + 8), BAD), (dict(words=None), BAD), (dict(words=_far(2) + 4), BAD),
-      (dict(rows=-1), BAD), (dict(cols=-1), BAD), (dict(rows=1 << 40), BAD), (dict(group=16), UNSUPPORTED),
+      (dict(rows=-1), BAD), (dict(cols=-1), BAD), (dict(rows=1 << 31, cols=1), BAD), (dict(rows=1, cols=1 << 31), BAD),
+      (dict(rows=1 << 30, cols=1 << 11), BAD), (dict(group=16), UNSUPPORTED),
       (dict(group=0), UNSUPPORTED), (dict(group=256), UNSUPPORTED)]
 
 
