@@ -588,6 +588,7 @@ def ia_embedding_mx4(table: Mx4, index, index_bytes: int, n: int, index_stride: 
                                    _ptr(out), ldo, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)  # a shape has one size
 def ia_embedding_backward_workspace_size(n: int, entries: int, dim: int) -> int:
     b = C.c_size_t()
     _check(load().ia_embedding_backward_workspace_size(n, entries, dim, C.byref(b)))
@@ -615,6 +616,7 @@ def ia_q4_dequantize(q: Q4, dtype: int, x, ldx: int, stream=None):
     _check(load().ia_q4_dequantize(C.byref(q), dtype, _ptr(x), ldx, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)  # a shape has one size
 def ia_q4_linear_workspace_size(dtype: int, M: int, K: int, N: int) -> int:
     n = C.c_size_t()
     _check(load().ia_q4_linear_workspace_size(dtype, M, K, N, C.byref(n)))

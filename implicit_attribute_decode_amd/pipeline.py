@@ -894,10 +894,12 @@ class Mx4Linear:
         return mx4_linear_backward(dy, x, self.wt, y if self.act == "relu" else None, want_x)
 
 
-def _here(t: torch.Tensor):
-    """Refuses a tensor that is not on the current GPU, whose stream the call takes."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("the tensors are not on the current device")
+def _here(*tensors):
+    """Refuses tensors that are not on the current GPU, whose stream the call takes (None stands for no tensor)."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("the tensors must be on the current device")
 
 
 class Dropout:
@@ -928,13 +930,12 @@ class Dropout:
         """x [rows, cols] (float32, float16 or bfloat16) with dropout; out may be x."""
         d, rows, cols, ldx = _matrix(x, "x")
         if out is None:
-            out, ldo = torch.empty((rows, cols), dtype=x.dtype, device=x.device), cols
+            out, ldo = x.new_empty((rows, cols)), cols
         else:
             do, r, c, ldo = _matrix(out, "out")
             if (do, r, c) != (d, rows, cols):
                 raise ValueError("out has another shape or type")
-        _here(x)
-        _one_device(x, out, self._step)
+        _here(x, out, self._step)
         ia.ia_dropout(x, d, rows, cols, ldx, self.c, out, ldo)
         return out
 
@@ -963,20 +964,19 @@ def embedding(table, index: torch.Tensor, scale: float = 1.0, dtype=None, dropou
     of zeros."""
     b, n, stride = _index(index)
     if packed := isinstance(table, Mx4Tensor):
-        entries, dim, device, own = table.rows, table.cols, table._codes.device, torch.float32
+        entries, dim, memory, own = table.rows, table.cols, table._codes, torch.float32
     else:
         d, entries, dim, ld = _matrix(table, "table")
-        device, own = table.device, table.dtype
+        memory, own = table, table.dtype
     if out is None:
-        out, ldo = torch.empty((n, dim), dtype=dtype or own, device=device), dim
+        out, ldo = memory.new_empty((n, dim), dtype=dtype or own), dim
         do = _dtype(out)
     else:
         do, rows, cols, ldo = _matrix(out, "out")
         if (rows, cols) != (n, dim) or dtype not in (None, out.dtype):
             raise ValueError("out has another shape or type")
-    _here(index)
-    _one_device(index, table._codes if packed else table, out, dropout and dropout._step)
-    drop = dropout and dropout.c
+    step, drop = (None, None) if dropout is None else (dropout._step, dropout.c)
+    _here(index, memory, out, step)
     if packed:
         ia.ia_embedding_mx4(table.c, index, b, n, stride, scale, drop, do, out, ldo)
     else:
@@ -994,13 +994,13 @@ def embedding_backward(dy: torch.Tensor, index: torch.Tensor, entries: int, scal
     if rows != n:
         raise ValueError(f"dy has {rows} rows for {n} indices")
     if out is None:
-        out = torch.empty((entries, dim), dtype=torch.float32, device=dy.device)
+        out = dy.new_empty((entries, dim), dtype=torch.float32)
     elif out.dtype != torch.float32 or out.shape != (entries, dim) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous float32 [{entries}, {dim}]")
-    _here(index)
-    _one_device(index, dy, out, dropout and dropout._step)
+    step, drop = (None, None) if dropout is None else (dropout._step, dropout.c)
+    _here(index, dy, out, step)
     ws = _bytes(ia.ia_embedding_backward_workspace_size(n, entries, dim), dy.device)
-    ia.ia_embedding_backward(dy, d, dim, ld, index, b, n, stride, entries, scale, dropout and dropout.c, out, ws)
+    ia.ia_embedding_backward(dy, d, dim, ld, index, b, n, stride, entries, scale, drop, out, ws)
     return out
 
 
@@ -1009,39 +1009,48 @@ class Q4Tensor:
     32, 64 or 128 values of a row, which stand for scale * (code - zero): codes
     uint8 [rows, groups * group / 2] (two a byte, the earlier one in the low
     half), words int32 [rows, groups rounded up to 4] (the bits of the scale as a
-    float32 whose lowest byte is zero, and in that byte the zero, 0..15)."""
+    float32 whose lowest byte is zero, and in that byte the zero, 0..15).  The
+    tensors are not replaced; their values may change (quantised anew)."""
 
     __slots__ = ("_codes", "_words", "rows", "cols", "group", "c")
 
     def __init__(self, codes: torch.Tensor, words: torch.Tensor, cols: int, group: int):
-        if group not in (32, 64, 128):
-            raise ValueError("groups are of 32, 64 or 128 values")
-        groups, rows = (cols + group - 1) // group, codes.shape[0]
+        shapes = self._shapes(codes.shape[0], cols, group)
         if codes.dtype != torch.uint8 or words.dtype != torch.int32 or not codes.is_cuda or not words.is_cuda:
             raise ValueError("codes must be uint8 and words int32 tensors on the GPU")
         _one_device(codes, words)
-        shapes = (rows, groups * group // 2), (rows, (groups + 3) // 4 * 4)
         if (codes.shape, words.shape) != shapes or not codes.is_contiguous() or not words.is_contiguous():
             raise ValueError(f"codes {list(shapes[0])} and words {list(shapes[1])} expected, contiguous")
-        self._codes, self._words, self.rows, self.cols, self.group = codes, words, rows, cols, group
-        self.c = ia.q4(codes, words, rows, cols, group)
+        self._set(codes, words, cols, group)
+
+    @staticmethod
+    def _shapes(rows: int, cols: int, group: int):
+        if group not in (32, 64, 128):
+            raise ValueError("groups are of 32, 64 or 128 values")
+        groups = (cols + group - 1) // group
+        return (rows, groups * group // 2), (rows, (groups + 3) // 4 * 4)
+
+    def _set(self, codes, words, cols, group):
+        self._codes, self._words, self.rows, self.cols, self.group = codes, words, codes.shape[0], cols, group
+        self.c = ia.q4(codes, words, self.rows, cols, group)
 
     codes = property(lambda self: self._codes)
     words = property(lambda self: self._words)
 
     @classmethod
     def empty(cls, rows: int, cols: int, group: int = 128, device="cuda"):
-        if group not in (32, 64, 128):
-            raise ValueError("groups are of 32, 64 or 128 values")
-        groups = (cols + group - 1) // group
-        return cls(torch.empty((rows, groups * group // 2), dtype=torch.uint8, device=device),
-                   torch.empty((rows, (groups + 3) // 4 * 4), dtype=torch.int32, device=device), cols, group)
+        codes, words = cls._shapes(rows, cols, group)
+        q = cls.__new__(cls)
+        q._set(torch.empty(codes, dtype=torch.uint8, device=device), torch.empty(words, dtype=torch.int32, device=device),
+               cols, group)
+        return q
 
     @classmethod
     def from_parts(cls, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | int, cols: int, group: int):
-        """From codes and a [rows, groups] tensor of scales (rounded to 16
-        significant bits; exact for float16 and bfloat16) and of zeros in 0..15
-        (or one zero for all)."""
+        """From codes and [rows, groups] tensors of scales (finite or NaN; rounded
+        to 16 significant bits, so exact for float16 and bfloat16) and of zeros in
+        0..15 (or one zero for all).  Looks at the zeros on the host: it waits for
+        the GPU."""
         bits = scales.to(torch.float32).contiguous().view(torch.int32)
         bits = torch.where(torch.isfinite(scales), bits + 127 + ((bits >> 8) & 1), bits) & ~255
         zeros = torch.as_tensor(zeros, device=scales.device)
@@ -1063,26 +1072,27 @@ class Q4Tensor:
     def dequantize(self, dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
         """The values, rounded once to dtype (float32, float16 or bfloat16)."""
         if out is None:
-            out = torch.empty((self.rows, self.cols), dtype=dtype, device=self._codes.device)
-        d, rows, cols, ld = _matrix(out, "out")
-        if (rows, cols) != (self.rows, self.cols):
-            raise ValueError("out has another shape")
-        _here(out)
-        _one_device(out, self._codes)
+            out, ld = self._codes.new_empty((self.rows, self.cols), dtype=dtype), self.cols
+            d = _dtype(out)
+        else:
+            d, rows, cols, ld = _matrix(out, "out")
+            if (rows, cols) != (self.rows, self.cols):
+                raise ValueError("out has another shape")
+        _here(out, self._codes)
         ia.ia_q4_dequantize(self.c, d, out, ld)
         return out
 
 
 def q4_quantize(x: torch.Tensor, group: int = 128, out: Q4Tensor | None = None) -> Q4Tensor:
     """x [rows, cols] in 4 bits with a scale and a zero for each group of a row:
-    scale = (greatest - least) / 15, zero included, codes rounded to nearest."""
+    scale = (greatest - least) / 15, zero included, codes rounded to nearest.
+    With out (whose groups count) its tensors are filled anew."""
     d, rows, cols, ld = _matrix(x, "x")
     if out is None:
         out = Q4Tensor.empty(rows, cols, group, x.device)
     elif (out.rows, out.cols) != (rows, cols):
         raise ValueError("out has another shape")
-    _here(x)
-    _one_device(x, out._codes)
+    _here(x, out._codes)
     ia.ia_q4_quantize(x, d, ld, out.c)
     return out
 
@@ -1092,16 +1102,16 @@ def q4_linear(x: torch.Tensor, w: Q4Tensor, bias: torch.Tensor | None = None, ac
     """A linear layer with 4-bit weights and its input as it is: act(x w^T +
     bias), x [M, K], w [N, K]; returns [M, N] of x's type; act "none" or "relu"."""
     d, M, K, ldx = _matrix(x, "x")
+    N = w.rows
     if K != w.cols:
         raise ValueError(f"x has {K} columns, the weights {w.cols}")
     if out is None:
-        out, ldy = torch.empty((M, w.rows), dtype=x.dtype, device=x.device), w.rows
+        out, ldy = x.new_empty((M, N)), N
     else:
         do, rows, cols, ldy = _matrix(out, "out")
-        if (do, rows, cols) != (d, M, w.rows):
+        if (do, rows, cols) != (d, M, N):
             raise ValueError("out has another shape or type")
-    _here(x)
-    _one_device(x, w._codes, bias, out)
-    ws = _bytes(ia.ia_q4_linear_workspace_size(d, M, K, w.rows), x.device)
-    ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
+    _here(x, w._codes, bias, out)
+    ws = _bytes(ia.ia_q4_linear_workspace_size(d, M, K, N), x.device)
+    ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, N), _ACTS[act], out, ldy, ws)
     return out

@@ -176,7 +176,7 @@ def calls(monkeypatch):
     """{entry point: arguments of its last call}; tensors off the GPU pass for GPU ones."""
     seen = {}
     monkeypatch.setattr(pipeline, "_dtype", lambda t: pipeline._DTYPES[t.dtype])
-    monkeypatch.setattr(pipeline, "_here", lambda t: None)
+    monkeypatch.setattr(pipeline, "_here", lambda *t: None)
     monkeypatch.setattr(pipeline, "_index", lambda i: (pipeline._INDEX_BYTES[i.dtype], i.shape[0], i.stride(0)))
     for name in ("ia_dropout", "ia_embedding", "ia_embedding_backward"):
         monkeypatch.setattr(ia, name, lambda *a, _n=name: seen.__setitem__(_n, a))
