@@ -111,7 +111,8 @@ struct ManyArgs {
     int parts;
     int64_t M, pairs;    // pairs of stages: K in steps of 128
     Q4Linear w;
-    int64_t tiles_m, tiles_n, per_split;  // pairs of a split
+    int64_t tile0, tiles_m, tiles_n;  // of the launch; of all
+    int64_t per_split;   // pairs of a split
     float* sums;         // [splits][M][N], or null
 };
 
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
     const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t im, in;
-    tile_of(blockIdx.x, p.tiles_m, p.tiles_n, im, in);
+    tile_of(p.tile0 + blockIdx.x, p.tiles_m, p.tiles_n, im, in);
     const int64_t m0 = im * BM, n0 = in * BN;
     const int wm = wave % WM * 32 * TI, wn = wave / WM * 32 * TJ;
     const int64_t ldc = p.w.groups * (G / 2), ldw = q4_word_stride(p.w.groups);
@@ -416,8 +417,10 @@ hipError_t run(const ManyArgs& a, int splits, hipStream_t s) {
     ManyArgs p = a;
     p.tiles_m = ceil_div(p.M, BM);
     p.tiles_n = ceil_div(p.w.N, BN);
-    IA_LAUNCH("q4_matmul_kernel", (q4_matmul_kernel<V, T, G, BM, BN, WM, WN>), dim3((unsigned)(p.tiles_m * p.tiles_n), splits),
-              dim3(64 * WM * WN), 0, s, p);
+    const int64_t tiles = p.tiles_m * p.tiles_n, most = 1 << 20;  // a grid has less than 2^32 threads
+    for (p.tile0 = 0; p.tile0 < tiles; p.tile0 += most)
+        IA_LAUNCH("q4_matmul_kernel", (q4_matmul_kernel<V, T, G, BM, BN, WM, WN>),
+                  dim3((unsigned)std::min(most, tiles - p.tile0), splits), dim3(64 * WM * WN), 0, s, p);
     return hipGetLastError();
 }
 

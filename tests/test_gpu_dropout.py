@@ -117,3 +117,12 @@ def test_large_matrix_share():
         assert abs(kept.mean().item() - (1 - p)) < 6 * (p * (1 - p) / x.numel()) ** 0.5
         rows = kept.mean(1)
         assert (rows - (1 - p)).abs().max().item() < 8 * (p * (1 - p) / 256) ** 0.5
+
+
+def test_more_than_2_32_values():
+    """140,000 x 32,000 bf16 values (9 GB): places, not offsets, decide."""
+    x = torch.ones((140_000, 32_000), dtype=torch.bfloat16, device="cuda")
+    y = Dropout(0.5, 3, 1)(x, out=x)
+    for r in (0, 67_108, 67_109, 134_217, 139_999):
+        got = _f64(y[r:r + 1, 31_996:])
+        assert np.array_equal(got[0], [2.0 * (O.philox([7999, r, 1, 0], [3, 0])[c] >= 2 ** 31) for c in range(4)])

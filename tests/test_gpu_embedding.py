@@ -232,3 +232,33 @@ def test_captured_graph_replays_with_new_inputs_and_masks():
         assert torch.equal(out, want[0]) and torch.equal(grad, want[1])
         on = O.kept(3000, 48, 0.25, 11, 100 + k)
         assert not host(out)[~on].any()
+
+
+def test_tables_past_32_bit_offsets():
+    """70,000,000 entries of 32 values (4.5 GB in fp16, a gradient of 9 GB)."""
+    entries = 70_000_000
+    table = torch.zeros((entries, 32), dtype=torch.float16, device="cuda")
+    index = torch.tensor([entries - 1, 0, entries, entries - 5, 69_000_000, entries - 1, -1], device="cuda")
+    table[index[[0, 1, 3, 4]]] = torch.randn((4, 32), device="cuda").half()
+    want = torch.zeros((7, 32), dtype=torch.float16, device="cuda")
+    on = torch.tensor([0, 1, 3, 4, 5], device="cuda")
+    want[on] = table[index[on]]
+    assert torch.equal(embedding(table, index), want)
+    del table
+    dy = torch.ones((7, 32), device="cuda")
+    g = embedding_backward(dy, index, entries)
+    assert (g[entries - 1] == 2).all() and (g[index[[1, 3, 4]]] == 1).all()
+    assert g.sum(dtype=torch.float64).item() == 5 * 32
+
+
+def test_many_rows_in_a_large_table():
+    """More rows than a block sorts alone, few used entries far apart: three passes, long runs of zeros."""
+    rng = np.random.default_rng(4)
+    entries = 5_000_000
+    at = np.sort(rng.choice(entries, 40, replace=False))
+    index = at[rng.integers(0, 40, 30_000)]
+    dy = _table(rng, 30_000, 8)
+    g = embedding_backward(dy, cuda(index), entries)
+    want = O.lookup_gradient(_f64(dy), np.searchsorted(at, index), 40)
+    _assert_gradient(g[cuda(at)], want)
+    assert int((g != 0).any(1).sum()) == 40
