@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
 // Microseconds that a product takes, as measured on bf16 in groups of 128 over M of
 // 33 to 100,000, K of 32 to 8,192 and N of 58 to 11,008 (in brackets a case):
 //   few rows' kernel: 16 outputs of 64 rows a block, 256 blocks side by side take
-//     16.3 for 4,096 inputs, 1.75 at least (256 x 8,192 -> 1,024: 36)
+//     16.3 for 4,096 inputs (fp32 twice that), 1.75 at least (256 x 8,192 -> 1,024: 36)
 //   tiles of 128: 6.5 and 1.75 a pair of stages for up to 256 blocks, 0.8 of that
 //     for each 256 more, two to a CU (2,048 x 4,096 -> 4,096: 101)
 //   tiles of 256: 4 and 3.7 a pair for up to 128 blocks, 8 and 4.8 for 256 (4,096
@@ -391,7 +391,7 @@ Plan plan_of(int parts, int group, int64_t M, int64_t K, int64_t N) {
     const auto tiles = [&](int64_t m, int64_t n) { return (double)(ceil_div(M, m) * ceil_div(N, n)); };
     Plan best{kFew, 1, pairs};
     if (M <= 16 || K >= (int64_t)1 << 22) return best;  // a tile's offsets have 32 bits
-    double least = 2.5 + std::max(0.8, tiles(64, 16) / 256) * std::max(1.75, 16.3 * (double)K / 4096);
+    double least = 2.5 + std::max(0.8, tiles(64, 16) / 256) * std::max(1.75, (parts > 1 ? 32.6 : 16.3) * (double)K / 4096);
     const auto offer = [&](Way way, int64_t splits, double blocks) {
         const int64_t per = ceil_div(pairs, splits);
         double t;
