@@ -572,20 +572,25 @@ def _ref(s):
     return None if s is None else C.byref(s)
 
 
+def _handle(stream) -> int:
+    """A stream's raw handle as it is, else the handle of a stream or of the current one."""
+    return stream if type(stream) is int else _stream(stream)
+
+
 def ia_dropout(x, dtype: int, rows: int, cols: int, ldx: int, drop: Drop, out, ldo: int, stream=None):
-    _check(load().ia_dropout(_ptr(x), dtype, rows, cols, ldx, _ref(drop), _ptr(out), ldo, _stream(stream)))
+    _check(load().ia_dropout(x.data_ptr(), dtype, rows, cols, ldx, C.byref(drop), out.data_ptr(), ldo, _handle(stream)))
 
 
 def ia_embedding(table, dtype: int, entries: int, dim: int, ld: int, index, index_bytes: int, n: int, index_stride: int,
                  scale: float, drop: Drop | None, out_dtype: int, out, ldo: int, stream=None):
-    _check(load().ia_embedding(_ptr(table), dtype, entries, dim, ld, _ptr(index), index_bytes, n, index_stride, scale,
-                               _ref(drop), out_dtype, _ptr(out), ldo, _stream(stream)))
+    _check(load().ia_embedding(table.data_ptr(), dtype, entries, dim, ld, index.data_ptr(), index_bytes, n, index_stride,
+                               scale, _ref(drop), out_dtype, out.data_ptr(), ldo, _handle(stream)))
 
 
 def ia_embedding_mx4(table: Mx4, index, index_bytes: int, n: int, index_stride: int, scale: float, drop: Drop | None,
                      out_dtype: int, out, ldo: int, stream=None):
-    _check(load().ia_embedding_mx4(C.byref(table), _ptr(index), index_bytes, n, index_stride, scale, _ref(drop), out_dtype,
-                                   _ptr(out), ldo, _stream(stream)))
+    _check(load().ia_embedding_mx4(C.byref(table), index.data_ptr(), index_bytes, n, index_stride, scale, _ref(drop),
+                                   out_dtype, out.data_ptr(), ldo, _handle(stream)))
 
 
 @functools.lru_cache(maxsize=256)  # a shape has one size
@@ -597,8 +602,9 @@ def ia_embedding_backward_workspace_size(n: int, entries: int, dim: int) -> int:
 
 def ia_embedding_backward(dy, dtype: int, dim: int, lddy: int, index, index_bytes: int, n: int, index_stride: int,
                           entries: int, scale: float, drop: Drop | None, grad, ws=None, stream=None):
-    _check(load().ia_embedding_backward(_ptr(dy), dtype, dim, lddy, _ptr(index), index_bytes, n, index_stride, entries,
-                                        scale, _ref(drop), _ptr(grad), _ptr(ws), _nbytes(ws), _stream(stream)))
+    _check(load().ia_embedding_backward(dy.data_ptr(), dtype, dim, lddy, index.data_ptr(), index_bytes, n, index_stride,
+                                        entries, scale, _ref(drop), grad.data_ptr(), _ptr(ws), _nbytes(ws),
+                                        _handle(stream)))
 
 
 # ----------------------------------------------------------------- group-scaled 4 bits
@@ -609,11 +615,11 @@ def q4(codes, words, rows: int, cols: int, group: int) -> Q4:
 
 
 def ia_q4_quantize(x, dtype: int, ldx: int, out: Q4, stream=None):
-    _check(load().ia_q4_quantize(_ptr(x), dtype, ldx, C.byref(out), _stream(stream)))
+    _check(load().ia_q4_quantize(x.data_ptr(), dtype, ldx, C.byref(out), _handle(stream)))
 
 
 def ia_q4_dequantize(q: Q4, dtype: int, x, ldx: int, stream=None):
-    _check(load().ia_q4_dequantize(C.byref(q), dtype, _ptr(x), ldx, _stream(stream)))
+    _check(load().ia_q4_dequantize(C.byref(q), dtype, x.data_ptr(), ldx, _handle(stream)))
 
 
 @functools.lru_cache(maxsize=256)  # a shape has one size
@@ -624,8 +630,8 @@ def ia_q4_linear_workspace_size(dtype: int, M: int, K: int, N: int) -> int:
 
 
 def ia_q4_linear(x, dtype: int, M: int, ldx: int, w: Q4, bias, act: int, y, ldy: int, ws=None, stream=None):
-    _check(load().ia_q4_linear(_ptr(x), dtype, M, ldx, C.byref(w), _ptr(bias), act, _ptr(y), ldy, _ptr(ws), _nbytes(ws),
-                               _stream(stream)))
+    _check(load().ia_q4_linear(x.data_ptr(), dtype, M, ldx, C.byref(w), _ptr(bias), act, y.data_ptr(), ldy, _ptr(ws),
+                               _nbytes(ws), _handle(stream)))
 
 
 # ----------------------------------------------------------------- diagnostics

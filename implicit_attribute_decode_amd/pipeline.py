@@ -894,12 +894,17 @@ class Mx4Linear:
         return mx4_linear_backward(dy, x, self.wt, y if self.act == "relu" else None, want_x)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here(*tensors):
-    """Refuses tensors that are not on the current GPU, whose stream the call takes (None stands for no tensor)."""
+    """The current stream's raw handle (None where torch has no call for it); refuses tensors that are not on the
+    current GPU (None stands for no tensor)."""
     device = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError("the tensors must be on the current device")
+    return None if _raw_stream is None else _raw_stream(device)
 
 
 class Dropout:
@@ -935,8 +940,8 @@ class Dropout:
             do, r, c, ldo = _matrix(out, "out")
             if (do, r, c) != (d, rows, cols):
                 raise ValueError("out has another shape or type")
-        _here(x, out, self._step)
-        ia.ia_dropout(x, d, rows, cols, ldx, self.c, out, ldo)
+        stream = _here(x, out, self._step)
+        ia.ia_dropout(x, d, rows, cols, ldx, self.c, out, ldo, stream)
         return out
 
     def backward(self, dy: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -962,7 +967,7 @@ def embedding(table, index: torch.Tensor, scale: float = 1.0, dtype=None, dropou
     [entries, dim] tensor (float32, float16 or bfloat16) or an Mx4Tensor, whose
     picked rows alone are read back.  An index outside [0, entries) gives a row
     of zeros."""
-    b, n, stride = _index(index)
+    b, n, between = _index(index)
     if packed := isinstance(table, Mx4Tensor):
         entries, dim, memory, own = table.rows, table.cols, table._codes, torch.float32
     else:
@@ -976,11 +981,11 @@ def embedding(table, index: torch.Tensor, scale: float = 1.0, dtype=None, dropou
         if (rows, cols) != (n, dim) or dtype not in (None, out.dtype):
             raise ValueError("out has another shape or type")
     step, drop = (None, None) if dropout is None else (dropout._step, dropout.c)
-    _here(index, memory, out, step)
+    stream = _here(index, memory, out, step)
     if packed:
-        ia.ia_embedding_mx4(table.c, index, b, n, stride, scale, drop, do, out, ldo)
+        ia.ia_embedding_mx4(table.c, index, b, n, between, scale, drop, do, out, ldo, stream)
     else:
-        ia.ia_embedding(table, d, entries, dim, ld, index, b, n, stride, scale, drop, do, out, ldo)
+        ia.ia_embedding(table, d, entries, dim, ld, index, b, n, between, scale, drop, do, out, ldo, stream)
     return out
 
 
@@ -989,7 +994,7 @@ def embedding_backward(dy: torch.Tensor, index: torch.Tensor, entries: int, scal
     """The table's gradient [entries, dim] (float32, dense) of embedding(table,
     index, scale, dropout=dropout) for upstream dy [n, dim]: the sum of the rows
     that picked an entry, zeros where none did; the same on every run."""
-    b, n, stride = _index(index)
+    b, n, between = _index(index)
     d, rows, dim, ld = _matrix(dy, "dy")
     if rows != n:
         raise ValueError(f"dy has {rows} rows for {n} indices")
@@ -998,9 +1003,9 @@ def embedding_backward(dy: torch.Tensor, index: torch.Tensor, entries: int, scal
     elif out.dtype != torch.float32 or out.shape != (entries, dim) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous float32 [{entries}, {dim}]")
     step, drop = (None, None) if dropout is None else (dropout._step, dropout.c)
-    _here(index, dy, out, step)
+    stream = _here(index, dy, out, step)
     ws = _bytes(ia.ia_embedding_backward_workspace_size(n, entries, dim), dy.device)
-    ia.ia_embedding_backward(dy, d, dim, ld, index, b, n, stride, entries, scale, drop, out, ws)
+    ia.ia_embedding_backward(dy, d, dim, ld, index, b, n, between, entries, scale, drop, out, ws, stream)
     return out
 
 
@@ -1078,8 +1083,8 @@ class Q4Tensor:
             d, rows, cols, ld = _matrix(out, "out")
             if (rows, cols) != (self.rows, self.cols):
                 raise ValueError("out has another shape")
-        _here(out, self._codes)
-        ia.ia_q4_dequantize(self.c, d, out, ld)
+        stream = _here(out, self._codes)
+        ia.ia_q4_dequantize(self.c, d, out, ld, stream)
         return out
 
 
@@ -1092,8 +1097,8 @@ def q4_quantize(x: torch.Tensor, group: int = 128, out: Q4Tensor | None = None) 
         out = Q4Tensor.empty(rows, cols, group, x.device)
     elif (out.rows, out.cols) != (rows, cols):
         raise ValueError("out has another shape")
-    _here(x, out._codes)
-    ia.ia_q4_quantize(x, d, ld, out.c)
+    stream = _here(x, out._codes)
+    ia.ia_q4_quantize(x, d, ld, out.c, stream)
     return out
 
 
@@ -1111,7 +1116,7 @@ def q4_linear(x: torch.Tensor, w: Q4Tensor, bias: torch.Tensor | None = None, ac
         do, rows, cols, ldy = _matrix(out, "out")
         if (do, rows, cols) != (d, M, N):
             raise ValueError("out has another shape or type")
-    _here(x, w._codes, bias, out)
+    stream = _here(x, w._codes, bias, out)
     ws = _bytes(ia.ia_q4_linear_workspace_size(d, M, K, N), x.device)
-    ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, N), _ACTS[act], out, ldy, ws)
+    ia.ia_q4_linear(x, d, M, ldx, w.c, _bias(bias, N), _ACTS[act], out, ldy, ws, stream)
     return out
