@@ -76,6 +76,9 @@ struct Mx4Table {
 // Eight values of EACH rows a thread: rows k, k + step, ... of `rows` from row0 on,
 // fewer than 2^31 threads.  An index outside [0, entries) gives zeros (entry 0 is
 // loaded for it).  A row's load waits for its index's, so several are under way.
+// 300,000 rows of 256 bf16 values, the k-th entry picked 1 / k as often as the first,
+// with dropout: 61 us, 2.5 TB/s of the rows written, bound by the generator
+// (dropout.hip) as much as by the rows; with one row a thread 62.
 template <typename Table, typename I, typename O, bool DROP, int EACH>
 __global__ void __launch_bounds__(256) embedding_kernel(Table t, const I* index, int64_t istride, uint32_t row0, uint32_t rows,
                                                         uint32_t step, int64_t entries, uint32_t dim, Divisor chunks,
@@ -186,7 +189,9 @@ __device__ __forceinline__ uint64_t word_of(const I* index, int64_t istride, int
 constexpr int kThreads = 256;
 
 // A share of the gradient's zeros, written by the blocks from `first` on of a
-// kernel that leaves most of the chip idle: part k of `parts` of it.
+// kernel that leaves most of the chip idle: part k of `parts` of it.  (With the
+// 102 MB of 50,021 x 512 values the six kernels of a sort of 131,071 rows take 38 us;
+// the three of a pass over 300,000 rows with next to none 14.)
 struct Zeros {
     float* grad;
     int64_t values;
@@ -533,7 +538,9 @@ struct Quad {
 // An entry that also reaches the tile after the next is long: every tile leaves the
 // sum of its own rows, and the join adds those in order.  The words of a block's
 // tiles pass through LDS, and which rows a group needs is known before they are
-// loaded: no row of dy is read twice.
+// loaded: no row of dy is read twice.  131,071 rows of 512 bf16 values into 50,021
+// entries: 43 us for 134 MB of rows read in any order and about 60 MB of sums written
+// (4.5 TB/s).  Each load converted behind a branch on the row's end took twice that.
 template <typename T, bool DROP, int QUADS, Rows ROWS>
 __global__ void __launch_bounds__(256) embedding_sums_kernel(const T* dy, int64_t lddy, SumArgs p, DropArgs a) {
     extern __shared__ uint64_t s_words[];  // from a tile and a word before the first tile to two tiles past the last one's start
@@ -633,6 +640,8 @@ __global__ void __launch_bounds__(256) embedding_sums_kernel(const T* dy, int64_
 }
 
 // Long entries: the sums that their tiles left, added in double in a fixed order.
+// Bound by latency: a block waits for its entry, its words and its sums in turn (370
+// entries of up to 12,000 rows of 512: 11 us with 4,096 blocks, 21 with 512).
 __global__ void __launch_bounds__(256) embedding_join_kernel(SumArgs p) {
     constexpr int COLS = 64, WAYS = 16;  // columns of a block's pass, tiles side by side
     __shared__ double s_sum[WAYS][COLS];
