@@ -200,7 +200,9 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
                                              (__attribute__((address_space(3))) void*)(to + (WAVES * i + wave) * 64), 16, 0, 0);
     };
     // and its half row of codes: 16 bytes and their word each stage
-    const int crow = threadIdx.x >> 1, half = threadIdx.x & 1;
+    // (neighbouring threads take rows whose slots differ: their stores meet different banks)
+    const int ct = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const int crow = (ct & ~15) | (ct & 1) << 1 | (ct & 2) << 2 | (ct >> 2 & 1) | (ct >> 1 & 4);
     const uint8_t* const codes = p.w.codes + n0 * ldc;
     const uint32_t* const words = p.w.words + n0 * ldw;
     const uint32_t cn = (uint32_t)min((int64_t)crow, p.w.N - 1 - n0), coff = cn * (uint32_t)ldc + 16 * half, cw = cn * (uint32_t)ldw;
