@@ -148,11 +148,13 @@ __device__ __forceinline__ void store_tile(const float* sums, int pitch, const M
 // stage is 64 inputs in one of two LDS buffers: the rows of x are copied there
 // by the LDS-DMA loads, the codes pass through registers, where each thread
 // turns 32 of them into operands between the current stage's products.  4,096 cubed
-// in bf16 and groups of 128: 159 us with warm clocks, 144 in a program's calls (860 and
-// 960 TFLOP/s; the library's product of bf16 matrices reaches 1,210).  The matrix
-// cores are busy 37 % of the time and the vector units, with conversions and the
-// sums' changes of unit, 46 %: what does not overlap is the distance.  About 20 us
-// are a tile's start and its stores, with one tile a CU.
+// in bf16 and groups of 128: 157 us of normally distributed rows, 144 of those of the
+// cases (875 and 960 TFLOP/s; the library's product of bf16 matrices reaches 1,210).
+// The matrix cores are busy 38 % of the time and the vector units, with conversions
+// and the sums' changes of unit, 39 %: what does not overlap is the distance.  About
+// 20 us are a tile's start and its stores, with one tile a CU.  Waves that raise their
+// priority for the matrix instructions take 166, operands made before or in fixed turn
+// with them no less.
 template <typename V, typename T, int G, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
     typedef typename Elem<V>::vec vec;
