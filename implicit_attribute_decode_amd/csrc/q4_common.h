@@ -92,7 +92,8 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p, int64_t count) {
     return r;
 }
 
-// The operand's parts, largest first.
+// The operand's parts, largest first: cut off, so that they add up to the value (to
+// within 2^-133, where bf16 ends).
 __device__ __forceinline__ void split(const Raw<_Float16>& r, halfx8 (&p)[1]) { __builtin_memcpy(&p[0], &r, sizeof(r)); }
 __device__ __forceinline__ void split(const Raw<__bf16>& r, bfloatx8 (&p)[1]) { __builtin_memcpy(&p[0], &r, sizeof(r)); }
 __device__ __forceinline__ void split(const Raw<float>& r, bfloatx8 (&p)[3]) {

@@ -58,6 +58,13 @@ __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
     return other ? 1.0f : e ? m : small;
 }
 
+// m / m'.  Where it passes fp32's range (fp16 only), a sum of zero stays zero, and
+// any other is infinite, as its product with such a scale is in fp16.
+__device__ __forceinline__ float ratio(float m, float next) {
+    const float f = m / next;
+    return fabsf(f) == __builtin_huge_valf() ? copysignf(3.402823466e+38f, f) : f;
+}
+
 // What a group's word does to its codes; operands are u (q - z).
 template <typename V>
 struct Group;
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
                 if ((kStage * s + 16 * k) % G == 0) {
 #pragma unroll
                     for (int j = 0; j < TJ; ++j) {
-                        const float u = unit_of<V>(word[j][16 * k / G]), f = unit[j] / u;
+                        const float u = unit_of<V>(word[j][16 * k / G]), f = ratio(unit[j], u);
                         unit[j] = u;
 #pragma unroll
                         for (int i = 0; i < TI; ++i)

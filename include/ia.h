@@ -758,7 +758,8 @@ IA_API ia_status ia_mx4_linear_backward(const void* dy, int64_t lddy, const void
 /* Tables of codes (embeddings) and dropout                                  */
 /* ------------------------------------------------------------------------ */
 
-/* Dropout with probability p.  Nothing is stored: value (r, c) of a matrix is
+/* Dropout with probability p (a host struct, read before the call returns).
+ * Nothing is stored: value (r, c) of a matrix is
  * kept where word c mod 4 of Philox4x32-10 (Salmon, Moraes, Dror & Shaw,
  * "Parallel random numbers: as easy as 1, 2, 3", 2011) of the counter
  * (c / 4, r, low half of o, high half of o) and the key (low half, high half of
@@ -859,8 +860,9 @@ IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_
 /* A linear layer with such weights and its input as it is: y = act(x w^T +
  * bias), x [M][K] of dtype (rows ldx apart, 0 repeats one row), w [N][K], y
  * [M][N] of dtype (rows ldy apart).  Any M from one row (serving) up.  A group's
- * products are summed in fp32 (those of fp32 rows exactly taken apart), scaled in
- * fp32 and added in fp32, rounded once, in a fixed order.  bias: device fp32 [N]
+ * products are summed in fp32 (fp32 inputs taken apart into three bf16 numbers
+ * that add up to them, to within bf16's least value, 2^-133), scaled in fp32 and
+ * added in fp32, rounded once, in a fixed order.  Scales are finite or NaN.  bias: device fp32 [N]
  * or NULL; act: IA_ACT_NONE or IA_ACT_RELU.  K = 0 gives act(bias).  y must not
  * overlap an input, nor ws (ia_q4_linear_workspace_size bytes, 256-byte aligned,
  * may be NULL when that is 0) anything.  M, N, K < 2^31.

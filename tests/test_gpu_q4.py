@@ -52,6 +52,10 @@ def _assert_linear(y, x, w, bias=None, relu=False):
         want = np.maximum(want, 0)
     K = x.shape[1] * (3 if y.dtype == torch.float32 else 1)
     tol = (K + K // 32 + 4) * 2.0 ** -24 * size + UNIT[y.dtype] * np.abs(want) * (1 + 2.0 ** -10) + TINY[y.dtype]
+    if y.dtype == torch.float32:
+        # The parts of a value are cut off where bf16 ends: its numbers below 2^-125 lie 2^-133 apart, so what three parts of
+        # v leave out is below 2^-133 (nothing where v's last place, 2^-23 |v| or less, is 2^-133 or more).
+        tol = tol + 2.0 ** -133 * np.abs(w).sum(1)
     g = _f64(y)
     assert g.shape == want.shape and (np.abs(g - want) <= tol).all(), float((np.abs(g - want) / tol).max())
 
@@ -280,6 +284,30 @@ def test_scales_of_any_size_and_sign(M, N, dtype):
     _assert_linear(q4_linear(x, w)[-100:], _f64(x)[-100:], v)
     x[:, :64 * 5] = 0  # small terms alone
     _assert_linear(q4_linear(x, w)[-100:], _f64(x)[-100:], v)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N", [(3, 40), (2100, 1100)])
+def test_huge_scales_over_zero_inputs(M, N, dtype):
+    """Groups of weights near 1e30 whose inputs are all zero leave the sums of the others, small ones, as they are."""
+    rng = np.random.default_rng(M)
+    scales = rng.normal(size=(N, 9)) * 0.01
+    scales[:, 0], scales[:, 4] = 1e30, -1e30
+    scales[5, 1:] *= 1e-20
+    codes = torch.as_tensor(rng.integers(0, 256, (N, 9 * 32)).astype(np.uint8), device="cuda")
+    w = Q4Tensor.from_parts(codes, cuda(scales.astype(np.float32)), 7, 9 * 64, 64)
+    x = _matrix(rng, M, 9 * 64, dtype)
+    x[:, :64] = x[:, 256:320] = 0
+    _assert_linear(q4_linear(x, w)[-100:], _f64(x)[-100:], _values(w))
+
+
+@pytest.mark.parametrize("M,N", [(4, 50), (2100, 1100)])
+def test_fp32_rows_near_the_least_values(M, N):
+    """Rows of 2^-120 and less: their parts are subnormal, and count down to bf16's least value."""
+    rng = np.random.default_rng(N)
+    w = q4_quantize(_matrix(rng, N, 512, scale=2.0 ** 40), 64)
+    x = _matrix(rng, M, 512) * 2.0 ** -122
+    _assert_linear(q4_linear(x, w)[-60:], _f64(x)[-60:], _values(w))
 
 
 def test_empty_products():
