@@ -165,8 +165,8 @@ hipError_t for_rows(const Q4View& q, const Fn& launch) {
 // ------------------------------------------------------------ product
 
 // Eight values of a row of x as matrix operands.  fp32 goes as three bf16 parts
-// of 8 bits each, cut off and not rounded, so that they add up to the value
-// exactly (a value that is not finite is its first part alone).
+// of 8 bits each, cut off and not rounded, so that they add up to the value (to
+// within 2^-133, bf16's least; a value that is not finite is its first part alone).
 template <typename T>
 struct Operand;
 template <>

@@ -11,9 +11,12 @@
 //   bf16: u = the power of two of s, so 1 <= |m| < 2 and nothing grows.
 //   fp16: u = 1 and m = s, which fp16's range needs.  A group with |s| under
 //   2^-80 counts as zero: with 2^31 inputs of at most 2^16 it adds less than
-//   2^-29, under half of fp16's smallest value.
+//   2^-29, under half of fp16's smallest value.  One with |s| over 2^46 counts as
+//   2^46: fp16 inputs are at least 2^-24, so what it adds is 0 or at least 2^22,
+//   past fp16's range.  So m / m' is a normal fp32 number.
 //   fp32 rows go as three bf16 parts of 8 bits each, cut off and not rounded,
-//   which add up to them exactly, one part after the other.
+//   which add up to them (to within 2^-133, where bf16 ends), one part after the
+//   other.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -48,7 +51,8 @@ template <typename V>
 __device__ __forceinline__ float unit_of(uint32_t word);
 template <>
 __device__ __forceinline__ float unit_of<_Float16>(uint32_t word) {
-    return fabsf(scale_of(word)) < 0x1p-80f ? 0x1p-80f : scale_of(word);
+    const float s = scale_of(word), size = fabsf(s);
+    return size < 0x1p-80f ? 0x1p-80f : size > 0x1p46f ? copysignf(0x1p46f, s) : s;
 }
 template <>
 __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
@@ -56,13 +60,6 @@ __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
     const bool other = e == 0x7f800000u || (word & 0x7fffff00u) == 0;  // not finite, or zero
     const float m = __builtin_bit_cast(float, (word & 0x807fff00u) | 0x3f800000u), small = scale_of(word) * 0x1p126f;
     return other ? 1.0f : e ? m : small;
-}
-
-// m / m'.  Where it passes fp32's range (fp16 only), a sum of zero stays zero, and
-// any other is infinite, as its product with such a scale is in fp16.
-__device__ __forceinline__ float ratio(float m, float next) {
-    const float f = m / next;
-    return fabsf(f) == __builtin_huge_valf() ? copysignf(3.402823466e+38f, f) : f;
 }
 
 // What a group's word does to its codes; operands are u (q - z).
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(64 * WM * WN) q4_matmul_kernel(ManyArgs p) {
                 if ((kStage * s + 16 * k) % G == 0) {
 #pragma unroll
                     for (int j = 0; j < TJ; ++j) {
-                        const float u = unit_of<V>(word[j][16 * k / G]), f = ratio(unit[j], u);
+                        const float u = unit_of<V>(word[j][16 * k / G]), f = unit[j] / u;
                         unit[j] = u;
 #pragma unroll
                         for (int i = 0; i < TI; ++i)

@@ -301,6 +301,25 @@ def test_huge_scales_over_zero_inputs(M, N, dtype):
     _assert_linear(q4_linear(x, w)[-100:], _f64(x)[-100:], _values(w))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N", [(3, 40), (2100, 1100)])
+def test_the_largest_scales(M, N, dtype):
+    """Scales near 2^123 between those of a thousandth: over zero inputs they change nothing, over others they rule."""
+    rng = np.random.default_rng(N)
+    scales = rng.normal(size=(N, 9)) * 0.001
+    scales[:, 3], scales[:, 7] = 1e37, 1e37
+    codes = torch.as_tensor(rng.integers(0, 256, (N, 9 * 32)).astype(np.uint8), device="cuda")
+    w = Q4Tensor.from_parts(codes, cuda(scales.astype(np.float32)), 0, 9 * 64, 64)
+    x = _matrix(rng, M, 9 * 64, dtype)
+    x[:, 192:256] = x[:, 448:512] = 0
+    _assert_linear(q4_linear(x, w)[-100:], _f64(x)[-100:], _values(w))
+    if dtype == torch.float16:  # every row of codes has one above zero there, so every sum passes fp16's range
+        x[:, 192:256] = x[:, 448:512] = 2.0 ** -24
+        x[M // 2:, 192:256] = x[M // 2:, 448:512] = -2.0 ** -24
+        y = q4_linear(x, w)
+        assert (y[:M // 2] == float("inf")).all() and (y[M // 2:] == float("-inf")).all()
+
+
 @pytest.mark.parametrize("M,N", [(4, 50), (2100, 1100)])
 def test_fp32_rows_near_the_least_values(M, N):
     """Rows of 2^-120 and less: their parts are subnormal, and count down to bf16's least value."""
