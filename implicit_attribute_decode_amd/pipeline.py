@@ -915,9 +915,11 @@ class Dropout:
     each step takes an offset of its own, and the backward that of its forward.
 
     step: a device int64 tensor of one element that is added to offset when the
-    work runs (not when it is enqueued), for captured graphs that are replayed."""
+    work runs (not when it is enqueued), for captured graphs that are replayed.
 
-    __slots__ = ("p", "seed", "offset", "_step", "c")
+    None of the four can be assigned: another p or offset is another Dropout."""
+
+    __slots__ = ("_step", "c")
 
     def __init__(self, p: float, seed: int, offset: int = 0, step: torch.Tensor | None = None):
         if not 0.0 <= p <= 1.0:
@@ -926,9 +928,12 @@ class Dropout:
             raise ValueError("seed and offset must be in [0, 2^64)")
         if step is not None and (step.dtype != torch.int64 or step.numel() != 1 or not step.is_cuda):
             raise ValueError("step must be an int64 tensor of one element on the GPU")
-        self.p, self.seed, self.offset, self._step = p, seed, offset, step
-        self.c = ia.Drop(p, seed, offset, None if step is None else step.data_ptr())
+        self._step, self.c = step, ia.Drop(p, seed, offset, None if step is None else step.data_ptr())
 
+    # what the kernels read
+    p = property(lambda self: self.c.p)
+    seed = property(lambda self: self.c.seed)
+    offset = property(lambda self: self.c.offset)
     step = property(lambda self: self._step)
 
     def __call__(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
