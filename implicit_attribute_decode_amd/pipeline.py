@@ -1020,9 +1020,9 @@ class Q4Tensor:
     uint8 [rows, groups * group / 2] (two a byte, the earlier one in the low
     half), words int32 [rows, groups rounded up to 4] (the bits of the scale as a
     float32 whose lowest byte is zero, and in that byte the zero, 0..15).  The
-    tensors are not replaced; their values may change (quantised anew)."""
+    tensors and sizes are not replaced; the tensors' values may change (quantised anew)."""
 
-    __slots__ = ("_codes", "_words", "rows", "cols", "group", "c")
+    __slots__ = ("_codes", "_words", "c")
 
     def __init__(self, codes: torch.Tensor, words: torch.Tensor, cols: int, group: int):
         shapes = self._shapes(codes.shape[0], cols, group)
@@ -1041,11 +1041,14 @@ class Q4Tensor:
         return (rows, groups * group // 2), (rows, (groups + 3) // 4 * 4)
 
     def _set(self, codes, words, cols, group):
-        self._codes, self._words, self.rows, self.cols, self.group = codes, words, codes.shape[0], cols, group
-        self.c = ia.q4(codes, words, self.rows, cols, group)
+        self._codes, self._words, self.c = codes, words, ia.q4(codes, words, codes.shape[0], cols, group)
 
     codes = property(lambda self: self._codes)
     words = property(lambda self: self._words)
+    # what the kernels read
+    rows = property(lambda self: self.c.rows)
+    cols = property(lambda self: self.c.cols)
+    group = property(lambda self: self.c.group)
 
     @classmethod
     def empty(cls, rows: int, cols: int, group: int = 128, device="cuda"):

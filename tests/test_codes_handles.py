@@ -13,3 +13,12 @@ def test_dropouts_are_not_changed_by_assignment(name, value):
         setattr(d, name, value)
     assert (d.p, d.seed, d.offset, d.step) == (0.5, 2 ** 64 - 1, 2 ** 40, None)
     assert (d.c.p, d.c.seed, d.c.offset, d.c.step) == (0.5, 2 ** 64 - 1, 2 ** 40, None)
+
+
+@pytest.mark.parametrize("name,value", [("rows", 2), ("cols", 64), ("group", 64), ("codes", None), ("words", None)])
+def test_4_bit_tensors_are_not_changed_by_assignment(name, value):
+    q = pipeline.Q4Tensor.empty(3, 100, 32, device="cpu")
+    with pytest.raises(AttributeError):
+        setattr(q, name, value)
+    assert (q.rows, q.cols, q.group) == (q.c.rows, q.c.cols, q.c.group) == (3, 100, 32)
+    assert q.codes.shape == (3, 64) and q.words.shape == (3, 4)
