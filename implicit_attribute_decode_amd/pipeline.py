@@ -750,9 +750,9 @@ class Mx4Tensor:
     """A [rows, cols] matrix in MXFP4: codes uint8 [rows, 16 ceil(cols / 32)]
     (two E2M1 codes a byte, the earlier value in the low half), scales uint8
     [rows, ceil(cols / 32)] (2^(byte - 127), 255 = NaN).  The tensors are not
-    replaced; their values may change (quantised anew)."""
+    replaced, nor are the sizes; their values may change (quantised anew)."""
 
-    __slots__ = ("_codes", "_scales", "rows", "cols", "c")
+    __slots__ = ("_codes", "_scales", "c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         blocks = (cols + 31) // 32
@@ -763,11 +763,13 @@ class Mx4Tensor:
         if (codes.shape != (rows, 16 * blocks) or scales.shape != (rows, blocks)
                 or not codes.is_contiguous() or not scales.is_contiguous()):
             raise ValueError(f"codes [{rows}, {16 * blocks}] and scales [{rows}, {blocks}] expected, contiguous")
-        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
-        self.c = ia.mx4(codes, scales, rows, cols)
+        self._codes, self._scales, self.c = codes, scales, ia.mx4(codes, scales, rows, cols)
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
+    # what the kernels read
+    rows = property(lambda self: self.c.rows)
+    cols = property(lambda self: self.c.cols)
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):

@@ -1,4 +1,4 @@
-"""Dropouts and 4-bit tensors say what the kernels read: what is described to
+"""Dropouts and tensors in 4 bits say what the kernels read: what is described to
 them once cannot be assigned afterwards."""
 import pytest
 import torch
@@ -22,3 +22,12 @@ def test_4_bit_tensors_are_not_changed_by_assignment(name, value):
         setattr(q, name, value)
     assert (q.rows, q.cols, q.group) == (q.c.rows, q.c.cols, q.c.group) == (3, 100, 32)
     assert q.codes.shape == (3, 64) and q.words.shape == (3, 4)
+
+
+@pytest.mark.parametrize("name,value", [("rows", 2), ("cols", 64), ("codes", None), ("scales", None)])
+def test_mxfp4_tensors_are_not_changed_by_assignment(name, value, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    q = pipeline.Mx4Tensor.empty(3, 100, device="cpu")
+    with pytest.raises(AttributeError):
+        setattr(q, name, value)
+    assert (q.rows, q.cols) == (q.c.rows, q.c.cols) == (3, 100)
