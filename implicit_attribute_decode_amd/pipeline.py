@@ -1066,11 +1066,17 @@ class Q4Tensor:
         to 16 significant bits, so exact for float16 and bfloat16) and of zeros in
         0..15 (or one zero for all).  Looks at the zeros on the host: it waits for
         the GPU."""
+        (rows, _), _ = cls._shapes(codes.shape[0], cols, group)
+        shape = (rows, (cols + group - 1) // group)
+        if scales.shape != shape:  # the constructor sees the padded words only
+            raise ValueError(f"scales {list(shape)} expected, got {list(scales.shape)}")
         bits = scales.to(torch.float32).contiguous().view(torch.int32)
         bits = torch.where(torch.isfinite(scales), bits + 127 + ((bits >> 8) & 1), bits) & ~255
         zeros = torch.as_tensor(zeros, device=scales.device)
         if zeros.dtype.is_floating_point or bool(((zeros < 0) | (zeros > 15)).any()):
             raise ValueError("zeros must be whole numbers in 0..15")
+        if any(z not in (1, n) for z, n in zip(zeros.shape[::-1], shape[::-1])) or zeros.dim() > 2:
+            raise ValueError(f"zeros {list(shape)} or one for all expected, got {list(zeros.shape)}")
         words = bits | zeros.to(torch.int32)
         return cls(codes, torch.nn.functional.pad(words, (0, -words.shape[1] % 4)).contiguous(), cols, group)
 

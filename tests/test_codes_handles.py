@@ -31,3 +31,35 @@ def test_mxfp4_tensors_are_not_changed_by_assignment(name, value, monkeypatch):
     with pytest.raises(AttributeError):
         setattr(q, name, value)
     assert (q.rows, q.cols) == (q.c.rows, q.c.cols) == (3, 100)
+
+
+@pytest.fixture
+def parts(monkeypatch):
+    """from_parts on the CPU: (words, cols) of what it would make."""
+    monkeypatch.setattr(pipeline.Q4Tensor, "__init__", lambda self, codes, words, cols, group: self._set(codes, words, cols, group))
+
+    def call(scales, zeros, cols, group, rows=3):
+        codes = torch.zeros((rows, -(-cols // group) * group // 2), dtype=torch.uint8)
+        return pipeline.Q4Tensor.from_parts(codes, scales, zeros, cols, group)
+    return call
+
+
+@pytest.mark.parametrize("shape", [(3, 1), (3, 5), (3, 6), (3, 8), (3,), (7,), (2, 7), (1, 7), (3, 7, 1), ()])
+def test_scales_of_other_shapes_are_refused(parts, shape):
+    """7 groups are padded to 8 words: 5, 6 or 8 scales a row would pad to as many."""
+    with pytest.raises(ValueError, match="scales"):
+        parts(torch.ones(shape), 7, 200, 32)
+
+
+@pytest.mark.parametrize("shape", [(3, 6), (2, 7), (3,), (1, 3, 7), (8,)])
+def test_zeros_of_other_shapes_are_refused(parts, shape):
+    with pytest.raises(ValueError, match="zeros"):
+        parts(torch.ones((3, 7)), torch.zeros(shape, dtype=torch.int32), 200, 32)
+
+
+@pytest.mark.parametrize("zeros", [9, torch.tensor(9), torch.tensor([9]), torch.full((7,), 9), torch.full((3, 1), 9),
+                                   torch.full((3, 7), 9, dtype=torch.uint8)])
+def test_words_of_scales_and_zeros(parts, zeros):
+    q = parts(torch.full((3, 7), 0.5, dtype=torch.float16), zeros, 200, 32)
+    assert q.words.shape == (3, 8) and (q.words[:, 7] == 0).all()
+    assert q.scales.shape == q.zeros.shape == (3, 7) and (q.scales == 0.5).all() and (q.zeros == 9).all()
