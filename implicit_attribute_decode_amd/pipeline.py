@@ -1062,16 +1062,18 @@ class Q4Tensor:
 
     @classmethod
     def from_parts(cls, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | int, cols: int, group: int):
-        """From codes and [rows, groups] tensors of scales (finite or NaN; rounded
-        to 16 significant bits, so exact for float16 and bfloat16) and of zeros in
-        0..15 (or one zero for all).  Looks at the zeros on the host: it waits for
-        the GPU."""
+        """From codes and [rows, groups] tensors of scales (NaN or, rounded to 16
+        significant bits, finite floats, so exact for float16 and bfloat16) and of
+        zeros in 0..15 (or one zero for all).  Looks at both on the host: it waits
+        for the GPU."""
         (rows, _), _ = cls._shapes(codes.shape[0], cols, group)
         shape = (rows, (cols + group - 1) // group)
         if scales.shape != shape:  # the constructor sees the padded words only
             raise ValueError(f"scales {list(shape)} expected, got {list(scales.shape)}")
         bits = scales.to(torch.float32).contiguous().view(torch.int32)
-        bits = torch.where(torch.isfinite(scales), bits + 127 + ((bits >> 8) & 1), bits) & ~255
+        bits = torch.where(torch.isnan(scales), 0x7fc00000, (bits + 127 + ((bits >> 8) & 1)) & ~255)
+        if bool(torch.isinf(bits.view(torch.float32)).any()):
+            raise ValueError("scales must be NaN or finite as floats of 16 significant bits")
         zeros = torch.as_tensor(zeros, device=scales.device)
         if zeros.dtype.is_floating_point or bool(((zeros < 0) | (zeros > 15)).any()):
             raise ValueError("zeros must be whole numbers in 0..15")

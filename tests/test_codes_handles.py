@@ -63,3 +63,24 @@ def test_words_of_scales_and_zeros(parts, zeros):
     q = parts(torch.full((3, 7), 0.5, dtype=torch.float16), zeros, 200, 32)
     assert q.words.shape == (3, 8) and (q.words[:, 7] == 0).all()
     assert q.scales.shape == q.zeros.shape == (3, 7) and (q.scales == 0.5).all() and (q.zeros == 9).all()
+
+
+@pytest.mark.parametrize("scale", [float("inf"), -float("inf"), torch.finfo(torch.float32).max, torch.finfo(torch.float32).min,
+                                   1e300])
+def test_scales_that_are_no_finite_floats_are_refused(parts, scale):
+    """Infinite, or so once rounded to a float of 16 significant bits."""
+    with pytest.raises(ValueError, match="scales"):
+        parts(torch.tensor([[1.0], [2.0], [scale]], dtype=torch.float64), 8, 32, 32)
+
+
+def test_scales_that_are_kept(parts):
+    """NaN whatever its payload, the largest float of 16 bits, ties to even, the least ones, zero of either sign."""
+    odd = torch.tensor([0x7F800001, -0x800000 + 1, 0x7F8000FF, 0x7FFFFFFF, -1], dtype=torch.int32).view(torch.float32)
+    assert torch.isnan(odd).all()
+    q = parts(odd.view(-1, 1), 3, 32, 32, rows=5)
+    assert torch.isnan(q.scales).all() and (q.zeros == 3).all()
+    top = 2.0 ** 128 - 2.0 ** 112
+    given = torch.tensor([top, -top, 1 + 2.0 ** -16, 1 + 3 * 2.0 ** -16, 2.0 ** -141, 0.0, -0.0])
+    want = torch.tensor([top, -top, 1.0, 1 + 2.0 ** -14, 2.0 ** -141, 0.0, -0.0])
+    q = parts(given.view(-1, 1), 0, 32, 32, rows=7)
+    assert torch.equal(q.scales[:, 0].view(torch.int32), want.view(torch.int32))
