@@ -185,6 +185,31 @@ struct Operand<float> {
     static constexpr int kParts = 3;
 };
 
+// What a group's word does to its codes: operands are the codes less their zero, and
+// the sum of a group is scaled.  Inputs in bf16 and fp32 reach the end of fp32's range,
+// which their sums would pass where the scale brings the result back: their operands
+// are 2^-11 times that, so that 128 terms of less than 2^132 stay below 2^128, and the
+// scale 2^11 times as large (not one past 2^64, where the result is out of range as well).
+template <typename V>
+struct Group;
+template <>
+struct Group<halfx8> {
+    float z, scale;
+    __device__ __forceinline__ explicit Group(uint32_t word) : z(zero_of(word)), scale(scale_of(word)) {}
+    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes, z); }
+};
+template <>
+struct Group<bfloatx8> {
+    float u, zu, scale;
+    __device__ __forceinline__ explicit Group(uint32_t word) {
+        const bool past = fabsf(scale_of(word)) >= 0x1p64f;
+        u = past ? 1.0f : 0x1p-11f;
+        zu = -zero_of(word) * u;
+        scale = scale_of(word) * (past ? 1.0f : 0x1p11f);
+    }
+    __device__ __forceinline__ bfloatx8 operand(uint32_t codes) const { return codes_times(codes, u, zu); }
+};
+
 __device__ __forceinline__ floatx4 mfma(halfx8 a, halfx8 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -247,16 +272,16 @@ __device__ __forceinline__ void multiply(const uintx4 (&codes)[NT], const uint32
         if (!kWhole<T, MT> && i < 3) get(x, i + 1);
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const vec b = codes_less(code[u][i], zero_of(words[u][g]), vec());
+            const Group<vec> group(words[u][g]);
+            const vec b = group.operand(code[u][i]);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 if (first) part[t][u] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int h = 0; h < PARTS; ++h) part[t][u] = mfma(a[t][h], b, part[t][u]);
                 if (last) {
-                    const float f = scale_of(words[u][g]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[t][u][j] = __builtin_fmaf(f, part[t][u][j], acc[t][u][j]);
+                    for (int j = 0; j < 4; ++j) acc[t][u][j] = __builtin_fmaf(group.scale, part[t][u][j], acc[t][u][j]);
                 }
             }
         }

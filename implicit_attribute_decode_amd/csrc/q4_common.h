@@ -44,7 +44,7 @@ struct Nibbles {
 };
 
 // q - z of eight codes (exact: whole numbers of at most 15).
-__device__ __forceinline__ halfx8 codes_less(uint32_t u, float z, halfx8) {
+__device__ __forceinline__ halfx8 codes_less(uint32_t u, float z) {
     // e4m3's values of the bytes 0..15 are 0..15 times 2^-9: the scaled conversion reads them as whole numbers
     const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;
     const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u), hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
@@ -62,12 +62,14 @@ __device__ __forceinline__ halfx8 codes_less(uint32_t u, float z, halfx8) {
     }
     return r;
 }
-__device__ __forceinline__ bfloatx8 codes_less(uint32_t u, float z, bfloatx8) {
-    const Nibbles n(u);
+// u (q - z) of eight codes, u a power of two and zu = -z u (exact but for u under 2^-133).
+__device__ __forceinline__ bfloatx8 codes_times(uint32_t codes, float u, float zu) {
+    const Nibbles n(codes);
     bfloatx8 r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const bfloatx2 w = __builtin_convertvector((floatx2{n.value<0>(j) - z, n.value<1>(j) - z}), bfloatx2);
+        const floatx2 v = {__builtin_fmaf(n.value<0>(j), u, zu), __builtin_fmaf(n.value<1>(j), u, zu)};
+        const bfloatx2 w = __builtin_convertvector(v, bfloatx2);
         r[2 * j] = w[0];
         r[2 * j + 1] = w[1];
     }

@@ -74,7 +74,7 @@ struct Group<_Float16> {
         keep = none ? 0u : ~0u;
         z = none ? 0.0f : zero_of(word);
     }
-    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes & keep, z, halfx8()); }
+    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes & keep, z); }
 };
 template <>
 struct Group<__bf16> {
@@ -85,21 +85,7 @@ struct Group<__bf16> {
         u = __builtin_bit_cast(float, e == 0x7f800000u ? word & ~255u : e ? e : low);
         zu = -zero_of(word) * u;
     }
-    __device__ __forceinline__ bfloatx8 operand(uint32_t codes) const {
-        const Nibbles n(codes);
-        floatx2 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = floatx2{__builtin_fmaf(n.value<0>(j), u, zu), __builtin_fmaf(n.value<1>(j), u, zu)};
-        bfloatx8 r;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bfloatx2 w = __builtin_convertvector(v[j], bfloatx2);
-            r[2 * j] = w[0];
-            r[2 * j + 1] = w[1];
-        }
-        return r;
-    }
+    __device__ __forceinline__ bfloatx8 operand(uint32_t codes) const { return codes_times(codes, u, zu); }
 };
 
 // A pointer that is the same for all lanes, in scalar registers.

@@ -1,0 +1,75 @@
+"""Products with 4-bit weights at the ends of the types' ranges, the few rows' kernel and the tiles alike, against
+the fp64 oracle.  Tolerances: test_gpu_q4.py's, (K + groups + 3) 2^-24 of the sum of the terms' magnitudes (3 K
+terms where fp32 rows go in three parts) and half a step of the type."""
+import numpy as np
+import pytest
+import torch
+
+from implicit_attribute_decode_amd import ia
+from implicit_attribute_decode_amd.pipeline import _DTYPES, Q4Tensor, q4_linear
+
+from gpu_util import cuda, host
+from test_gpu_q4 import TYPES, _assert_linear, _f64, _matrix, _values, ids
+
+pytestmark = pytest.mark.gpu
+
+SIZES = [(1, 50), (17, 50), (40, 50), (5, 16400), (2100, 1100)]  # the last one in tiles
+GROUPS = 9
+
+
+def _weights(rng, N, scales, zeros=None, group=64):
+    codes = torch.as_tensor(rng.integers(0, 256, (N, GROUPS * group // 2)).astype(np.uint8), device="cuda")
+    zeros = cuda(rng.integers(0, 16, (N, GROUPS))) if zeros is None else zeros
+    return Q4Tensor.from_parts(codes, cuda(np.broadcast_to(scales, (N, GROUPS)).astype(np.float32)), zeros, GROUPS * group, group)
+
+
+def _takes_tiles(M, K, N, dtype):
+    return ia.ia_q4_linear_workspace_size(_DTYPES[dtype], M, K, N) > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=ids)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N", SIZES)
+def test_inputs_near_the_largest_float(M, N, group, dtype):
+    """Inputs of 3e38 against weights of a hundredth: a group's inputs times whole numbers pass fp32's range, its sum does
+    not (at most 0.15 (3 * 3e38 + 1152 * 1e36) = 3.1e38)."""
+    rng = np.random.default_rng(M + N)
+    w = _weights(rng, N, rng.uniform(0.001, 0.01, (N, GROUPS)) * np.sign(rng.normal(size=(N, GROUPS))), group=group)
+    x = torch.as_tensor(rng.uniform(-1, 1, (M, GROUPS * group)), device="cuda") * 1e36
+    x[:, 3], x[:, GROUPS * group // 2], x[:, -1] = 3e38, -3e38, 3e38
+    x = x.to(dtype)
+    assert M < 1000 or _takes_tiles(M, GROUPS * group, N, dtype)
+    y = q4_linear(x, w)
+    assert torch.isfinite(y).all()
+    _assert_linear(y[-60:], _f64(x)[-60:], _values(w))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=ids)
+@pytest.mark.parametrize("M,N", SIZES)
+@pytest.mark.parametrize("weights", [2.0 ** 40, 1.0])
+def test_inputs_near_the_least_float(M, N, weights, dtype):
+    """Inputs of 2^-122 and less down to subnormal ones."""
+    rng = np.random.default_rng(M + N)
+    w = _weights(rng, N, rng.uniform(0.1, 1, (N, GROUPS)) * weights)
+    x = (_matrix(rng, M, GROUPS * 64) * 2.0 ** -122).to(dtype)
+    x[:, :8] *= 2.0 ** -6
+    y, v, rows = q4_linear(x, w)[-60:], _values(w), _f64(x)[-60:]
+    if dtype == torch.float32:
+        _assert_linear(y, rows, v)
+    else:  # bf16 inputs are taken whole: what is below fp32's least value is lost, half of 2^-149 a term
+        want, size = rows @ v.T, np.abs(rows) @ np.abs(v).T
+        tol = (v.shape[1] + 22) * (2.0 ** -24 * size + 2.0 ** -150) + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -10) + 2.0 ** -134
+        assert (np.abs(_f64(y) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("M,N", SIZES)
+def test_scales_past_2_64(M, N):
+    """The largest scales over inputs of a size that keeps the results below fp32's end; zeros elsewhere."""
+    rng = np.random.default_rng(M + N)
+    scales = rng.uniform(0.5, 1, (N, GROUPS)) * 2.0 ** rng.integers(60, 124, (N, GROUPS))
+    w = _weights(rng, N, scales)
+    x = _matrix(rng, M, GROUPS * 64) * 2.0 ** -20
+    y = q4_linear(x, w)
+    assert torch.isfinite(y).all()
+    _assert_linear(y[-60:], _f64(x)[-60:], _values(w))
+    assert (q4_linear(torch.zeros_like(x), w) == 0).all()
