@@ -194,9 +194,10 @@ template <typename V>
 struct Group;
 template <>
 struct Group<halfx8> {
-    float z, scale;
-    __device__ __forceinline__ explicit Group(uint32_t word) : z(zero_of(word)), scale(scale_of(word)) {}
-    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes, z); }
+    halfx2 zu;
+    float scale;
+    __device__ __forceinline__ explicit Group(uint32_t word) : zu(twice(-zero_of(word))), scale(scale_of(word)) {}
+    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_times(codes, 512.0f, zu); }
 };
 template <>
 struct Group<bfloatx8> {

@@ -43,25 +43,24 @@ struct Nibbles {
     }
 };
 
-// q - z of eight codes (exact: whole numbers of at most 15).
-__device__ __forceinline__ halfx8 codes_less(uint32_t u, float z) {
+// u (q - z) of eight codes, u a power of two from 2^-24 to 2^8, given as 512 u, and
+// zu = -z u twice: exact in fp16, which ends at 2^-24 and 2^16.
+__device__ __forceinline__ halfx8 codes_times(uint32_t codes, float u512, halfx2 zu) {
     // e4m3's values of the bytes 0..15 are 0..15 times 2^-9: the scaled conversion reads them as whole numbers
-    const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;
+    const uint32_t even = codes & 0x0f0f0f0fu, odd = (codes >> 4) & 0x0f0f0f0fu;
     const int lo = (int)__builtin_amdgcn_perm(odd, even, 0x05010400u), hi = (int)__builtin_amdgcn_perm(odd, even, 0x07030602u);
-    const halfx2 zz = {(_Float16)z, (_Float16)z};
-    halfx2 h[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false),
-                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true),
-                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false),
-                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true)};
+    halfx2 h[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, u512, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, u512, true),
+                   __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, u512, false), __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, u512, true)};
     halfx8 r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        h[j] -= zz;
+        h[j] += zu;
         r[2 * j] = h[j][0];
         r[2 * j + 1] = h[j][1];
     }
     return r;
 }
+__device__ __forceinline__ halfx2 twice(float v) { return halfx2{(_Float16)v, (_Float16)v}; }
 // u (q - z) of eight codes, u a power of two and zu = -z u (exact but for u under 2^-133).
 __device__ __forceinline__ bfloatx8 codes_times(uint32_t codes, float u, float zu) {
     const Nibbles n(codes);

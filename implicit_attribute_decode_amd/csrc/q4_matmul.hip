@@ -9,11 +9,14 @@
 // its weight row's current m: where a group ends it is multiplied by m / m', m'
 // being the next group's, and at the end by the last m.
 //   bf16: u = the power of two of s, so 1 <= |m| < 2 and nothing grows.
-//   fp16: u = 1 and m = s, which fp16's range needs.  A group with |s| under
-//   2^-80 counts as zero: with 2^31 inputs of at most 2^16 it adds less than
-//   2^-29, under half of fp16's smallest value.  One with |s| over 2^46 counts as
-//   2^46: fp16 inputs are at least 2^-24, so what it adds is 0 or at least 2^22,
-//   past fp16's range.  So m / m' is a normal fp32 number.
+//   fp16: the same from 2^-24 to 2^8, where u (q - z) is a number of fp16; u ends
+//   there, and m goes on below 1 and above 2.  A group with |s| under 2^-66 counts as
+//   zero: with the 2^20 inputs of less than 2^16 that tiles take it adds less than
+//   2^-26, under half of fp16's least value.  Powers of two in s past 2^45 count as
+//   2^45: fp16 inputs are at least 2^-24, so what such a group adds is 0 or at least
+//   2^21, past fp16's range.  A sum, of 2^20 terms of at most 15 * 2^46 * 65504, is
+//   below 2^86 then and in units of m, 2^-42 or more, below 2^128: a change of unit
+//   never makes it infinite.
 //   fp32 rows go as three bf16 parts of 8 bits each, cut off and not rounded,
 //   which add up to them (to within 2^-133, where bf16 ends), one part after the
 //   other.
@@ -46,13 +49,19 @@ __device__ __forceinline__ floatx16 mfma(bfloatx8 a, bfloatx8 b, floatx16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// The power of two in a scale, as bits, held between two powers.
+__device__ __forceinline__ uint32_t power_of(uint32_t word, int least, int most) {
+    return min(max(word & 0x7f800000u, (uint32_t)(127 + least) << 23), (uint32_t)(127 + most) << 23);
+}
+// A group's u in fp16, as bits.
+__device__ __forceinline__ uint32_t half_unit(uint32_t word) { return power_of(word, -24, 8); }
+
 // A group's m.
 template <typename V>
 __device__ __forceinline__ float unit_of(uint32_t word);
 template <>
 __device__ __forceinline__ float unit_of<_Float16>(uint32_t word) {
-    const float s = scale_of(word), size = fabsf(s);
-    return size < 0x1p-80f ? 0x1p-80f : size > 0x1p46f ? copysignf(0x1p46f, s) : s;
+    return __builtin_bit_cast(float, (word & 0x807fff00u) | (power_of(word, -66, 45) - half_unit(word) + 0x3f800000u));
 }
 template <>
 __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
@@ -67,14 +76,16 @@ template <typename V>
 struct Group;
 template <>
 struct Group<_Float16> {
-    uint32_t keep;
-    float z;
+    float u512;
+    halfx2 zu;
     __device__ __forceinline__ explicit Group(uint32_t word) {
-        const bool none = fabsf(scale_of(word)) < 0x1p-80f;
-        keep = none ? 0u : ~0u;
-        z = none ? 0.0f : zero_of(word);
+        const uint32_t e = word & 0x7f800000u;
+        // a scale that is not finite goes into the operand as it is; codes times 2^-118 are zero in fp16
+        const uint32_t u = e == 0x7f800000u ? word & ~255u : e < (127u - 66) << 23 ? 0u : half_unit(word);
+        u512 = __builtin_bit_cast(float, u + (9u << 23));
+        zu = twice(-zero_of(word) * __builtin_bit_cast(float, u));
     }
-    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_less(codes & keep, z); }
+    __device__ __forceinline__ halfx8 operand(uint32_t codes) const { return codes_times(codes, u512, zu); }
 };
 template <>
 struct Group<__bf16> {
@@ -378,6 +389,8 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
 //     cubed: 163, in tiles of 128 226)
 //   joining splits: 3 and 8 bytes a sum at 4 TB/s (128 x 4,096 -> 4,096 in four
 //     splits: 28, in one 59).
+int parts_of(int32_t dtype) { return dtype == IA_DTYPE_F32 ? 3 : 1; }
+
 enum Way { kFew, kSmall, kLarge };
 struct Plan {
     Way way;
@@ -385,11 +398,13 @@ struct Plan {
     int64_t per_split;
 };
 
-Plan plan_of(int parts, int group, int64_t M, int64_t K, int64_t N) {
+Plan plan_of(int32_t dtype, int group, int64_t M, int64_t K, int64_t N) {
+    const int parts = parts_of(dtype);
     const int64_t pairs = ceil_div(K, 128) * parts;
     const auto tiles = [&](int64_t m, int64_t n) { return (double)(ceil_div(M, m) * ceil_div(N, n)); };
     Plan best{kFew, 1, pairs};
-    if (M <= 16 || K >= (int64_t)1 << 22) return best;  // a tile's offsets have 32 bits
+    // a tile's offsets have 32 bits, fp16 sums 2^20 terms
+    if (M <= 16 || K >= (int64_t)1 << (dtype == IA_DTYPE_F16 ? 20 : 22)) return best;
     double least = 2.5 + std::max(0.8, tiles(64, 16) / 256) * std::max(1.75, (parts > 1 ? 32.6 : 16.3) * (double)K / 4096);
     const auto offer = [&](Way way, int64_t splits, double blocks) {
         const int64_t per = ceil_div(pairs, splits);
@@ -459,25 +474,24 @@ hipError_t launch_matmul(const void* x, int64_t M, int64_t ldx, int group, const
     typedef std::conditional_t<std::is_same<T, _Float16>::value, _Float16, __bf16> V;
     constexpr int PARTS = std::is_same<T, float>::value ? 3 : 1;
     const T* const t = (const T*)x;
-    const Plan plan = plan_of(PARTS, group, M, w.K, w.N);
+    constexpr int32_t DTYPE = PARTS > 1 ? IA_DTYPE_F32 : std::is_same<T, _Float16>::value ? IA_DTYPE_F16 : IA_DTYPE_BF16;
+    const Plan plan = plan_of(DTYPE, group, M, w.K, w.N);
     return group == 32   ? matmul<V, T, PARTS, 32>(plan, t, M, ldx, w, ws, s)
            : group == 64 ? matmul<V, T, PARTS, 64>(plan, t, M, ldx, w, ws, s)
                          : matmul<V, T, PARTS, 128>(plan, t, M, ldx, w, ws, s);
 }
 
-int parts_of(int32_t dtype) { return dtype == IA_DTYPE_F32 ? 3 : 1; }
-
 }  // namespace
 
 bool q4_takes_tiles(int32_t dtype, int group, int64_t M, int64_t K, int64_t N) {
-    return K > 0 && plan_of(parts_of(dtype), group, M, K, N).way != kFew;
+    return K > 0 && plan_of(dtype, group, M, K, N).way != kFew;
 }
 
 size_t q4_matmul_workspace(int32_t dtype, int64_t M, int64_t K, int64_t N) {
     const int parts = parts_of(dtype);
     size_t most = 0;  // of any group
     for (int group : {32, 128}) {
-        const Plan p = plan_of(parts, group, M, K, N);
+        const Plan p = plan_of(dtype, group, M, K, N);
         if (K > 0 && p.way != kFew)
             most = std::max(most, pack_bytes(parts, M, K) + (p.splits > 1 ? (size_t)p.splits * (size_t)M * (size_t)N * 4 : 0));
     }

@@ -863,8 +863,9 @@ IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_
  * products are summed in fp32 (fp32 inputs taken apart into three bf16 numbers
  * that add up to them, to within bf16's least value, 2^-133), scaled in fp32 and
  * added in fp32, rounded once, in a fixed order.  Scales are NaN or below 2^124
- * in magnitude (so that s (q - z) is finite); with fp16, those past 2^46, whose
- * terms are 0 or past fp16's range, may count as 2^46.  bias: device fp32 [N]
+ * in magnitude (so that s (q - z) is finite); with fp16, those of 2^46 and more,
+ * whose terms are 0 or past fp16's range, may count as smaller ones, of 2^45 or
+ * more.  bias: device fp32 [N]
  * or NULL; act: IA_ACT_NONE or IA_ACT_RELU.  K = 0 gives act(bias).  y must not
  * overlap an input, nor ws (ia_q4_linear_workspace_size bytes, 256-byte aligned,
  * may be NULL when that is 0) anything.  M, N, K < 2^31.

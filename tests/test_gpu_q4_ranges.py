@@ -73,3 +73,35 @@ def test_scales_past_2_64(M, N):
     assert torch.isfinite(y).all()
     _assert_linear(y[-60:], _f64(x)[-60:], _values(w))
     assert (q4_linear(torch.zeros_like(x), w) == 0).all()
+
+
+@pytest.mark.parametrize("tiny", [2.0 ** -100, -2.0 ** -81, 2.0 ** -79, 2.0 ** -66, -2.0 ** -60, 0.0])
+@pytest.mark.parametrize("M,N", SIZES)
+def test_large_sums_that_cancel(M, N, tiny):
+    """A group of scale 2^42, one of next to nothing and one of -2^42 over the same codes and inputs: whole numbers, whose
+    sums (64 * 15 * 3 * 2^42 at most) are exact and cancel, so that the other groups' sum remains as if alone."""
+    rng = np.random.default_rng(M + N)
+    scales = rng.uniform(0.001, 0.01, (N, GROUPS))
+    scales[:, 0], scales[:, 1], scales[:, 2] = 2.0 ** 42, tiny, -2.0 ** 42
+    codes = rng.integers(0, 256, (N, GROUPS * 32)).astype(np.uint8)
+    codes[:, 64:96] = codes[:, :32]
+    w = Q4Tensor.from_parts(torch.as_tensor(codes, device="cuda"), cuda(scales.astype(np.float32)), 3, GROUPS * 64, 64)
+    x = _matrix(rng, M, GROUPS * 64, torch.float16)
+    x[:, :192] = torch.as_tensor(rng.integers(-3, 4, (M, 192)), device="cuda")
+    x[:, 128:192] = x[:, :64]
+    assert M < 1000 or _takes_tiles(M, GROUPS * 64, N, torch.float16)
+    y = q4_linear(x, w)
+    # what the tiny scale adds is below 2^-60 * 64 * 12 * 3
+    _assert_linear(y[-60:], _f64(x[-60:, 192:]), _values(w)[:, 192:])
+
+
+@pytest.mark.parametrize("power", [-30, -25, -24, -23, -18, -14, -10, 0, 7, 8, 9, 12])
+@pytest.mark.parametrize("M,N", SIZES)
+def test_fp16_scales_of_every_power(M, N, power):
+    """Scales about 2^power, over inputs of a size that keeps the results in fp16's middle."""
+    rng = np.random.default_rng(M + N)
+    w = _weights(rng, N, rng.uniform(1, 2, (N, GROUPS)) * 2.0 ** power * np.sign(rng.normal(size=(N, GROUPS))))
+    x = (torch.as_tensor(rng.uniform(-1, 1, (M, GROUPS * 64)), device="cuda") * 2.0 ** min(max(-power, -12), 15)).half()
+    y = q4_linear(x, w)
+    assert torch.isfinite(y).all() and (y != 0).any()
+    _assert_linear(y[-60:], _f64(x)[-60:], _values(w))
