@@ -10,9 +10,10 @@
 // being the next group's, and at the end by the last m.
 //   bf16: u = the power of two of s, so 1 <= |m| < 2 and nothing grows.
 //   fp16: the same from 2^-24 to 2^8, where u (q - z) is a number of fp16; u ends
-//   there, and m goes on below 1 and above 2.  A group with |s| under 2^-66 counts as
-//   zero: with the 2^20 inputs of less than 2^16 that tiles take it adds less than
-//   2^-26, under half of fp16's least value.  Powers of two in s past 2^45 count as
+//   there, and m goes on below 1 and above 2.  Powers of two in s below 2^-66 count
+//   as 2^-66: with the 2^20 inputs of less than 2^16 that tiles take, such groups add
+//   less than 2^-25, half of fp16's least value.  (They are not left out: an infinite
+//   input gives an infinity against any weight but zero.)  Those past 2^45 count as
 //   2^45: fp16 inputs are at least 2^-24, so what such a group adds is 0 or at least
 //   2^21, past fp16's range.  A sum, of 2^20 terms of at most 15 * 2^46 * 65504, is
 //   below 2^86 then and in units of m, 2^-42 or more, below 2^128: a change of unit
@@ -79,9 +80,9 @@ struct Group<_Float16> {
     float u512;
     halfx2 zu;
     __device__ __forceinline__ explicit Group(uint32_t word) {
-        const uint32_t e = word & 0x7f800000u;
-        // a scale that is not finite goes into the operand as it is; codes times 2^-118 are zero in fp16
-        const uint32_t u = e == 0x7f800000u ? word & ~255u : e < (127u - 66) << 23 ? 0u : half_unit(word);
+        // a scale that is not finite goes into the operand as it is, as zero does (codes times 2^-118 are zero in fp16)
+        const bool other = (word & 0x7f800000u) == 0x7f800000u || (word & 0x7fffff00u) == 0;
+        const uint32_t u = other ? word & 0x7fffff00u : half_unit(word);
         u512 = __builtin_bit_cast(float, u + (9u << 23));
         zu = twice(-zero_of(word) * __builtin_bit_cast(float, u));
     }

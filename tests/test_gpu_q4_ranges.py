@@ -105,3 +105,24 @@ def test_fp16_scales_of_every_power(M, N, power):
     y = q4_linear(x, w)
     assert torch.isfinite(y).all() and (y != 0).any()
     _assert_linear(y[-60:], _f64(x)[-60:], _values(w))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N", SIZES)
+def test_infinite_inputs_over_scales_of_any_size(M, N, dtype):
+    """An infinite input gives an infinity of the weight's sign however small the scale, NaN against a weight of zero (of a
+    zero scale as well)."""
+    rng = np.random.default_rng(M + N)
+    scales = rng.uniform(0.001, 0.01, (N, GROUPS))
+    scales[:, 1], scales[:, 3], scales[:, 4], scales[:, 6], scales[:, 7] = 2.0 ** -100, -2.0 ** -81, 2.0 ** -66, 0.0, 2.0 ** -40
+    w = _weights(rng, N, scales)
+    v = _values(w)
+    for g in range(GROUPS):
+        x = _matrix(rng, M, GROUPS * 64, dtype)
+        k = 64 * g + int(rng.integers(64))
+        x[M - 1, k] = float("inf") * (1 if g % 2 else -1)
+        y = _f64(q4_linear(x, w))
+        assert np.isfinite(y[:M - 1]).all()
+        zero = v[:, k] == 0
+        assert np.isnan(y[M - 1, zero]).all() and zero.all() == (g == 6)
+        assert np.array_equal(y[M - 1, ~zero], (1 if g % 2 else -1) * np.sign(v[~zero, k]) * np.inf)
