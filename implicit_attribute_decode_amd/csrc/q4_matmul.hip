@@ -8,7 +8,8 @@
 // at most 4 significant bits and m goes to the sums.  A sum is kept in units of
 // its weight row's current m: where a group ends it is multiplied by m / m', m'
 // being the next group's, and at the end by the last m.
-//   bf16: u = the power of two of s, so 1 <= |m| < 2 and nothing grows.
+//   bf16: u = the power of two of s, so 1 <= |m| < 2 and nothing grows; 2^123 at most
+//   (15 u is in range) and 2^-126 at least, past which m goes on.
 //   fp16: the same from 2^-24 to 2^8, where u (q - z) is a number of fp16; u ends
 //   there, and m goes on below 1 and above 2.  Powers of two in s below 2^-66 count
 //   as 2^-66: with the 2^20 inputs of less than 2^16 that tiles take, such groups add
@@ -57,6 +58,8 @@ __device__ __forceinline__ uint32_t power_of(uint32_t word, int least, int most)
 // A group's u in fp16, as bits.
 __device__ __forceinline__ uint32_t half_unit(uint32_t word) { return power_of(word, -24, 8); }
 
+constexpr int kMostPower = 123;  // of u in bf16: times 15 it is in range
+
 // A group's m.
 template <typename V>
 __device__ __forceinline__ float unit_of(uint32_t word);
@@ -66,10 +69,8 @@ __device__ __forceinline__ float unit_of<_Float16>(uint32_t word) {
 }
 template <>
 __device__ __forceinline__ float unit_of<__bf16>(uint32_t word) {
-    const uint32_t e = word & 0x7f800000u;
-    const bool other = e == 0x7f800000u || (word & 0x7fffff00u) == 0;  // not finite, or zero
-    const float m = __builtin_bit_cast(float, (word & 0x807fff00u) | 0x3f800000u), small = scale_of(word) * 0x1p126f;
-    return other ? 1.0f : e ? m : small;
+    const float s = scale_of(word);
+    return s == 0.0f ? 1.0f : s * __builtin_bit_cast(float, (254u << 23) - power_of(word, -126, kMostPower));  // 1 / u
 }
 
 // What a group's word does to its codes; operands are u (q - z).
@@ -94,7 +95,7 @@ struct Group<__bf16> {
     __device__ __forceinline__ explicit Group(uint32_t word) {
         const uint32_t e = word & 0x7f800000u, low = (word & 0x7fff00u) ? 0x00800000u : 0u;
         // a scale that is not finite goes into the operand as it is
-        u = __builtin_bit_cast(float, e == 0x7f800000u ? word & ~255u : e ? e : low);
+        u = __builtin_bit_cast(float, e == 0x7f800000u ? word & ~255u : e ? power_of(word, -126, kMostPower) : low);
         zu = -zero_of(word) * u;
     }
     __device__ __forceinline__ bfloatx8 operand(uint32_t codes) const { return codes_times(codes, u, zu); }

@@ -853,7 +853,8 @@ typedef struct {
  * UNSUPPORTED (dtype, group), DEVICE. */
 IA_API ia_status ia_q4_quantize(const void* x, int32_t dtype, int64_t ldx, const ia_q4* out, void* stream);
 
-/* x[rows][cols] (rows ldx >= cols apart) = s (q - z), rounded once to dtype.
+/* x[rows][cols] (rows ldx >= cols apart) = s (q - z), rounded once to dtype (an
+ * infinity past its range, which a code next to its type's largest value can reach).
  * Errors: as ia_q4_quantize. */
 IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_t ldx, void* stream);
 
@@ -862,11 +863,11 @@ IA_API ia_status ia_q4_dequantize(const ia_q4* q, int32_t dtype, void* x, int64_
  * [M][N] of dtype (rows ldy apart).  Any M from one row (serving) up.  A group's
  * products are summed in fp32 (fp32 inputs taken apart into three bf16 numbers
  * that add up to them, to within bf16's least value, 2^-133), scaled in fp32 and
- * added in fp32, rounded once, in a fixed order.  Scales are NaN or below 2^124
- * in magnitude (so that s (q - z) is finite); with fp16, those of 2^46 and more,
- * whose terms are 0 or past fp16's range, may count as smaller ones, of 2^45 or
- * more.  bias: device fp32 [N]
- * or NULL; act: IA_ACT_NONE or IA_ACT_RELU.  K = 0 gives act(bias).  y must not
+ * added in fp32, rounded once, in a fixed order.  Scales are NaN or finite; with
+ * fp16, those of 2^46 and more, whose terms are 0 or past fp16's range, may count
+ * as smaller ones, of 2^45 or more.  (A sum past 2^113 may become infinite where
+ * it meets a scale that is subnormal, below 2^-126; ia_q4_quantize makes none.)
+ * bias: device fp32 [N] or NULL; act: IA_ACT_NONE or IA_ACT_RELU.  K = 0 gives act(bias).  y must not
  * overlap an input, nor ws (ia_q4_linear_workspace_size bytes, 256-byte aligned,
  * may be NULL when that is 0) anything.  M, N, K < 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, act, group), WORKSPACE_TOO_SMALL,

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from implicit_attribute_decode_amd import ia
-from implicit_attribute_decode_amd.pipeline import _DTYPES, Q4Tensor, q4_linear
+from implicit_attribute_decode_amd.pipeline import _DTYPES, Q4Tensor, q4_linear, q4_quantize
 
 from gpu_util import cuda, host
 from test_gpu_q4 import TYPES, _assert_linear, _f64, _matrix, _values, ids
@@ -126,3 +126,28 @@ def test_infinite_inputs_over_scales_of_any_size(M, N, dtype):
         zero = v[:, k] == 0
         assert np.isnan(y[M - 1, zero]).all() and zero.all() == (g == 6)
         assert np.array_equal(y[M - 1, ~zero], (1 if g % 2 else -1) * np.sign(v[~zero, k]) * np.inf)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,N", SIZES)
+def test_weights_of_the_whole_range(M, N, dtype):
+    """Weights of either sign up to the largest float: their scales pass 2^125, their values (from the rounding of the zero)
+    fp32's range, and a code less its zero, -8, times 2^125 does so too.  Small inputs and zeros give the products of those values all the same."""
+    rng = np.random.default_rng(M + N)
+    wf = rng.normal(size=(N, GROUPS * 64))
+    big = float(np.finfo(np.float32).max)
+    wf[:, 5], wf[:, 9], wf[:, 200], wf[:, 250], wf[:, 400], wf[:, 440] = -3.3e38, 3.13e38, -big, 0.3 * big, big, -big
+    w = q4_quantize(torch.as_tensor(wf, device="cuda").float(), 64)
+    v = _values(w)
+    assert np.abs(v).max() > big and float(w.scales[:, 0].min()) > 2.0 ** 125 and int(w.zeros[0, 0]) == 8
+    x = _matrix(rng, M, GROUPS * 64, dtype)
+    x[:, :64] = x[:, 192:256] = x[:, 384:448] = 0
+    y = q4_linear(x, w)
+    assert torch.isfinite(y).all()
+    _assert_linear(y[-60:], _f64(x)[-60:], v)
+    if dtype != torch.float16:
+        x = x * 2.0 ** -20
+        x[:, :64] = x[:, 192:256] = x[:, 384:448] = 2.0 ** -30
+        y = q4_linear(x, w)
+        assert torch.isfinite(y).all()
+        _assert_linear(y[-60:], _f64(x)[-60:], v)
