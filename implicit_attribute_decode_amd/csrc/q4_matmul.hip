@@ -435,7 +435,7 @@ hipError_t run(const ManyArgs& a, int splits, hipStream_t s) {
     p.tiles_n = ceil_div(p.w.N, BN);
     const int64_t tiles = p.tiles_m * p.tiles_n, most = 1 << 20;  // a grid has less than 2^32 threads
     for (p.tile0 = 0; p.tile0 < tiles; p.tile0 += most)
-        IA_LAUNCH("q4_matmul_kernel", (q4_matmul_kernel<V, T, G, BM, BN, WM, WN>),
+        IA_LAUNCH(BM == 256 ? "q4_matmul_kernel<256>" : "q4_matmul_kernel<128>", (q4_matmul_kernel<V, T, G, BM, BN, WM, WN>),
                   dim3((unsigned)std::min(most, tiles - p.tile0), splits), dim3(64 * WM * WN), 0, s, p);
     return hipGetLastError();
 }
