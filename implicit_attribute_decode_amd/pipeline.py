@@ -752,7 +752,7 @@ class Mx4Tensor:
     [rows, ceil(cols / 32)] (2^(byte - 127), 255 = NaN).  The tensors are not
     replaced, nor are the sizes; their values may change (quantised anew)."""
 
-    __slots__ = ("_codes", "_scales", "c")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "c")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
         blocks = (cols + 31) // 32
@@ -763,13 +763,13 @@ class Mx4Tensor:
         if (codes.shape != (rows, 16 * blocks) or scales.shape != (rows, blocks)
                 or not codes.is_contiguous() or not scales.is_contiguous()):
             raise ValueError(f"codes [{rows}, {16 * blocks}] and scales [{rows}, {blocks}] expected, contiguous")
-        self._codes, self._scales, self.c = codes, scales, ia.mx4(codes, scales, rows, cols)
+        self._codes, self._scales, self._rows, self._cols = codes, scales, rows, cols
+        self.c = ia.mx4(codes, scales, rows, cols)
 
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
-    # what the kernels read
-    rows = property(lambda self: self.c.rows)
-    cols = property(lambda self: self.c.cols)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
@@ -827,17 +827,18 @@ def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: torch.Tensor | None = None, 
     """A linear layer with MXFP4 weights: act(Q(x) w^T + bias), x [M, K]
     quantised along its rows, w [N, K]; returns [M, N] of x's type."""
     d, M, K, ldx = _matrix(x, "x")
+    N = w.rows
     if K != w.cols:
         raise ValueError(f"x has {K} columns, the weights {w.cols}")
     if out is None:
-        out, ldy = torch.empty((M, w.rows), dtype=x.dtype, device=x.device), w.rows
+        out, ldy = torch.empty((M, N), dtype=x.dtype, device=x.device), N
     else:
         do, rows, cols, ldy = _matrix(out, "out")
-        if (do, rows, cols) != (d, M, w.rows):
+        if (do, rows, cols) != (d, M, N):
             raise ValueError("out has another shape or type")
     _one_device(x, w._codes, bias, out)
-    ws = _bytes(ia.ia_mx4_linear_workspace_size(M, K, w.rows), x.device)
-    ia.ia_mx4_linear(x, d, M, ldx, w.c, _bias(bias, w.rows), _ACTS[act], out, ldy, ws)
+    ws = _bytes(ia.ia_mx4_linear_workspace_size(M, K, N), x.device)
+    ia.ia_mx4_linear(x, d, M, ldx, w.c, _bias(bias, N), _ACTS[act], out, ldy, ws)
     return out
 
 
@@ -976,7 +977,7 @@ def embedding(table, index: torch.Tensor, scale: float = 1.0, dtype=None, dropou
     of zeros."""
     b, n, between = _index(index)
     if packed := isinstance(table, Mx4Tensor):
-        entries, dim, memory, own = table.rows, table.cols, table._codes, torch.float32
+        entries, dim, memory, own = table._rows, table._cols, table._codes, torch.float32
     else:
         d, entries, dim, ld = _matrix(table, "table")
         memory, own = table, table.dtype
@@ -1024,7 +1025,7 @@ class Q4Tensor:
     float32 whose lowest byte is zero, and in that byte the zero, 0..15).  The
     tensors and sizes are not replaced; the tensors' values may change (quantised anew)."""
 
-    __slots__ = ("_codes", "_words", "c")
+    __slots__ = ("_codes", "_words", "_rows", "_cols", "_group", "c")
 
     def __init__(self, codes: torch.Tensor, words: torch.Tensor, cols: int, group: int):
         shapes = self._shapes(codes.shape[0], cols, group)
@@ -1043,14 +1044,14 @@ class Q4Tensor:
         return (rows, groups * group // 2), (rows, (groups + 3) // 4 * 4)
 
     def _set(self, codes, words, cols, group):
-        self._codes, self._words, self.c = codes, words, ia.q4(codes, words, codes.shape[0], cols, group)
+        self._codes, self._words, self._rows, self._cols, self._group = codes, words, codes.shape[0], cols, group
+        self.c = ia.q4(codes, words, self._rows, cols, group)
 
     codes = property(lambda self: self._codes)
     words = property(lambda self: self._words)
-    # what the kernels read
-    rows = property(lambda self: self.c.rows)
-    cols = property(lambda self: self.c.cols)
-    group = property(lambda self: self.c.group)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    group = property(lambda self: self._group)
 
     @classmethod
     def empty(cls, rows: int, cols: int, group: int = 128, device="cuda"):
@@ -1095,7 +1096,7 @@ class Q4Tensor:
     def dequantize(self, dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
         """The values, rounded once to dtype (float32, float16 or bfloat16)."""
         if out is None:
-            out, ld = self._codes.new_empty((self.rows, self.cols), dtype=dtype), self.cols
+            out, ld = self._codes.new_empty((self._rows, self._cols), dtype=dtype), self._cols
             d = _dtype(out)
         else:
             d, rows, cols, ld = _matrix(out, "out")
@@ -1125,9 +1126,9 @@ def q4_linear(x: torch.Tensor, w: Q4Tensor, bias: torch.Tensor | None = None, ac
     """A linear layer with 4-bit weights and its input as it is: act(x w^T +
     bias), x [M, K], w [N, K]; returns [M, N] of x's type; act "none" or "relu"."""
     d, M, K, ldx = _matrix(x, "x")
-    N = w.rows
-    if K != w.cols:
-        raise ValueError(f"x has {K} columns, the weights {w.cols}")
+    N = w._rows
+    if K != w._cols:
+        raise ValueError(f"x has {K} columns, the weights {w._cols}")
     if out is None:
         out, ldy = x.new_empty((M, N)), N
     else:
