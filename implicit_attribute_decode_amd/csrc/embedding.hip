@@ -464,6 +464,7 @@ struct SumArgs {
     int tile;         // sorted rows that a group starts from
     int64_t slices;   // groups side by side over the columns
     int64_t tiles;
+    int64_t block0;   // first of the launch
     float factor;
     float* grad;      // [entries][dim], zeros
     float* part;      // [tiles][2][dim]: sums of a long entry's rows in a tile, at its end (0) and at its start (1)
@@ -545,12 +546,12 @@ template <typename T, bool DROP, int QUADS, Rows ROWS>
 __global__ void __launch_bounds__(256) embedding_sums_kernel(const T* dy, int64_t lddy, SumArgs p, DropArgs a) {
     extern __shared__ uint64_t s_words[];  // from a tile and a word before the first tile to two tiles past the last one's start
     const int groups = 256 / p.lanes, group = threadIdx.x / p.lanes, lane = threadIdx.x % p.lanes;
-    const int64_t unit = (int64_t)blockIdx.x * groups + group;
-    const int64_t tile0 = (int64_t)blockIdx.x * groups / p.slices;
+    const int64_t block = p.block0 + blockIdx.x, unit = block * groups + group;
+    const int64_t tile0 = block * groups / p.slices;
     const int before = p.tile + 1;
     {
         const int64_t from = tile0 * p.tile - before;
-        const int count = (int)(((int64_t)(blockIdx.x + 1) * groups - 1) / p.slices - tile0 + 2) * p.tile + before + 1;
+        const int count = (int)(((block + 1) * groups - 1) / p.slices - tile0 + 2) * p.tile + before + 1;
         for (int i = threadIdx.x; i < count; i += 256) s_words[i] = p.words[min(max(from + i, (int64_t)0), p.n - 1)];
         __syncthreads();
     }
@@ -720,17 +721,21 @@ GradLayout grad_layout(int64_t n, int64_t dim) {
 __global__ void __launch_bounds__(kThreads) embedding_zero_kernel(Zeros z) { zero_share(z); }
 
 template <typename T, int QUADS, Rows ROWS>
-hipError_t launch_sums(const T* dy, int64_t lddy, const SumArgs& p, const DropArgs* d, hipStream_t s) {
+hipError_t launch_sums(const T* dy, int64_t lddy, const SumArgs& a, const DropArgs* d, hipStream_t s) {
+    SumArgs p = a;
     const int groups = 256 / p.lanes;
-    const dim3 grid((unsigned)ceil_div(p.tiles * p.slices, groups));
     // the tiles of a block, the one before and two behind
     const size_t lds = 8 * ((size_t)(ceil_div(groups - 1, p.slices) + 3) * p.tile + p.tile + 2);
-    if (d)
-        IA_LAUNCH("embedding_sums_kernel", (embedding_sums_kernel<T, true, QUADS, ROWS>), grid, dim3(256), lds, s, dy, lddy, p,
-                  *d);
-    else
-        IA_LAUNCH("embedding_sums_kernel", (embedding_sums_kernel<T, false, QUADS, ROWS>), grid, dim3(256), lds, s, dy, lddy,
-                  p, DropArgs{});
+    const int64_t blocks = ceil_div(p.tiles * p.slices, groups), most = 1 << 23;  // a grid has less than 2^32 threads
+    for (p.block0 = 0; p.block0 < blocks; p.block0 += most) {
+        const dim3 grid((unsigned)std::min(most, blocks - p.block0));
+        if (d)
+            IA_LAUNCH("embedding_sums_kernel", (embedding_sums_kernel<T, true, QUADS, ROWS>), grid, dim3(256), lds, s, dy, lddy,
+                      p, *d);
+        else
+            IA_LAUNCH("embedding_sums_kernel", (embedding_sums_kernel<T, false, QUADS, ROWS>), grid, dim3(256), lds, s, dy,
+                      lddy, p, DropArgs{});
+    }
     return hipGetLastError();
 }
 template <typename T>

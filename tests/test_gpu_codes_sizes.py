@@ -165,6 +165,15 @@ def test_the_most_rows():
     assert abs(share - 0.5) < 6 * 0.5 / n ** 0.5
 
 
+def test_gradient_of_the_most_rows():
+    """2^31 - 1 rows of 129 values (one row repeated) of one entry: 2^24 blocks of tiles, 2^32 threads (105 GB of workspace)."""
+    n = 2 ** 31 - 1
+    dy = (torch.arange(129, device="cuda") % 3 - 1).to(torch.bfloat16).view(1, 129).expand(n, 129)
+    g = embedding_backward(dy, torch.tensor([1], dtype=torch.int32, device="cuda").expand(n), 3)
+    # sums of whole numbers: exact in a tile and in the join in double, then 2^31 - 1 rounds to 2^31
+    assert torch.equal(g[1], dy[0].float() * 2.0 ** 31) and not bool(g[0].any()) and not bool(g[2].any())
+
+
 def test_4_bit_conversions_in_several_launches():
     """2^29 + 100 rows of one value in groups of 32: a launch takes 2^29 - 64 of them."""
     n = 2 ** 29 + 100
