@@ -428,9 +428,15 @@ hipError_t few(const T* x, int64_t M, int64_t ldx, const Q4Linear& p, hipStream_
 }
 template <typename T, int G>
 hipError_t linear(const T* x, int64_t M, int64_t ldx, const Q4Linear& p, hipStream_t s) {
-    // Two tiles of outputs a wave halve the reading of x, where blocks of four waves fill
-    // the chip all the same (5 x 8,192 -> 16,384: 31 -> 26 us; -> 8,192: 12 either way)
-    if (M <= 16) return p.N >= 16384 ? few<T, 1, 2, G, 4>(x, M, ldx, p, s) : few<T, 1, 1, G, 8>(x, M, ldx, p, s);
+    // Two tiles of outputs a wave halve the reading of x, and blocks of four waves leave fewer
+    // rounds of them on the chip; up to 8,192 outputs there are few blocks then (times of calls
+    // with one and with two, us):
+    //   outputs                         8,192        10,240       12,288       16,384
+    //   1 fp16 row of 4,096          9.9  10.2    14.0  13.3    14.3  13.7    17.1  14.1
+    //   5 bf16 rows of 8,192        17.2  16.8    23.4  24.0    24.3  24.1    30.1  24.8
+    //   16 bf16 rows of 4,096       14.6  12.2    20.6  18.0    21.1  18.1    25.5  18.6
+    //   8 fp32 rows of 4,096        22.2  16.7    32.0  25.1    32.5  24.9    42.2  25.8
+    if (M <= 16) return p.N > 8192 ? few<T, 1, 2, G, 4>(x, M, ldx, p, s) : few<T, 1, 1, G, 8>(x, M, ldx, p, s);
     if (M <= 32) return few<T, 2, 1, G, 8>(x, M, ldx, p, s);
     return few<T, 4, 1, G, 8>(x, M, ldx, p, s);
 }

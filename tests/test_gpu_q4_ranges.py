@@ -151,3 +151,14 @@ def test_weights_of_the_whole_range(M, N, dtype):
         y = q4_linear(x, w)
         assert torch.isfinite(y).all()
         _assert_linear(y[-60:], _f64(x)[-60:], v)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,K,N", [(1, 1030, 8192), (1, 1030, 8193), (16, 300, 8200), (3, 4096, 12289)])
+def test_few_rows_of_wide_layers(M, K, N, group, dtype):
+    """Either side of the number of outputs from which a wave takes two tiles of them."""
+    rng = np.random.default_rng(M + K + N)
+    x, w = _matrix(rng, M, K, dtype), q4_quantize(_matrix(rng, N, K, scale=K ** -0.5), group)
+    bias = cuda(rng.normal(size=N).astype(np.float32))
+    _assert_linear(q4_linear(x, w, bias, "relu"), _f64(x), _values(w), _f64(bias), relu=True)
