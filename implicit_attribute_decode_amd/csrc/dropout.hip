@@ -13,7 +13,7 @@ namespace {
 
 // A thread takes eight values of a row: two counters give their eight words.
 // Rows from row0 on, fewer than 2^31 threads.  300,000 x 256 fp16 values (307 MB) take
-// 53 us (5.8 TB/s, a copy 6.2); the generator's multiplications alone, at a quarter
+// 54 us (5.7 TB/s, a copy 6.2); the generator's multiplications alone, at a quarter
 // of the rate of other instructions, keep the SIMDs busy for about as long.
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, int64_t ldx, T* out, int64_t ldo, uint32_t row0,

@@ -294,7 +294,7 @@ __device__ __forceinline__ void multiply(const uintx4 (&codes)[NT], const uint32
 // words, and the codes are consecutive.  The codes less their zero are exact matrix
 // operands; a group's sum is scaled in fp32; the waves' sums are added in order.
 // One fp16 row through 4,096 -> 4,096 (8.9 MB): 7.3 us, most of it the launch and one
-// round of loads.  Five bf16 rows through 8,192 -> 16,384 (71 MB): 26 us (2.8 TB/s).
+// round of loads.  Five bf16 rows through 8,192 -> 16,384 (71 MB): 26 us (2.7 TB/s).
 // There the loads' own handling binds: without x's 24, without x and words 23, and
 // without the conversions too 19 (measured with one tile of outputs a wave, 33 in all).
 template <typename T, int MT, int NT, int G, int WAVES>

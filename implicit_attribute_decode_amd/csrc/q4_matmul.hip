@@ -148,11 +148,11 @@ __device__ __forceinline__ void store_tile(const float* sums, int pitch, const M
 }
 
 // A block computes BM rows by BN outputs, a wave 32 TI by 32 TJ of them.  A
-// stage is 64 inputs in one of two LDS buffers: the rows of x are copied there
-// by the LDS-DMA loads, the codes pass through registers, where each thread
+// stage is 64 inputs: the rows of x are copied into one of three LDS buffers by the
+// LDS-DMA loads, the codes reach one of two through registers, where each thread
 // turns 32 of them into operands between the current stage's products.  4,096 cubed
-// in bf16 and groups of 128: 157 us of normally distributed rows, 144 of those of the
-// cases (875 and 960 TFLOP/s; the library's product of bf16 matrices reaches 1,210).
+// in bf16 and groups of 128: 157 us of normally distributed rows, 144 of rows of
+// different sizes (875 and 960 TFLOP/s; the library's product of bf16 matrices reaches 1,210).
 // The matrix cores are busy 38 % of the time and the vector units, with conversions
 // and the sums' changes of unit, 39 %: what does not overlap is the distance.  About
 // 20 us are a tile's start and its stores, with one tile a CU.  Waves that raise their
@@ -381,6 +381,8 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
     }
 }
 
+int parts_of(int32_t dtype) { return dtype == IA_DTYPE_F32 ? 3 : 1; }
+
 // Microseconds that a product takes, as measured on bf16 in groups of 128 over M of
 // 33 to 100,000, K of 32 to 8,192 and N of 58 to 11,008 (in brackets a case):
 //   few rows' kernel: 16 outputs of 64 rows a block, 256 blocks side by side take
@@ -391,8 +393,9 @@ __global__ void __launch_bounds__(256) q4_join_kernel(const float* sums, int spl
 //     cubed: 163, in tiles of 128 226)
 //   joining splits: 3 and 8 bytes a sum at 4 TB/s (128 x 4,096 -> 4,096 in four
 //     splits: 28, in one 59).
-int parts_of(int32_t dtype) { return dtype == IA_DTYPE_F32 ? 3 : 1; }
-
+// It stands for the other types and groups as well, whose tiles take longer: 4,096 cubed
+// in groups of 32 takes 244 where this says 200.  Packing x, for fp32 rows and for
+// rows that are no whole lines, is not counted.
 enum Way { kFew, kSmall, kLarge };
 struct Plan {
     Way way;
