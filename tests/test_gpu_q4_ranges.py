@@ -162,3 +162,20 @@ def test_few_rows_of_wide_layers(M, K, N, group, dtype):
     x, w = _matrix(rng, M, K, dtype), q4_quantize(_matrix(rng, N, K, scale=K ** -0.5), group)
     bias = cuda(rng.normal(size=N).astype(np.float32))
     _assert_linear(q4_linear(x, w, bias, "relu"), _f64(x), _values(w), _f64(bias), relu=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("M,K,N", [(20, 2 ** 20 - 5, 60), (20, 2 ** 20 + 3, 60), (3, 2 ** 20 + 3, 60), (20, 2 ** 22 + 70, 5)])
+def test_a_million_inputs(M, K, N, dtype):
+    """Around the inputs up to which tiles are taken: whole numbers, whose sums (2^22 * 15 at most) fp32 holds up to 2^24,
+    which sums of inputs -1, 0 and 1 at random do not reach (the oracle says so), so that they are exact."""
+    rng = np.random.default_rng(K + M)
+    groups = -(-K // 128)
+    codes = rng.integers(0, 256, (N, groups * 64)).astype(np.uint8)
+    w = Q4Tensor.from_parts(torch.as_tensor(codes, device="cuda"), torch.ones((N, groups), device="cuda"), 7, K, 128)
+    x = rng.integers(-1, 2, (M, K)).astype(np.float32)
+    v = _values(w).astype(np.float32)
+    want = x.astype(np.float64) @ v.astype(np.float64).T
+    assert np.abs(want).max() < 60000
+    got = q4_linear(cuda(x).to(dtype), w)
+    assert torch.equal(got.cpu(), torch.as_tensor(want).to(dtype))
